@@ -14,6 +14,13 @@ output comes from the chunk-start weights.  Variants: ``momentum=False``
 (W_t = alpha_t W_{t-1} - eta_t g_t) and ``chunk_avg=True`` (the per-token
 kernels replaced by their chunk means).  ``chunk_backward`` is the
 vector-Jacobian product of ``chunk_forward`` (SwiGLU MFMA path).
+
+The other operators of a hybrid layer (``layer.py``, include/e2ttt_layer.h):
+causal grouped-head attention over packed sequences with an optional window
+(``attention_forward``, ``attention_backward``, ``attention``), attention of
+new tokens over a paged cache (``paged_attention``) and the root-mean-square
+norm with the residual's addition (``norm_forward``, ``norm_backward``,
+``rms_norm``).
 """
 from __future__ import annotations
 
@@ -25,7 +32,11 @@ from . import _lib
 from ._lib import (E2TTTError, FLAG_CHUNK_AVG, FLAG_FORCE_GENERIC, FLAG_NO_MOMENTUM, FLAG_PRECISE, FLAG_SAVE_STATES,
                    make_desc)
 
-__all__ = ["chunk_forward", "chunk_forward_noalloc", "chunk_backward", "chunk_update", "training_workspace", "logscan", "workspace_size", "param_count", "path", "validate", "E2TTTError",
+from .layer import (attention, attention_backward, attention_forward, norm_backward, norm_forward, paged_attention,
+                    rms_norm)
+
+__all__ = ["attention", "attention_forward", "attention_backward", "paged_attention", "rms_norm", "norm_forward",
+           "norm_backward", "chunk_forward", "chunk_forward_noalloc", "chunk_backward", "chunk_update", "training_workspace", "logscan", "workspace_size", "param_count", "path", "validate", "E2TTTError",
            "library"]
 
 

@@ -26,12 +26,37 @@ EXPORTS = ("e2ttt_param_count", "e2ttt_workspace_size", "e2ttt_path", "e2ttt_val
            "e2ttt_backward_workspace_size", "e2ttt_validate_backward", "e2ttt_chunk_backward",
            "e2ttt_chunk_backward_events", "e2ttt_chunk_forward_noalloc")
 
+# include/e2ttt_layer.h
+LAYER_EXPORTS = ("e2ttt_attention_workspace_size", "e2ttt_attention_forward", "e2ttt_attention_backward_workspace_size",
+                 "e2ttt_attention_backward", "e2ttt_paged_workspace_size", "e2ttt_paged_attention",
+                 "e2ttt_norm_forward", "e2ttt_norm_backward_workspace_size", "e2ttt_norm_backward")
+
 
 class Desc(ctypes.Structure):
     _fields_ = [("kind", ctypes.c_int32), ("loss", ctypes.c_int32), ("io_dtype", ctypes.c_int32),
                 ("flags", ctypes.c_int32), ("B", ctypes.c_int64), ("H", ctypes.c_int64),
                 ("T", ctypes.c_int64), ("D", ctypes.c_int64), ("Hd", ctypes.c_int64),
                 ("chunk", ctypes.c_int64)]
+
+
+class AttentionDesc(ctypes.Structure):
+    _fields_ = [("io_dtype", ctypes.c_int32), ("window", ctypes.c_int32), ("tokens", ctypes.c_int64),
+                ("seqs", ctypes.c_int64), ("heads", ctypes.c_int64), ("kv_heads", ctypes.c_int64),
+                ("D", ctypes.c_int64), ("scale", ctypes.c_float), ("reserved", ctypes.c_int32),
+                ("q_tok", ctypes.c_int64), ("q_head", ctypes.c_int64), ("k_tok", ctypes.c_int64),
+                ("k_head", ctypes.c_int64), ("v_tok", ctypes.c_int64), ("v_head", ctypes.c_int64)]
+
+
+class PagedDesc(ctypes.Structure):
+    _fields_ = [("a", AttentionDesc), ("pages", ctypes.c_int64), ("page_size", ctypes.c_int64),
+                ("table_width", ctypes.c_int64), ("kc_page", ctypes.c_int64), ("kc_head", ctypes.c_int64),
+                ("kc_slot", ctypes.c_int64), ("vc_page", ctypes.c_int64), ("vc_head", ctypes.c_int64),
+                ("vc_slot", ctypes.c_int64)]
+
+
+class NormDesc(ctypes.Structure):
+    _fields_ = [("io_dtype", ctypes.c_int32), ("bits8", ctypes.c_int32), ("rows", ctypes.c_int64),
+                ("width", ctypes.c_int64), ("eps", ctypes.c_float), ("reserved", ctypes.c_int32)]
 
 
 class E2TTTError(RuntimeError):
@@ -77,6 +102,18 @@ def load() -> ctypes.CDLL:
     lib.e2ttt_chunk_backward.restype = ctypes.c_int
     lib.e2ttt_chunk_backward_events.argtypes = [pd] + [vp] * 19 + [vp, sz, vp, ctypes.POINTER(vp)]
     lib.e2ttt_chunk_backward_events.restype = ctypes.c_int
+    pa, pp, pn = ctypes.POINTER(AttentionDesc), ctypes.POINTER(PagedDesc), ctypes.POINTER(NormDesc)
+    for fn, args, res in (("e2ttt_attention_workspace_size", [pa], sz),
+                          ("e2ttt_attention_forward", [pa] + [vp] * 6 + [vp, sz, vp], ctypes.c_int),
+                          ("e2ttt_attention_backward_workspace_size", [pa], sz),
+                          ("e2ttt_attention_backward", [pa] + [vp] * 10 + [vp, sz, vp], ctypes.c_int),
+                          ("e2ttt_paged_workspace_size", [pp], sz),
+                          ("e2ttt_paged_attention", [pp] + [vp] * 9 + [vp, sz, vp], ctypes.c_int),
+                          ("e2ttt_norm_forward", [pn] + [vp] * 7 + [vp], ctypes.c_int),
+                          ("e2ttt_norm_backward_workspace_size", [pn], sz),
+                          ("e2ttt_norm_backward", [pn] + [vp] * 7 + [vp, sz, vp], ctypes.c_int)):
+        getattr(lib, fn).argtypes = args
+        getattr(lib, fn).restype = res
     lib.e2ttt_status_string.argtypes = [ctypes.c_int]
     lib.e2ttt_status_string.restype = ctypes.c_char_p
     _lib = lib

@@ -1,0 +1,343 @@
+// Gradients of the causal grouped-head attention, bf16 MFMA:
+//
+//   p_ij = exp(s_ij - lse_i),        delta_i = <dout_i, out_i>,
+//   ds_ij = p_ij (<dout_i, v_j> - delta_i),
+//   dv_j = sum_i p_ij dout_i,  dk_j = scale sum_i ds_ij q_i,
+//   dq_i = scale sum_j ds_ij k_j.
+//
+// Two kernels, each with its sums in registers: attn_dq_kernel owns query rows
+// and walks over keys (and computes delta for the other), attn_dkdv_kernel
+// owns keys and walks over the rows of their whole group.  That is seven
+// products instead of the five of a single kernel, but no sum passes through
+// memory and none depends on the order of workgroups: a single kernel would
+// add dq to HBM in fp32 from every key block.
+//
+// Scores are recomputed in the orientation in which p and ds leave the MFMA as
+// the next product's operand (attn_common.h): S^T with a query per lane for
+// dq, S with a key per lane for dk and dv.
+#include "attn_common.h"
+
+namespace e2ttt {
+namespace attn {
+namespace {
+
+constexpr int BM = 128;  // rows (dq) or keys (dkdv) of a workgroup: 4 waves x 32
+constexpr int BN = 64;   // keys or rows of a staged tile
+
+__device__ __align__(256) unsigned char zeros[256];  // read in place of rows outside a sequence
+
+template <int DP>
+struct CopyPlan {
+    static constexpr int RPI = 512 / DP;       // rows per copy instruction
+    static constexpr int NI = (BN / 4) / RPI;  // instructions per wave and tensor
+    static constexpr int CH = DP / 8;          // chunks per row
+};
+
+// Two accumulator columns' worth of output, d-major per lane: 4 consecutive
+// values of the head dimension per store.
+template <int DT>
+__device__ __forceinline__ void store_row(__bf16* o, const f32x16 (&acc)[DT], float f, int g, int D) {
+#pragma unroll
+    for (int dt = 0; dt < DT; ++dt)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int d = 32 * dt + 8 * j + 4 * g;
+            if (d < D) {
+                bf16x4 w;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) w[e] = (__bf16)(acc[dt][4 * j + e] * f);
+                *(bf16x4*)(o + d) = w;
+            }
+        }
+}
+
+template <int DP>
+__global__ __launch_bounds__(256, 2) void attn_dq_kernel(AttnBwdArgs a) {
+    constexpr int TILE = BN * DP * 2;
+    constexpr int KS = DP / 16, DT = DP / 32;
+    using P = CopyPlan<DP>;
+    __shared__ __attribute__((aligned(1024))) unsigned char lds[2][2][TILE];  // [stage][K, V]
+
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int g = lane >> 5, col = lane & 31, G = a.G;
+    const int kvh = blockIdx.x % a.K, t = blockIdx.x / a.K;
+    Item it;
+    if (!find_item(a.cu, a.S, (int)a.N, t, [&](int, int n) { return (int)(((int64_t)n * G + BM - 1) / BM); }, it)) return;
+    const int r0 = (it.tiles - 1 - it.tile) * BM;
+    const int rows = it.n * G;
+    const int first = div_group(r0, G, a.gmagic);
+    const int last = div_group(r0 + BM < rows ? r0 + BM - 1 : rows - 1, G, a.gmagic);
+    const int lo = a.window > 0 && first - a.window + 1 > 0 ? (first - a.window + 1) & ~(BN - 1) : 0;
+    const int nb = (last - lo) / BN + 1;
+
+    const int row = r0 + 32 * wave + col;
+    const bool live = row < rows;
+    const int tok = live ? div_group(row, G, a.gmagic) : 0, hg = live ? row - tok * G : 0;
+    const int qpos = live ? tok : -1;
+    const int qlow = a.window > 0 ? qpos - a.window : -1;
+    const int64_t qtok = it.tok0 + tok;
+    const int head = kvh * G + hg;
+    const int64_t at = qtok * a.H + head;
+
+    bf16x8 qf[KS], df[KS];
+    float delta = 0.f;
+    {
+        const __bf16* qp = (const __bf16*)a.q + qtok * a.q_tok + (int64_t)head * a.q_head;
+        const __bf16* dp = (const __bf16*)a.dout + at * a.D;
+        const __bf16* op = (const __bf16*)a.out + at * a.D;
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+            const int d = 8 * chunk_of(s, g);
+            const bool in = live && d < a.D;
+            bf16x8 z = {};
+            qf[s] = in ? *(const bf16x8*)(qp + d) : z;
+            df[s] = in ? *(const bf16x8*)(dp + d) : z;
+            const bf16x8 of = in ? *(const bf16x8*)(op + d) : z;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) delta = __builtin_fmaf((float)df[s][e], (float)of[e], delta);
+        }
+    }
+    delta += other_half(delta, lane);
+    if (live && g == 0) a.delta[at] = delta;
+    const float lse2 = live ? a.lse[at] * kLog2e : 0.f;
+
+    const char* ksrc = (const char*)a.k + 2 * (it.tok0 * a.k_tok + kvh * a.k_head);
+    const char* vsrc = (const char*)a.v + 2 * (it.tok0 * a.v_tok + kvh * a.v_head);
+    const int crow = lane / P::CH, cpc = lane % P::CH;
+    unsigned koff[P::NI], voff[P::NI];
+#pragma unroll
+    for (int i = 0; i < P::NI; ++i) {
+        const int r = 16 * wave + P::RPI * i + crow;
+        const int c = cpc ^ swz<DP>(r);
+        const bool in = 8 * c < a.D;
+        koff[i] = in ? (unsigned)(r * a.k_tok * 2 + 16 * c) : kOutside;
+        voff[i] = in ? (unsigned)(r * a.v_tok * 2 + 16 * c) : kOutside;
+    }
+    const unsigned base = lds_addr(&lds[0][0][0]) + wave * (TILE / 4);
+    auto copy_tile = [&](int j, int stage) {
+        const unsigned dst = base + stage * (2 * TILE);
+        const int p0 = lo + j * BN;
+        const int left = last + 1 - p0 < BN ? last + 1 - p0 : BN;
+        const u32x4 kr = buffer_rsrc(ksrc + (int64_t)p0 * a.k_tok * 2, (int)((left - 1) * a.k_tok * 2) + 2 * a.D);
+        const u32x4 vr = buffer_rsrc(vsrc + (int64_t)p0 * a.v_tok * 2, (int)((left - 1) * a.v_tok * 2) + 2 * a.D);
+#pragma unroll
+        for (int i = 0; i < P::NI; ++i) {
+            copy16(kr, dst + 1024 * i, koff[i]);
+            copy16(vr, dst + TILE + 1024 * i, voff[i]);
+        }
+    };
+    unsigned tro[DT][2];
+#pragma unroll
+    for (int dt = 0; dt < DT; ++dt) {
+        tro[dt][0] = tr_offset<DP>(dt, 0, lane);
+        tro[dt][1] = tr_offset<DP>(dt, 1, lane);
+    }
+
+    f32x16 acc[DT] = {};
+    const int wr0 = r0 + 32 * wave;
+    const int wfirst = div_group(wr0, G, a.gmagic);
+    const int wlast = div_group(wr0 + 31 < rows ? wr0 + 31 : rows - 1, G, a.gmagic);
+    const bool wlive = wr0 < rows;
+
+    copy_tile(0, 0);
+    for (int j = 0; j < nb; ++j) {
+        const int stage = j & 1;
+        wait_vm<0>();
+        barrier_lds();
+        if (j + 1 < nb) copy_tile(j + 1, stage ^ 1);
+        const int p0 = lo + j * BN;
+        if (!wlive || p0 > wlast || (a.window > 0 && p0 + BN - 1 <= wfirst - a.window)) continue;
+        const unsigned char *kt = lds[stage][0], *vt = lds[stage][1];
+        const bool edge = p0 + BN - 1 > wfirst || (a.window > 0 && p0 <= wlast - a.window) || wr0 + 32 > rows;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            f32x16 sc = {}, dp = {};
+#pragma unroll
+            for (int s = 0; s < KS; ++s) {
+                sc = mfma32(row_frag<DP>(kt, 32 * h + col, s, g), qf[s], sc);
+                dp = mfma32(row_frag<DP>(vt, 32 * h + col, s, g), df[s], dp);
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                sc[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[i], a.sl2, -lse2)) * (dp[i] - delta);
+            if (edge) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const int p = p0 + 32 * h + acc_row(i, g);
+                    if (p > qpos || p <= qlow) sc[i] = 0.f;
+                }
+            }
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                const bf16x8 sf = pack_half(sc, s);
+#pragma unroll
+                for (int dt = 0; dt < DT; ++dt)
+                    acc[dt] = mfma32(tr_frag(kt + (2 * h + s) * (32 * DP), tro[dt][0], tro[dt][1]), sf, acc[dt]);
+            }
+        }
+    }
+    if (live) store_row<DT>((__bf16*)a.dq + at * a.D, acc, a.scale, g, a.D);
+}
+
+template <int DP>
+__global__ __launch_bounds__(256, 2) void attn_dkdv_kernel(AttnBwdArgs a) {
+    constexpr int TILE = BN * DP * 2;
+    constexpr int KS = DP / 16, DT = DP / 32;
+    using P = CopyPlan<DP>;
+    __shared__ __attribute__((aligned(1024))) unsigned char lds[2][2][TILE];  // [stage][Q, dout]
+    __shared__ __attribute__((aligned(256))) float stat[2][2][BN];            // [stage][lse, delta]
+
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int g = lane >> 5, col = lane & 31, G = a.G;
+    const int kvh = blockIdx.x % a.K, t = blockIdx.x / a.K;
+    Item it;
+    // key blocks in order: the first of a sequence has the most rows
+    if (!find_item(a.cu, a.S, (int)a.N, t, [&](int, int n) { return (n + BM - 1) / BM; }, it)) return;
+    const int k0 = it.tile * BM;
+    const int rows = it.n * G;
+    const int klast = k0 + BM < it.n ? k0 + BM - 1 : it.n - 1;
+    const int rbeg = (k0 * G) & ~(BN - 1);
+    int64_t re = a.window > 0 ? ((int64_t)klast + a.window) * G : rows;
+    const int rend = re < rows ? (int)re : rows;  // rows that see some key of the block: [k0 G, rend)
+    const int nb = (rend - rbeg + BN - 1) / BN;
+
+    const int key = k0 + 32 * wave + col;
+    const bool live = key < it.n;
+    const int64_t ktok = it.tok0 + (live ? key : 0);
+    // rows that see this lane's key: [rlo, rhi)
+    const int rlo = live ? key * G : 0x7fffffff;
+    int64_t rh = a.window > 0 ? ((int64_t)key + a.window) * G : rows;
+    const int rhi = rh < rows ? (int)rh : rows;
+
+    bf16x8 kf[KS], vf[KS];
+    {
+        const __bf16* kp = (const __bf16*)a.k + ktok * a.k_tok + (int64_t)kvh * a.k_head;
+        const __bf16* vp = (const __bf16*)a.v + ktok * a.v_tok + (int64_t)kvh * a.v_head;
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+            const int d = 8 * chunk_of(s, g);
+            const bool in = live && d < a.D;
+            bf16x8 z = {};
+            kf[s] = in ? *(const bf16x8*)(kp + d) : z;
+            vf[s] = in ? *(const bf16x8*)(vp + d) : z;
+        }
+    }
+
+    const int crow = lane / P::CH, cpc = lane % P::CH;
+    const unsigned base = lds_addr(&lds[0][0][0]) + wave * (TILE / 4);
+    const unsigned sbase = lds_addr(&stat[0][0][0]);
+    const char* qsrc = (const char*)a.q + 2 * (it.tok0 * a.q_tok + (int64_t)kvh * G * a.q_head);
+    const int64_t first_row = (int64_t)it.tok0 * a.H + kvh * G;  // row 0 in [N][H] order
+    const char* dsrc = (const char*)a.dout + 2 * first_row * a.D;
+    auto copy_tile = [&](int j, int stage) {
+        const unsigned dst = base + stage * (2 * TILE);
+#pragma unroll
+        for (int i = 0; i < P::NI; ++i) {
+            const int rr = 16 * wave + P::RPI * i + crow;
+            const int r = rbeg + j * BN + rr;
+            const int c = cpc ^ swz<DP>(rr);
+            const char *qp = (const char*)zeros, *dp = (const char*)zeros;
+            if (8 * c < a.D && r < rows) {
+                const int tk = div_group(r, G, a.gmagic), hg = r - tk * G;
+                qp = qsrc + 2 * (tk * a.q_tok + hg * a.q_head) + 16 * c;
+                dp = dsrc + 2 * (int64_t)(tk * a.H + hg) * a.D + 16 * c;
+            }
+            copy16_at(qp, dst + 1024 * i);
+            copy16_at(dp, dst + TILE + 1024 * i);
+        }
+        if (wave < 2) {  // wave 0: lse, wave 1: delta, of the tile's 64 rows
+            const int r = rbeg + j * BN + lane;
+            const int tk = r < rows ? div_group(r, G, a.gmagic) : 0, hg = r < rows ? r - tk * G : 0;
+            const float* src = wave == 0 ? a.lse : a.delta;
+            copy4_at(src + first_row + (int64_t)tk * a.H + hg, sbase + stage * (2 * BN * 4) + wave * (BN * 4));
+        }
+    };
+    unsigned tro[DT][2];
+#pragma unroll
+    for (int dt = 0; dt < DT; ++dt) {
+        tro[dt][0] = tr_offset<DP>(dt, 0, lane);
+        tro[dt][1] = tr_offset<DP>(dt, 1, lane);
+    }
+
+    f32x16 dk[DT] = {}, dv[DT] = {};
+    const int wk0 = k0 + 32 * wave;                                        // this wave's keys
+    const int wklast = wk0 + 31;
+    const bool wlive = wk0 < it.n;
+
+    if (nb > 0) copy_tile(0, 0);
+    for (int j = 0; j < nb; ++j) {
+        const int stage = j & 1;
+        wait_vm<0>();
+        barrier_lds();
+        if (j + 1 < nb) copy_tile(j + 1, stage ^ 1);
+        const int p0 = rbeg + j * BN;
+        if (!wlive || p0 + BN - 1 < wk0 * G) continue;
+        const unsigned char *qt = lds[stage][0], *dt_ = lds[stage][1];
+        const bool edge = p0 < wklast * G || p0 + BN > rows || wklast >= it.n ||
+                          (a.window > 0 && p0 + BN > ((int64_t)wk0 + a.window) * G);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            f32x16 sc = {}, dp = {};
+#pragma unroll
+            for (int s = 0; s < KS; ++s) {
+                sc = mfma32(row_frag<DP>(qt, 32 * h + col, s, g), kf[s], sc);
+                dp = mfma32(row_frag<DP>(dt_, 32 * h + col, s, g), vf[s], dp);
+            }
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                const f32x4 ls = *(const f32x4*)&stat[stage][0][32 * h + 8 * b + 4 * g];
+                const f32x4 de = *(const f32x4*)&stat[stage][1][32 * h + 8 * b + 4 * g];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int i = 4 * b + e;
+                    sc[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[i], a.sl2, -ls[e] * kLog2e));
+                    dp[i] = sc[i] * (dp[i] - de[e]);
+                }
+            }
+            if (edge) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const int r = p0 + 32 * h + acc_row(i, g);
+                    if (r < rlo || r >= rhi) {
+                        sc[i] = 0.f;
+                        dp[i] = 0.f;
+                    }
+                }
+            }
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                const bf16x8 pf = pack_half(sc, s), sf = pack_half(dp, s);
+                const unsigned o = (2 * h + s) * (32 * DP);
+#pragma unroll
+                for (int dt = 0; dt < DT; ++dt) {
+                    dv[dt] = mfma32(tr_frag(dt_ + o, tro[dt][0], tro[dt][1]), pf, dv[dt]);
+                    dk[dt] = mfma32(tr_frag(qt + o, tro[dt][0], tro[dt][1]), sf, dk[dt]);
+                }
+            }
+        }
+    }
+    if (!live) return;
+    const int64_t at = (ktok * a.K + kvh) * a.D;
+    store_row<DT>((__bf16*)a.dk + at, dk, a.scale, g, a.D);
+    store_row<DT>((__bf16*)a.dv + at, dv, 1.f, g, a.D);
+}
+
+template <int DP>
+hipError_t launch(const AttnBwdArgs& a, hipStream_t s) {
+    const int64_t dq_grid = (a.N * a.G / BM + a.S) * a.K, dkv_grid = (a.N / BM + a.S) * a.K;
+    if (dq_grid > 0x7fffffff) return hipErrorInvalidValue;
+    attn_dq_kernel<DP><<<dim3((unsigned)dq_grid), dim3(256), 0, s>>>(a);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    attn_dkdv_kernel<DP><<<dim3((unsigned)dkv_grid), dim3(256), 0, s>>>(a);
+    return hipGetLastError();
+}
+
+}  // namespace
+}  // namespace attn
+
+hipError_t launch_attn_bwd_bf16(const AttnBwdArgs& a, hipStream_t s) {
+    return a.D <= 64 ? attn::launch<64>(a, s) : attn::launch<128>(a, s);
+}
+
+}  // namespace e2ttt

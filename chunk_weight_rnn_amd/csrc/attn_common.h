@@ -1,0 +1,258 @@
+// Shared by the attention kernels (attn_fwd.hip, attn_bwd.hip, attn_f32.hip):
+// argument structs, the work items of packed sequences, and the LDS tile
+// layout of the bf16 MFMA kernels.
+//
+// A row is one (token, query head) pair.  The G = heads / kv_heads query
+// heads that share a key head are packed into the rows of one tile, token
+// major: row r of a sequence's key head is token r / G, head r % G of its
+// group.  So a key/value tile that was staged once serves the whole group, in
+// the backward the sums over a group are ordinary sums over rows, and a single
+// new token still fills as many rows as its group has heads.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "layer_internal.h"
+
+namespace e2ttt {
+namespace attn {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) bf16x4 lds_bf16x4_t;
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+__device__ __forceinline__ float neg_inf() { return -__builtin_inff(); }
+
+__device__ __forceinline__ f32x16 mfma32(bf16x8 a, bf16x8 b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+
+// Value of the lane that holds the same column in the other half (lane ^ 32).
+__device__ __forceinline__ float other_half(float x, int lane) {
+    const unsigned u = __builtin_bit_cast(unsigned, x);
+    const auto r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+    return __builtin_bit_cast(float, lane < 32 ? r[1] : r[0]);
+}
+
+// Row r's token, r / G (the host bounds r G below 2^32).
+__device__ __forceinline__ int div_group(int r, int G, unsigned magic) {
+    return G == 1 ? r : (int)__umulhi((unsigned)r, magic);
+}
+
+// ------------------------------------------------------------- work items
+// The t-th tile of BM rows, counted over all sequences; a sequence of n tokens
+// has ceil(n G / BM) of them.  Every wave searches for itself, 64 sequences
+// per step, from the offsets in memory (clamped, so that whatever they hold no
+// address leaves the tensors).  False past the last tile.
+struct Item {
+    int seq, tok0, n;  // sequence, its first token, its length
+    int tile, tiles;   // tile within the sequence, tiles of the sequence
+};
+
+__device__ __forceinline__ int clamped(int x, int hi) { return x < 0 ? 0 : (x > hi ? hi : x); }
+
+template <class F>
+__device__ __forceinline__ bool find_item(const int* __restrict__ cu, int S, int N, int t, F&& tiles_of, Item& it) {
+    const int lane = threadIdx.x & 63;
+    int base = 0;
+    for (int s0 = 0; s0 < S; s0 += 64) {
+        const int s = s0 + lane;
+        int a = 0, n = 0, m = 0;
+        if (s < S) {
+            a = clamped(cu[s], N);
+            n = clamped(cu[s + 1], N) - a;
+            n = n > 0 ? n : 0;
+            m = tiles_of(s, n);
+        }
+        int incl = m;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const int y = __shfl_up(incl, d);
+            if (lane >= d) incl += y;
+        }
+        const unsigned long long past = __ballot(base + incl > t);
+        if (past) {
+            const int l = __builtin_ctzll(past);
+            it.seq = s0 + l;
+            it.tok0 = __builtin_amdgcn_readfirstlane(__shfl(a, l));
+            it.n = __builtin_amdgcn_readfirstlane(__shfl(n, l));
+            it.tiles = __builtin_amdgcn_readfirstlane(__shfl(m, l));
+            it.tile = t - base - __builtin_amdgcn_readfirstlane(__shfl(incl, l)) + it.tiles;
+            return true;
+        }
+        base += __builtin_amdgcn_readfirstlane(__shfl(incl, 63));
+    }
+    return false;
+}
+
+// Tokens a sequence has in the cache, clamped to what its page table holds.
+__device__ __forceinline__ int kept_tokens(const PagedKV& pg, int seq, int n) {
+    const int64_t room = ((int64_t)pg.wide << pg.shift) - n;
+    return clamped(pg.cached[seq], room > 0 ? (int)room : 0);
+}
+
+// Writes new tokens' keys and values into their slots: block b of
+// append_blocks, one 16-byte chunk of k and of v per thread.  Nothing else in
+// the call reads these slots: positions >= cached come from k and v.
+template <typename T>
+__device__ __forceinline__ void append_block(const AttnArgs& a, int b) {
+    constexpr int E = 16 / sizeof(T);
+    const int64_t u = (int64_t)b * 256 + threadIdx.x;
+    const int ch = a.D / E;
+    const int64_t nk = u / ch;
+    const int64_t n = nk / a.K;
+    if (n >= a.N) return;
+    const int c = (int)(u - nk * ch) * E, kvh = (int)(nk - n * a.K);
+    int lo = 0, hi = a.S;  // the last sequence that starts at or before token n
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (a.cu[mid] <= n) lo = mid;
+        else hi = mid;
+    }
+    const int t0 = clamped(a.cu[lo], (int)a.N), count = clamped(a.cu[lo + 1], (int)a.N) - t0;
+    const int i = (int)n - t0;
+    if (i < 0 || i >= count) return;
+    const int64_t pos = (int64_t)kept_tokens(a.pg, lo, count) + i;
+    if ((pos >> a.pg.shift) >= a.pg.wide) return;
+    const int page = a.pg.table[(int64_t)lo * a.pg.wide + (pos >> a.pg.shift)];
+    if ((unsigned)page >= (unsigned)a.pg.pages) return;
+    const int64_t slot = pos & (((int64_t)1 << a.pg.shift) - 1);
+    const u32x4 kx = *(const u32x4*)((const T*)a.k + n * a.k_tok + kvh * a.k_head + c);
+    const u32x4 vx = *(const u32x4*)((const T*)a.v + n * a.v_tok + kvh * a.v_head + c);
+    *(u32x4*)((T*)a.pg.kc + page * a.pg.k_page + kvh * a.pg.k_head + slot * a.pg.k_slot + c) = kx;
+    *(u32x4*)((T*)a.pg.vc + page * a.pg.v_page + kvh * a.pg.v_head + slot * a.pg.v_slot + c) = vx;
+}
+
+// -------------------------------------------------------------- LDS tiles
+// A bf16 tile holds rows of DP values (DP = 64 or 128, head dims below it
+// filled with zeros), 2 DP bytes each, with 16-byte chunk c of row t at
+// physical chunk c ^ swz(t).  Two reads have to be free of bank conflicts (64
+// four-byte banks, i.e. 16 chunks side by side):
+//  * row fragments, ds_read_b128: lanes 8a .. 8a+7 and 32+8a .. 32+8a+7 are
+//    served together, eight consecutive rows at a chunk and at the same chunk
+//    with bit 1 flipped (chunk_of), which the swizzle puts on 16 different
+//    chunk columns;
+//  * transpose fragments, ds_read_b64_tr_b16: lanes 0..31 together, four
+//    consecutive rows at four aligned chunks; rows r .. r+3 land on different
+//    groups of four chunk columns.
+template <int DP>
+__device__ __forceinline__ int swz(int t) {
+    if constexpr (DP == 128) return ((t & 3) << 2) | ((t >> 2) & 3);
+    else return (((t >> 1) & 1) << 2) | ((t >> 2) & 3);
+}
+
+// Chunk of the head dimension that lane half g holds at k-step s of a
+// 32x32x16 product over it.  Any order does, if both operands follow it.
+__device__ __forceinline__ constexpr int chunk_of(int s, int g) { return ((s >> 1) << 2) | (g << 1) | (s & 1); }
+
+// Row fragment: operand row t, k-step s.
+template <int DP>
+__device__ __forceinline__ bf16x8 row_frag(const unsigned char* tile, int t, int s, int g) {
+    return *(const bf16x8*)(tile + t * (2 * DP) + 16 * (chunk_of(s, g) ^ swz<DP>(t)));
+}
+
+// Transpose fragment offsets: operand row = head-dim column 32 dt + lane % 32,
+// operand k 0..3 = tile rows 16 s + 4 (lane / 32) + {0..3} (hi = 0), k 4..7 the
+// same + 8 (hi = 1).  A k-step adds 16 rows, 32 DP bytes, and keeps the
+// swizzle.  This is the row order in which a 32x32 accumulator holds its rows,
+// so an accumulator packed to bf16 is the other operand without any exchange.
+template <int DP>
+__device__ __forceinline__ unsigned tr_offset(int dt, int hi, int lane) {
+    const int p = lane & 15, G = lane >> 4;
+    const int r = 4 * (G >> 1) + 8 * hi + (p >> 2);
+    const int chunk = 4 * dt + 2 * (G & 1) + ((p & 3) >> 1);
+    return (unsigned)(r * (2 * DP) + 16 * (chunk ^ swz<DP>(r)) + 8 * (p & 1));
+}
+
+__device__ __forceinline__ bf16x8 tr_frag(const unsigned char* tile, unsigned off0, unsigned off1) {
+    const bf16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_bf16x4_t*)(tile + off0));
+    const bf16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_bf16x4_t*)(tile + off1));
+    return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+
+// Row of a 32x32 accumulator element i in lane half g.
+__device__ __forceinline__ constexpr int acc_row(int i, int g) { return 8 * (i >> 2) + 4 * g + (i & 3); }
+
+// Half hs (elements 8 hs .. 8 hs + 7, 16 rows) of an accumulator as a bf16
+// operand, rounded to nearest even.
+__device__ __forceinline__ bf16x8 pack_half(const f32x16& x, int hs) {
+    bf16x8 r;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) r[e] = (__bf16)x[8 * hs + e];
+    return r;
+}
+
+// ------------------------------------------------------- copies to the LDS
+// dword 3 of a raw buffer resource (gfx9 family: 32-bit data format, no swizzle)
+constexpr int RSRC_W3 = 0x00020000;
+constexpr unsigned kOutside = 0x7fffff00u;  // a buffer offset past every resource here: reads zeros
+
+__device__ __forceinline__ u32x4 buffer_rsrc(const void* base, int num_bytes) {
+    const unsigned long long p = (unsigned long long)base;
+    u32x4 r;
+    r[0] = __builtin_amdgcn_readfirstlane((unsigned)p);
+    r[1] = __builtin_amdgcn_readfirstlane((unsigned)(p >> 32) & 0xFFFFu);
+    r[2] = __builtin_amdgcn_readfirstlane((unsigned)num_bytes);
+    r[3] = RSRC_W3;
+    return r;
+}
+
+// 16 bytes per lane from base + voff (zeros at or past the resource's end) to
+// LDS byte lds + 16 lane.  No register is written; wait with wait_vm.
+__device__ __forceinline__ void copy16(u32x4 rsrc, unsigned lds, unsigned voff) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+                 :
+                 : "s"(lds), "v"(voff), "s"(rsrc)
+                 : "memory", "m0");
+}
+
+// The same from a 64-bit address per lane.
+__device__ __forceinline__ void copy16_at(const void* p, unsigned lds) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
+                 :
+                 : "s"(lds), "v"(p)
+                 : "memory", "m0");
+}
+
+// 4 bytes per lane.
+__device__ __forceinline__ void copy4_at(const void* p, unsigned lds) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off"
+                 :
+                 : "s"(lds), "v"(p)
+                 : "memory", "m0");
+}
+
+__device__ __forceinline__ unsigned lds_addr(const void* p) {
+    return __builtin_amdgcn_readfirstlane((unsigned)(uintptr_t)(__attribute__((address_space(3))) const void*)p);
+}
+
+template <int N>
+__device__ __forceinline__ void wait_vm() {
+    static_assert(N >= 0 && N < 64, "vmcnt holds 6 bits");
+    __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | 0x0F70);
+    asm volatile("" ::: "memory");
+}
+
+// Workgroup barrier that waits for this wave's LDS accesses, not for its
+// copies in flight.
+__device__ __forceinline__ void barrier_lds() {
+    __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+// Blocks that append_block needs (none when nothing is appended).
+inline int64_t append_blocks(const AttnArgs& a, int elems) {
+    return a.pg.append ? (a.N * a.K * (a.D / elems) + 255) / 256 : 0;
+}
+
+}  // namespace attn
+}  // namespace e2ttt

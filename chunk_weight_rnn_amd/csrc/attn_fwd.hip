@@ -1,0 +1,375 @@
+// Causal grouped-head attention, bf16 MFMA forward: packed sequences, and new
+// tokens over a paged cache.
+//
+//   s_ij = scale <q_i, k_j>,   out_i = sum_j exp(s_ij - lse_i) v_j
+//
+// One pass over the keys with the running maximum m and sum l of the softmax:
+// a key tile's scores S^T = K Q^T leave the MFMA with a query per lane, so the
+// maximum, the exponentials and the rescaling need no exchange beyond the two
+// lane halves, and P^T, packed to bf16, is the second operand of
+// O^T += V^T P^T as it stands (attn_common.h).  V^T comes from the row-major
+// tile by the transpose read.
+//
+// A workgroup is 4 waves of 32 rows each over shared tiles of 64 keys, two
+// stages deep; two workgroups share a compute unit, so that one's softmax
+// (VALU) runs beside the other's products.
+#include "attn_common.h"
+
+namespace e2ttt {
+namespace attn {
+namespace {
+
+constexpr int BM = 128;  // rows of a tile: 4 waves x 32
+constexpr int BN = 64;   // keys of a tile
+
+// The running maximum is only raised when a row exceeds it by this many
+// powers of two: sums up to 2^8 times larger lose nothing in fp32, and most
+// tiles skip the rescaling of the outputs.
+constexpr float kLazy = 8.f;
+
+__device__ __align__(256) unsigned char zeros[256];  // read in place of rows outside a sequence
+
+// Source of the key/value rows of one (sequence, key head).
+struct Source {
+    const char *k, *v;        // packed rows: position 0
+    const char *kc, *vc;      // paged: this key head in page 0
+    const int* table;         // this sequence's pages
+    int fresh;                // positions >= fresh come from the packed rows (position - fresh)
+    int begin, end;           // positions outside [begin, end) are read as zeros (paged), or past end (packed)
+};
+
+// A wave's part of a tile copy: BN / 4 rows, 1 KiB (1024 / (2 DP) rows) per
+// instruction.
+template <int DP>
+struct CopyPlan {
+    static constexpr int RPI = 512 / DP;       // rows per instruction
+    static constexpr int NI = (BN / 4) / RPI;  // instructions per wave and tensor
+    static constexpr int CH = DP / 8;          // chunks per row
+};
+
+template <int DP, bool PAGED, bool SPLIT>
+__global__ __launch_bounds__(256, 2) void attn_fwd_kernel(AttnArgs a) {
+    constexpr int TILE = BN * DP * 2;
+    constexpr int KS = DP / 16, DT = DP / 32;
+    using P = CopyPlan<DP>;
+    __shared__ __attribute__((aligned(1024))) unsigned char lds[2][2][TILE];  // [stage][K, V]
+
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int g = lane >> 5, col = lane & 31;
+    int b = blockIdx.x;
+    if constexpr (PAGED) {  // blocks past the tiles write the new tokens into their slots
+        const int tiles = a.ntiles * a.nsplit * a.K;
+        if (b >= tiles) {
+            append_block<__bf16>(a, b - tiles);
+            return;
+        }
+    }
+    const int kvh = b % a.K;
+    b /= a.K;
+    const int split = SPLIT ? b % a.nsplit : 0;
+    const int t = SPLIT ? b / a.nsplit : b;
+    Item it;
+    const int G = a.G;
+    if (!find_item(a.cu, a.S, (int)a.N, t, [&](int, int n) { return (int)(((int64_t)n * G + BM - 1) / BM); }, it)) return;
+    // the longest rows of a sequence first: its last tile has the most keys
+    const int r0 = (it.tiles - 1 - it.tile) * BM;
+    const int rows = it.n * G;
+    int kept = 0;
+    if constexpr (PAGED) {
+        kept = kept_tokens(a.pg, it.seq, it.n);
+    }
+    const int first = kept + div_group(r0, G, a.gmagic);                                            // position of the tile's first row
+    const int last = kept + div_group(r0 + BM < rows ? r0 + BM - 1 : rows - 1, G, a.gmagic);  // and of its last
+    const int lo = a.window > 0 && first - a.window + 1 > 0 ? (first - a.window + 1) & ~(BN - 1) : 0;
+    const int nb = (last - lo) / BN + 1;
+    int j0 = 0, j1 = nb;
+    if (SPLIT) {
+        const int per = (nb + a.nsplit - 1) / a.nsplit;
+        j0 = split * per;
+        j1 = j0 + per < nb ? j0 + per : nb;
+    }
+
+    // this lane's row
+    const int row = r0 + 32 * wave + col;
+    const bool live = row < rows;
+    const int tok = live ? div_group(row, G, a.gmagic) : 0, hg = live ? row - tok * G : 0;
+    const int qpos = live ? kept + tok : -1;
+    const int qlow = a.window > 0 ? qpos - a.window : -1;  // keys at or below it are out of the window
+    const int64_t qtok = it.tok0 + tok;
+    const int head = kvh * G + hg;
+
+    bf16x8 qf[KS];
+    {
+        const __bf16* qp = (const __bf16*)a.q + qtok * a.q_tok + (int64_t)head * a.q_head;
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+            const int d = 8 * chunk_of(s, g);
+            bf16x8 z = {};
+            qf[s] = live && d < a.D ? *(const bf16x8*)(qp + d) : z;
+        }
+    }
+
+    Source src;
+    src.k = (const char*)a.k + 2 * (it.tok0 * a.k_tok + kvh * a.k_head);
+    src.v = (const char*)a.v + 2 * (it.tok0 * a.v_tok + kvh * a.v_head);
+    src.begin = a.window > 0 ? first - a.window + 1 : 0;
+    src.end = last + 1;
+    if constexpr (PAGED) {
+        src.kc = (const char*)a.pg.kc + 2 * kvh * a.pg.k_head;
+        src.vc = (const char*)a.pg.vc + 2 * kvh * a.pg.v_head;
+        src.table = a.pg.table + (int64_t)it.seq * a.pg.wide;
+        src.fresh = a.pg.append ? kept : 0x7fffffff;
+    }
+
+    // copy offsets: row (within this wave's quarter) and chunk of this lane
+    const int crow = lane / P::CH, cpc = lane % P::CH;
+    unsigned koff[P::NI], voff[P::NI];
+#pragma unroll
+    for (int i = 0; i < P::NI; ++i) {
+        const int r = 16 * wave + P::RPI * i + crow;
+        const int c = cpc ^ swz<DP>(r);
+        const bool in = 8 * c < a.D;
+        koff[i] = in ? (unsigned)(r * a.k_tok * 2 + 16 * c) : kOutside;
+        voff[i] = in ? (unsigned)(r * a.v_tok * 2 + 16 * c) : kOutside;
+    }
+    const unsigned base = lds_addr(&lds[0][0][0]) + wave * (TILE / 4);
+
+    int page[P::NI];  // paged: the next tile's page indices, loaded a tile ahead
+    auto load_pages = [&](int j) {
+        if constexpr (PAGED) {
+#pragma unroll
+            for (int i = 0; i < P::NI; ++i) {
+                const int pos = lo + j * BN + 16 * wave + P::RPI * i + crow;
+                const int pi = pos >> a.pg.shift;
+                page[i] = pos >= src.begin && pos < src.end && pos < src.fresh && pi < a.pg.wide ? src.table[pi] : -1;
+            }
+        }
+    };
+    auto copy_tile = [&](int j, int stage) {
+        const unsigned dst = base + stage * (2 * TILE);
+        const int p0 = lo + j * BN;
+        if constexpr (PAGED) {
+#pragma unroll
+            for (int i = 0; i < P::NI; ++i) {
+                const int r = 16 * wave + P::RPI * i + crow;
+                const int pos = p0 + r;
+                const int64_t c = 16 * (cpc ^ swz<DP>(r));
+                const char *kp = (const char*)zeros, *vp = (const char*)zeros;
+                if (c < 2 * a.D && pos >= src.begin && pos < src.end) {
+                    if (pos >= src.fresh) {
+                        kp = src.k + 2 * (pos - src.fresh) * a.k_tok + c;
+                        vp = src.v + 2 * (pos - src.fresh) * a.v_tok + c;
+                    } else if ((unsigned)page[i] < (unsigned)a.pg.pages) {
+                        const int64_t slot = pos & ((1 << a.pg.shift) - 1);
+                        kp = src.kc + 2 * (page[i] * a.pg.k_page + slot * a.pg.k_slot) + c;
+                        vp = src.vc + 2 * (page[i] * a.pg.v_page + slot * a.pg.v_slot) + c;
+                    }
+                }
+                copy16_at(kp, dst + 1024 * i);
+                copy16_at(vp, dst + TILE + 1024 * i);
+            }
+        } else {
+            const int left = src.end - p0 < BN ? src.end - p0 : BN;  // rows of the tile that exist
+            const u32x4 kr = buffer_rsrc(src.k + (int64_t)p0 * a.k_tok * 2, (int)((left - 1) * a.k_tok * 2) + 2 * a.D);
+            const u32x4 vr = buffer_rsrc(src.v + (int64_t)p0 * a.v_tok * 2, (int)((left - 1) * a.v_tok * 2) + 2 * a.D);
+#pragma unroll
+            for (int i = 0; i < P::NI; ++i) {
+                copy16(kr, dst + 1024 * i, koff[i]);
+                copy16(vr, dst + TILE + 1024 * i, voff[i]);
+            }
+        }
+    };
+
+    unsigned tro[DT][2];
+#pragma unroll
+    for (int dt = 0; dt < DT; ++dt) {
+        tro[dt][0] = tr_offset<DP>(dt, 0, lane);
+        tro[dt][1] = tr_offset<DP>(dt, 1, lane);
+    }
+
+    f32x16 acc[DT] = {};
+    float m = neg_inf(), l = 0.f;
+    // rows of this wave: the positions that bound its masks
+    const int wr0 = r0 + 32 * wave;
+    const int wfirst = kept + div_group(wr0, G, a.gmagic);
+    const int wlast = kept + div_group(wr0 + 31 < rows ? wr0 + 31 : rows - 1, G, a.gmagic);
+    const bool wlive = wr0 < rows;
+
+    if (j0 < j1) {
+        load_pages(j0);
+        copy_tile(j0, 0);
+        load_pages(j0 + 1);
+    }
+    for (int j = j0; j < j1; ++j) {
+        const int stage = (j - j0) & 1;
+        wait_vm<0>();
+        barrier_lds();
+        if (j + 1 < j1) {
+            copy_tile(j + 1, stage ^ 1);
+            load_pages(j + 2);
+        }
+        const int p0 = lo + j * BN;
+        if (!wlive || p0 > wlast || (a.window > 0 && p0 + BN - 1 <= wfirst - a.window)) continue;
+        const unsigned char *kt = lds[stage][0], *vt = lds[stage][1];
+        f32x16 sc[2] = {};
+#pragma unroll
+        for (int s = 0; s < KS; ++s)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) sc[h] = mfma32(row_frag<DP>(kt, 32 * h + col, s, g), qf[s], sc[h]);
+        if (p0 + BN - 1 > wfirst || (a.window > 0 && p0 <= wlast - a.window) || wr0 + 32 > rows) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const int p = p0 + 32 * h + acc_row(i, g);
+                    if (p > qpos || p <= qlow) sc[h][i] = neg_inf();
+                }
+        }
+        float mx = fmaxf(sc[0][0], sc[1][0]);
+#pragma unroll
+        for (int i = 1; i < 16; ++i) mx = fmaxf(mx, fmaxf(sc[0][i], sc[1][i]));
+        mx = fmaxf(mx, other_half(mx, lane)) * a.sl2;
+        if (__any(mx > m + kLazy)) {
+            const float mn = fmaxf(m, mx);
+            const float f = mn == neg_inf() ? 1.f : __builtin_amdgcn_exp2f(m - mn);
+            m = mn;
+            l *= f;
+#pragma unroll
+            for (int dt = 0; dt < DT; ++dt)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) acc[dt][i] *= f;
+        }
+        const float mu = m == neg_inf() ? 0.f : m;
+        float sum = 0.f;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                sc[h][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[h][i], a.sl2, -mu));
+                sum += sc[h][i];
+            }
+        l += sum;
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            const bf16x8 pf = pack_half(sc[s >> 1], s & 1);
+#pragma unroll
+            for (int dt = 0; dt < DT; ++dt)
+                acc[dt] = mfma32(tr_frag(vt + s * (32 * DP), tro[dt][0], tro[dt][1]), pf, acc[dt]);
+        }
+    }
+
+    l += other_half(l, lane);
+    if (!live) return;
+    const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // a row that sees nothing gives 0; NaN stays
+    if (SPLIT) {
+        const int64_t at = ((int64_t)split * a.N + qtok) * a.H + head;
+        if (g == 0) a.pl[at] = l > 0.f ? m + __builtin_amdgcn_logf(l) : (l == 0.f ? neg_inf() : l);
+        float* o = a.po + at * a.D;
+        if (j0 < j1) {
+#pragma unroll
+            for (int dt = 0; dt < DT; ++dt)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int d = 32 * dt + 8 * j + 4 * g;
+                    if (d < a.D) {
+                        f32x4 w;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) w[e] = acc[dt][4 * j + e] * inv;
+                        *(f32x4*)(o + d) = w;
+                    }
+                }
+        }
+        return;
+    }
+    if (a.lse && g == 0) a.lse[qtok * a.H + head] = l > 0.f ? (m + __builtin_amdgcn_logf(l)) * kLn2 : (l == 0.f ? neg_inf() : l);
+    __bf16* o = (__bf16*)a.out + (qtok * a.H + head) * a.D;
+#pragma unroll
+    for (int dt = 0; dt < DT; ++dt)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int d = 32 * dt + 8 * j + 4 * g;
+            if (d < a.D) {
+                bf16x4 w;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) w[e] = (__bf16)(acc[dt][4 * j + e] * inv);
+                *(bf16x4*)(o + d) = w;
+            }
+        }
+}
+
+// Joins the partial results of a split call: one wave per (token, head),
+//   out = sum_i 2^(pl_i - m) po_i / sum_i 2^(pl_i - m).
+template <typename T>
+__global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
+    const int64_t r = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    const int64_t NH = a.N * a.H;
+    if (r >= NH) return;
+    // a token outside every sequence has no partial results
+    const int tok = (int)(r / a.H);
+    if (tok < clamped(a.cu[0], (int)a.N) || tok >= clamped(a.cu[a.S], (int)a.N)) return;
+    const int lane = threadIdx.x & 63;
+    float m = neg_inf();
+    for (int i = 0; i < a.nsplit; ++i) {
+        const float x = a.pl[i * NH + r];
+        m = x != x ? x : fmaxf(m, x);  // NaN stays
+    }
+    float o0 = 0.f, o1 = 0.f, w = 0.f;
+    const int d = 2 * lane;
+    if (m != neg_inf())
+        for (int i = 0; i < a.nsplit; ++i) {
+            const float x = a.pl[i * NH + r];
+            if (x == neg_inf()) continue;  // this range saw nothing and wrote nothing
+            const float f = __builtin_amdgcn_exp2f(x - m);
+            w += f;
+            if (d < a.D) {
+                const float2 v = *(const float2*)(a.po + (i * NH + r) * a.D + d);
+                o0 += f * v.x;
+                o1 += f * v.y;
+            }
+        }
+    const float inv = w > 0.f ? 1.f / w : w;
+    if (d < a.D) {
+        T* o = (T*)a.out + r * a.D + d;
+        o[0] = (T)(o0 * inv);
+        o[1] = (T)(o1 * inv);
+    }
+    if (a.lse && lane == 0) a.lse[r] = w == 0.f ? neg_inf() : (m + __builtin_amdgcn_logf(w)) * kLn2;
+}
+
+template <int DP>
+hipError_t launch(const AttnArgs& a, hipStream_t s) {
+    const bool paged = a.pg.kc != nullptr;
+    const int64_t grid = (int64_t)a.ntiles * a.K * a.nsplit + (paged ? append_blocks(a, 8) : 0);
+    if (grid == 0) return hipSuccess;
+    if (grid > 0x7fffffff) return hipErrorInvalidValue;
+    const dim3 gr((unsigned)grid), bl(256);
+    if (paged && a.nsplit > 1)
+        attn_fwd_kernel<DP, true, true><<<gr, bl, 0, s>>>(a);
+    else if (paged)
+        attn_fwd_kernel<DP, true, false><<<gr, bl, 0, s>>>(a);
+    else if (a.nsplit > 1)
+        attn_fwd_kernel<DP, false, true><<<gr, bl, 0, s>>>(a);
+    else
+        attn_fwd_kernel<DP, false, false><<<gr, bl, 0, s>>>(a);
+    return hipGetLastError();
+}
+
+}  // namespace
+}  // namespace attn
+
+hipError_t launch_attn_fwd_bf16(const AttnArgs& a, hipStream_t s) {
+    return a.D <= 64 ? attn::launch<64>(a, s) : attn::launch<128>(a, s);
+}
+
+hipError_t launch_attn_join(const AttnArgs& a, bool f32, hipStream_t s) {
+    const int64_t grid = (a.N * a.H + 3) / 4;
+    if (grid == 0) return hipSuccess;
+    if (grid > 0x7fffffff) return hipErrorInvalidValue;
+    if (f32)
+        attn::attn_join_kernel<float><<<dim3((unsigned)grid), dim3(256), 0, s>>>(a);
+    else
+        attn::attn_join_kernel<__bf16><<<dim3((unsigned)grid), dim3(256), 0, s>>>(a);
+    return hipGetLastError();
+}
+
+}  // namespace e2ttt
