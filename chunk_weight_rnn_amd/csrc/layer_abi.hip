@@ -47,12 +47,13 @@ int attention_desc_status(const e2ttt_attention_desc* d, bool packed_kv) {
     const int64_t es = elem(d->io_dtype), lim = (int64_t)1 << 23;
     if (d->heads > 65536 || d->seqs >= (1 << 28) || d->tokens > 0x7fffffff) return E2TTT_ERR_UNSUPPORTED;
     const int64_t st[6] = {d->q_tok, d->q_head, d->k_tok, d->k_head, d->v_tok, d->v_head};
-    for (int i = 0; i < (packed_kv ? 6 : 2); ++i)
-        if (!stride_ok(st[i], es)) return E2TTT_ERR_INVALID_ARG;
+    const int64_t sizes[6] = {d->tokens, d->heads, d->tokens, d->kv_heads, d->tokens, d->kv_heads};
+    for (int i = 0; i < (packed_kv ? 6 : 2); ++i)  // the stride of a dimension of one is never used
+        if (sizes[i] > 1 && !stride_ok(st[i], es)) return E2TTT_ERR_INVALID_ARG;
     if (d->tokens > 1 && (d->q_tok < d->D || (packed_kv && (d->k_tok < d->D || d->v_tok < d->D))))
         return E2TTT_ERR_INVALID_ARG;
     for (int i = 0; i < (packed_kv ? 6 : 2); ++i)
-        if (st[i] > lim) return E2TTT_ERR_UNSUPPORTED;
+        if (sizes[i] > 1 && st[i] > lim) return E2TTT_ERR_UNSUPPORTED;
     const int64_t G = d->heads / d->kv_heads;
     if ((d->tokens + 256) * d->heads > 0x7fffffff) return E2TTT_ERR_UNSUPPORTED;
     if ((d->tokens + 256) * G >= ((int64_t)1 << 32) / G) return E2TTT_ERR_UNSUPPORTED;
@@ -67,14 +68,11 @@ int paged_desc_status(const e2ttt_paged_desc* d, bool append) {
         return E2TTT_ERR_INVALID_ARG;
     const int64_t es = elem(d->a.io_dtype), D = d->a.D;
     const int64_t s[6] = {d->kc_page, d->kc_head, d->kc_slot, d->vc_page, d->vc_head, d->vc_slot};
+    const int64_t n[3] = {d->pages, d->a.kv_heads, d->page_size}, lim = (int64_t)1 << 40;
+    for (int i = 0; i < 6; ++i)  // slots that the call writes must not overlap
+        if (n[i % 3] > 1 && (!stride_ok(s[i], es) || s[i] < D)) return E2TTT_ERR_INVALID_ARG;
     for (int i = 0; i < 6; ++i)
-        if (!stride_ok(s[i], es)) return E2TTT_ERR_INVALID_ARG;
-    const int64_t n[3] = {d->pages, d->a.kv_heads, d->page_size};
-    for (int i = 0; i < 6; ++i)
-        if (n[i % 3] > 1 && s[i] < D) return E2TTT_ERR_INVALID_ARG;  // slots written by the call would overlap
-    const int64_t lim = (int64_t)1 << 40;
-    for (int i = 0; i < 6; ++i)
-        if (s[i] > lim) return E2TTT_ERR_UNSUPPORTED;
+        if (n[i % 3] > 1 && s[i] > lim) return E2TTT_ERR_UNSUPPORTED;
     if (d->pages > 0x7fffffff || d->page_size > (1 << 24)) return E2TTT_ERR_UNSUPPORTED;
     if (d->table_width > 0x7fffffff || d->table_width * d->page_size + d->a.tokens + 256 > 0x7fffffff)
         return E2TTT_ERR_UNSUPPORTED;
@@ -98,6 +96,7 @@ AttnArgs make_args(const e2ttt_attention_desc& d) {
     a.k_head = d.k_head;
     a.v_tok = d.v_tok;
     a.v_head = d.v_head;
+    if (a.N == 1) a.q_tok = a.k_tok = a.v_tok = a.D;  // strides of a dimension of one are not checked
     return a;
 }
 
@@ -118,15 +117,35 @@ void plan(AttnArgs& a, bool f32, int64_t longest) {
     }
 }
 
+// A paged call of few rows per sequence on average goes to the decoding kernel
+// (bf16), which needs one launch where no context can be longer than
+// kOneLaunch keys, and two where the keys are shared out.
+constexpr int64_t kOneLaunch = 1024;
+void plan_paged(AttnArgs& a, bool f32, int64_t longest) {
+    const int64_t units = (longest + a.N + 127) / 128, tiles = a.N * a.G / 32 + a.S;
+    if (!f32 && a.N * a.G <= 32 * (int64_t)a.S && tiles * a.K <= 0x7fffffff / (units + 1)) {
+        a.decode = 1;
+        a.ntiles = (int)tiles;
+        if (a.window > 0 && longest > a.window + 64) longest = a.window + 64;
+        a.nsplit = longest <= kOneLaunch ? 1 : 2;
+        return;
+    }
+    plan(a, f32, longest);
+}
+
+size_t partial_rows(const AttnArgs& a) {
+    return a.decode ? (size_t)2 * kDecodeGroups * 32 : (size_t)a.nsplit * a.N * a.H;
+}
+
 size_t split_bytes(const AttnArgs& a) {
     if (a.nsplit == 1) return 0;
-    const size_t rows = (size_t)a.nsplit * a.N * a.H;
+    const size_t rows = partial_rows(a);
     return (rows * a.D * 4 + kWsAlign - 1) / kWsAlign * kWsAlign + rows * 4;
 }
 
 void set_split(AttnArgs& a, void* ws) {
     if (a.nsplit == 1) return;
-    const size_t rows = (size_t)a.nsplit * a.N * a.H;
+    const size_t rows = partial_rows(a);
     a.po = (float*)ws;
     a.pl = (float*)((char*)ws + (rows * a.D * 4 + kWsAlign - 1) / kWsAlign * kWsAlign);
 }
@@ -148,6 +167,7 @@ int alias_status(const Span (&in)[NI], const Span (&out)[NO]) {
 }
 
 int run_forward(AttnArgs& a, bool f32, hipStream_t s) {
+    if (a.decode) return launch_attn_decode_bf16(a, s) == hipSuccess ? E2TTT_OK : E2TTT_ERR_HIP;
     hipError_t e = f32 ? launch_attn_fwd_f32(a, s) : launch_attn_fwd_bf16(a, s);
     if (e == hipSuccess && a.nsplit > 1) e = launch_attn_join(a, f32, s);
     return e == hipSuccess ? E2TTT_OK : E2TTT_ERR_HIP;
@@ -242,12 +262,12 @@ int e2ttt_attention_backward(const e2ttt_attention_desc* d, const void* q, const
     a.dout = dout;
     a.lse = lse;
     a.cu = cu;
-    a.q_tok = d->q_tok;
-    a.q_head = d->q_head;
-    a.k_tok = d->k_tok;
-    a.k_head = d->k_head;
-    a.v_tok = d->v_tok;
-    a.v_head = d->v_head;
+    a.q_tok = f.q_tok;
+    a.q_head = f.q_head;
+    a.k_tok = f.k_tok;
+    a.k_head = f.k_head;
+    a.v_tok = f.v_tok;
+    a.v_head = f.v_head;
     a.N = N;
     a.S = f.S;
     a.H = f.H;
@@ -270,7 +290,7 @@ int e2ttt_attention_backward(const e2ttt_attention_desc* d, const void* q, const
 size_t e2ttt_paged_workspace_size(const e2ttt_paged_desc* d) {
     if (paged_desc_status(d, false) != E2TTT_OK) return kBad;
     AttnArgs a = make_args(d->a);
-    plan(a, d->a.io_dtype == E2TTT_F32, d->table_width * d->page_size);
+    plan_paged(a, d->a.io_dtype == E2TTT_F32, d->table_width * d->page_size);
     return split_bytes(a);
 }
 
@@ -288,7 +308,7 @@ int e2ttt_paged_attention(const e2ttt_paged_desc* d, const void* q, const void* 
     if (d->table_width > 0 && !aligned(table, 4)) return E2TTT_ERR_INVALID_ARG;
     const bool f32 = d->a.io_dtype == E2TTT_F32;
     AttnArgs a = make_args(d->a);
-    plan(a, f32, d->table_width * d->page_size);
+    plan_paged(a, f32, d->table_width * d->page_size);
     const size_t need = split_bytes(a);
     const int wst = workspace_status(ws, ws_bytes, need);
     if (wst != E2TTT_OK) return wst;

@@ -35,6 +35,7 @@ struct AttnArgs {
     float sl2;    // scale * log2(e)
     int ntiles;   // row tiles at most, over all sequences
     int nsplit;   // key ranges per row tile; > 1: partial results, joined after
+    int decode;   // paged: the kernel for few rows per sequence
     float* po;    // [nsplit][N][H][D] partial outputs
     float* pl;    // [nsplit][N][H] their base-2 log sums
     PagedKV pg;
@@ -44,6 +45,11 @@ struct AttnArgs {
 int attn_fwd_rows(const AttnArgs& a, bool f32);
 hipError_t launch_attn_fwd_bf16(const AttnArgs& a, hipStream_t s);
 hipError_t launch_attn_fwd_f32(const AttnArgs& a, hipStream_t s);
+// Few new tokens per sequence over a paged cache; nsplit > 1: the keys of all
+// items shared out evenly over kDecodeGroups workgroups, po / pl
+// [2 kDecodeGroups][32][D] / [2 kDecodeGroups][32].
+constexpr int kDecodeGroups = 512;
+hipError_t launch_attn_decode_bf16(const AttnArgs& a, hipStream_t s);
 hipError_t launch_attn_join(const AttnArgs& a, bool f32, hipStream_t s);
 
 struct AttnBwdArgs {

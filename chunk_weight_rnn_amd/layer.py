@@ -9,6 +9,7 @@ allocated through torch.  CPU tensors raise.
 from __future__ import annotations
 
 import ctypes
+from functools import lru_cache
 
 import torch
 
@@ -20,43 +21,50 @@ _BAD = ctypes.c_size_t(-1).value
 F8 = torch.float8_e4m3fn
 
 
+def _device(first, **others) -> int:
+    """The one GPU that every tensor is on."""
+    dev = first.get_device()
+    if dev < 0:
+        raise ValueError("tensors must be on a GPU (no CPU path exists)")
+    for name, t in others.items():
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"{name} must be a GPU tensor on the same device as the others")
+    return dev
+
+
+def _call(fn: str, dev: int, stream, *args):
+    """Calls the library on `stream` (default: the current stream of the
+    tensors' device, which is made current for the call if it is not)."""
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return _call(fn, dev, stream, *args)
+    s = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    st = getattr(_lib.load(), fn)(*args, s)
+    if st != 0:
+        raise E2TTTError(fn, st)
+
+
 def _p(t):
     return None if t is None else t.data_ptr()
 
 
-def _stream(stream):
-    return (stream if stream is not None else torch.cuda.current_stream()).cuda_stream
-
-
-def _gpu(**tensors):
-    for name, t in tensors.items():
-        if t is not None and not t.is_cuda:
-            raise ValueError(f"{name} must be a GPU tensor (no CPU path exists)")
-
-
-def _io(t: torch.Tensor) -> int:
-    if t.dtype not in _IO:
-        raise TypeError(f"expected float32 or bfloat16, got {t.dtype}")
-    return _IO[t.dtype]
-
-
-def _heads3(name, t, N, D, dtype):
+def _heads3(name, shape, stride, dtype, N, D, want):
     """Checks a [tokens, heads, D] tensor whose last dimension is contiguous."""
-    if t.dim() != 3 or t.shape[0] != N or t.shape[2] != D:
-        raise ValueError(f"{name} must have shape ({N}, heads, {D}), got {tuple(t.shape)}")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}")
-    if t.stride(2) != 1 and D > 1:
+    if len(shape) != 3 or shape[0] != N or shape[2] != D:
+        raise ValueError(f"{name} must have shape ({N}, heads, {D}), got {tuple(shape)}")
+    if dtype != want:
+        raise TypeError(f"{name} must be {want}")
+    if D > 1 and stride[2] != 1:
         raise ValueError(f"{name}'s last dimension must be contiguous")
 
 
 def _int32(name, t, shape):
-    if t.dtype != torch.int32 or tuple(t.shape) != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous int32 tensor of shape {shape}")
+    if t.dtype != torch.int32 or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 tensor of shape {tuple(shape)}")
 
 
 def _full(name, t, shape, dtype):
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}")
@@ -64,35 +72,89 @@ def _full(name, t, shape, dtype):
         raise ValueError(f"{name} must be contiguous")
 
 
-def _attention_desc(q, k, v, cu_seqlens, window, scale, kv_heads) -> AttentionDesc:
-    if q.dim() != 3:
-        raise ValueError(f"q must have shape (tokens, heads, D), got {tuple(q.shape)}")
-    N, H, D = q.shape
-    _heads3("q", q, N, D, q.dtype)
-    io = _io(q)
+def _size(fn, desc):
+    """Workspace bytes, 0 for a descriptor that the call itself will refuse."""
+    n = getattr(_lib.load(), fn)(ctypes.byref(desc))
+    return 0 if n == _BAD else n
+
+
+def _layout(t):
+    return None if t is None else (t.shape, t.stride(), t.dtype)
+
+
+# Descriptors and workspace sizes by shapes, strides and types alone, so that a
+# step of a serving loop builds and checks them once.
+@lru_cache(maxsize=512)
+def _attention_desc(q, k, v, cu, window, scale, kv_heads):
+    shape, stride, dtype = q
+    if len(shape) != 3:
+        raise ValueError(f"q must have shape (tokens, heads, D), got {tuple(shape)}")
+    N, H, D = shape
+    if dtype not in _IO:
+        raise TypeError(f"expected float32 or bfloat16, got {dtype}")
+    _heads3("q", *q, N, D, dtype)
+    ks = vs = (0, 0)
     if k is not None:
-        _heads3("k", k, N, D, q.dtype)
-        _heads3("v", v, N, D, q.dtype)
-        if k.shape[1] != kv_heads or v.shape[1] != kv_heads:
-            raise ValueError("k and v must have the same heads")
-    if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
-        raise ValueError("cu_seqlens must have shape (sequences + 1,)")
-    _int32("cu_seqlens", cu_seqlens, (cu_seqlens.shape[0],))
+        _heads3("k", *k, N, D, dtype)
+        _heads3("v", *v, N, D, dtype)
+        if kv_heads is None:
+            kv_heads = k[0][1]
+        if k[0][1] != kv_heads or v[0][1] != kv_heads:
+            raise ValueError(f"k and v must both have {kv_heads} heads")
+        ks, vs = k[1], v[1]
+    if len(cu[0]) != 1 or cu[0][0] < 1 or cu[2] != torch.int32 or (cu[0][0] > 1 and cu[1][0] != 1):
+        raise ValueError("cu_seqlens must be a contiguous int32 tensor of shape (sequences + 1,)")
     if scale is None:
         scale = D ** -0.5 if D else 1.0
-    s = (0, 0) if k is None else k.stride()
-    t = (0, 0) if v is None else v.stride()
-    return AttentionDesc(io, window, N, cu_seqlens.shape[0] - 1, H, kv_heads, D, scale, 0, q.stride(0), q.stride(1),
-                         s[0], s[1], t[0], t[1])
+    return AttentionDesc(_IO[dtype], window, N, cu[0][0] - 1, H, kv_heads, D, scale, 0, stride[0], stride[1],
+                         ks[0], ks[1], vs[0], vs[1])
 
 
-def _workspace(fn, desc, workspace, device):
-    n = getattr(_lib.load(), fn)(ctypes.byref(desc))
-    if n == _BAD:
-        return None, 0  # the call itself names the reason
+@lru_cache(maxsize=512)
+def _attention_plan(q, k, v, cu, window, scale):
+    d = _attention_desc(q, k, v, cu, window, scale, None)
+    return (d, ctypes.byref(d), _size("e2ttt_attention_workspace_size", d),
+            _size("e2ttt_attention_backward_workspace_size", d))
+
+
+@lru_cache(maxsize=512)
+def _paged_plan(q, k, v, kc, vc, table, cu, window, scale):
+    if len(kc[0]) != 4 or kc[0] != vc[0]:
+        raise ValueError("k_cache and v_cache must share one shape (pages, K, page_size, D)")
+    P, K, ps, D = kc[0]
+    if kc[2] != q[2] or vc[2] != q[2]:
+        raise TypeError(f"k_cache and v_cache must be {q[2]}")
+    a = _attention_desc(q, k, v, cu, window, scale, K)
+    if a.D != D or (D > 1 and (kc[1][3] != 1 or vc[1][3] != 1)):
+        raise ValueError(f"k_cache and v_cache must have a contiguous last dimension of {a.D}")
+    if len(table[0]) != 2:
+        raise ValueError("table must have shape (sequences, width)")
+    s, t = kc[1], vc[1]
+    d = PagedDesc(a, P, ps, table[0][1], s[0], s[1], s[2], t[0], t[1], t[2])
+    return d, ctypes.byref(d), _size("e2ttt_paged_workspace_size", d)
+
+
+@lru_cache(maxsize=512)
+def _norm_plan(shape, dtype, eps, bits8):
+    if len(shape) < 1:
+        raise ValueError("x must have shape (..., width)")
+    if dtype not in _IO:
+        raise TypeError(f"expected float32 or bfloat16, got {dtype}")
+    rows = 1
+    for n in shape[:-1]:
+        rows *= n
+    d = NormDesc(_IO[dtype], int(bits8), rows, shape[-1], eps, 0)
+    return d, ctypes.byref(d), shape[:-1], _size("e2ttt_norm_backward_workspace_size", d)
+
+
+def _workspace(workspace, n, like):
     if workspace is None:
-        workspace = torch.empty(n, dtype=torch.uint8, device=device) if n else None
-    return workspace, (0 if workspace is None else workspace.numel())
+        if n == 0:
+            return None, 0
+        workspace = torch.empty(n, dtype=torch.uint8, device=like.device)
+    elif workspace.get_device() != like.get_device():
+        raise ValueError("workspace must be a GPU tensor on the same device as the others")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def attention_forward(q, k, v, cu_seqlens, *, window: int = 0, scale: float | None = None, out=None, lse=None,
@@ -107,22 +169,20 @@ def attention_forward(q, k, v, cu_seqlens, *, window: int = 0, scale: float | No
     default.  out: [N, H, D]; lse: [N, H] float32, the log of each row's
     softmax sum, which the backward needs.
     """
-    _gpu(q=q, k=k, v=v, cu_seqlens=cu_seqlens, out=out, lse=lse)
-    desc = _attention_desc(q, k, v, cu_seqlens, window, scale, k.shape[1] if k.dim() == 3 else 0)
-    N, H, D = q.shape
+    dev = _device(q, k=k, v=v, cu_seqlens=cu_seqlens, out=out, lse=lse)
+    _, desc, need, _ = _attention_plan(_layout(q), _layout(k), _layout(v), _layout(cu_seqlens), window, scale)
+    shape = q.shape
     if out is None:
-        out = torch.empty(N, H, D, dtype=q.dtype, device=q.device)
+        out = torch.empty(shape, dtype=q.dtype, device=q.device)
     else:
-        _full("out", out, (N, H, D), q.dtype)
+        _full("out", out, shape, q.dtype)
     if lse is None:
-        lse = torch.empty(N, H, dtype=torch.float32, device=q.device)
+        lse = torch.empty(shape[:2], dtype=torch.float32, device=q.device)
     else:
-        _full("lse", lse, (N, H), torch.float32)
-    ws, n = _workspace("e2ttt_attention_workspace_size", desc, workspace, q.device)
-    st = _lib.load().e2ttt_attention_forward(ctypes.byref(desc), _p(q), _p(k), _p(v), _p(cu_seqlens), _p(out),
-                                             _p(lse), _p(ws), n, _stream(stream))
-    if st != 0:
-        raise E2TTTError("e2ttt_attention_forward", st)
+        _full("lse", lse, shape[:2], torch.float32)
+    ws, n = _workspace(workspace, need, q)
+    _call("e2ttt_attention_forward", dev, stream, desc, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+          cu_seqlens.data_ptr(), out.data_ptr(), lse.data_ptr(), ws, n)
     return out, lse
 
 
@@ -130,19 +190,17 @@ def attention_backward(q, k, v, out, lse, dout, cu_seqlens, *, window: int = 0, 
                        workspace=None, stream=None):
     """Gradients of <dout, out> through ``attention_forward``, from its inputs
     and outputs; returns a dict with keys q, k, v (the I/O dtype, contiguous)."""
-    _gpu(q=q, k=k, v=v, out=out, lse=lse, dout=dout, cu_seqlens=cu_seqlens)
-    desc = _attention_desc(q, k, v, cu_seqlens, window, scale, k.shape[1] if k.dim() == 3 else 0)
-    N, H, D = q.shape
-    _full("out", out, (N, H, D), q.dtype)
-    _full("dout", dout, (N, H, D), q.dtype)
-    _full("lse", lse, (N, H), torch.float32)
+    dev = _device(q, k=k, v=v, out=out, lse=lse, dout=dout, cu_seqlens=cu_seqlens)
+    _, desc, _, need = _attention_plan(_layout(q), _layout(k), _layout(v), _layout(cu_seqlens), window, scale)
+    shape = q.shape
+    _full("out", out, shape, q.dtype)
+    _full("dout", dout, shape, q.dtype)
+    _full("lse", lse, shape[:2], torch.float32)
     g = {n: torch.empty(t.shape, dtype=q.dtype, device=q.device) for n, t in (("q", q), ("k", k), ("v", v))}
-    ws, n = _workspace("e2ttt_attention_backward_workspace_size", desc, workspace, q.device)
-    st = _lib.load().e2ttt_attention_backward(ctypes.byref(desc), _p(q), _p(k), _p(v), _p(out), _p(lse), _p(dout),
-                                              _p(cu_seqlens), _p(g["q"]), _p(g["k"]), _p(g["v"]), _p(ws), n,
-                                              _stream(stream))
-    if st != 0:
-        raise E2TTTError("e2ttt_attention_backward", st)
+    ws, n = _workspace(workspace, need, q)
+    _call("e2ttt_attention_backward", dev, stream, desc, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
+          lse.data_ptr(), dout.data_ptr(), cu_seqlens.data_ptr(), g["q"].data_ptr(), g["k"].data_ptr(),
+          g["v"].data_ptr(), ws, n)
     return g
 
 
@@ -183,41 +241,21 @@ def paged_attention(q, k, v, k_cache, v_cache, table, cu_seqlens, cached, *, win
     """
     if (k is None) != (v is None):
         raise ValueError("k and v must both be given, or neither")
-    _gpu(q=q, k=k, v=v, k_cache=k_cache, v_cache=v_cache, table=table, cu_seqlens=cu_seqlens, cached=cached, out=out)
-    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape:
-        raise ValueError("k_cache and v_cache must share one shape (pages, K, page_size, D)")
-    P, K, ps, Dc = k_cache.shape
-    if k_cache.dtype != q.dtype or v_cache.dtype != q.dtype:
-        raise TypeError(f"k_cache and v_cache must be {q.dtype}")
-    a = _attention_desc(q, k, v, cu_seqlens, window, scale, K)
-    N, H, D = q.shape
-    if Dc != D or (D > 1 and (k_cache.stride(3) != 1 or v_cache.stride(3) != 1)):
-        raise ValueError(f"k_cache and v_cache must have a contiguous last dimension of {D}")
+    dev = _device(q, k=k, v=v, k_cache=k_cache, v_cache=v_cache, table=table, cu_seqlens=cu_seqlens, cached=cached,
+                  out=out)
+    _, desc, need = _paged_plan(_layout(q), _layout(k), _layout(v), _layout(k_cache), _layout(v_cache), _layout(table),
+                                _layout(cu_seqlens), window, scale)
     S = cu_seqlens.shape[0] - 1
-    if table.dim() != 2:
-        raise ValueError("table must have shape (sequences, width)")
     _int32("table", table, (S, table.shape[1]))
     _int32("cached", cached, (S,))
     if out is None:
-        out = torch.empty(N, H, D, dtype=q.dtype, device=q.device)
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
     else:
-        _full("out", out, (N, H, D), q.dtype)
-    s, t = k_cache.stride(), v_cache.stride()
-    desc = PagedDesc(a, P, ps, table.shape[1], s[0], s[1], s[2], t[0], t[1], t[2])
-    ws, n = _workspace("e2ttt_paged_workspace_size", desc, workspace, q.device)
-    st = _lib.load().e2ttt_paged_attention(ctypes.byref(desc), _p(q), _p(k), _p(v), _p(k_cache), _p(v_cache),
-                                           _p(table), _p(cu_seqlens), _p(cached), _p(out), _p(ws), n, _stream(stream))
-    if st != 0:
-        raise E2TTTError("e2ttt_paged_attention", st)
+        _full("out", out, q.shape, q.dtype)
+    ws, n = _workspace(workspace, need, q)
+    _call("e2ttt_paged_attention", dev, stream, desc, q.data_ptr(), _p(k), _p(v), k_cache.data_ptr(),
+          v_cache.data_ptr(), table.data_ptr(), cu_seqlens.data_ptr(), cached.data_ptr(), out.data_ptr(), ws, n)
     return out
-
-
-def _norm_desc(x, weight, eps, bits8) -> NormDesc:
-    if x.dim() < 1 or not x.is_contiguous():
-        raise ValueError("x must be contiguous, [..., width]")
-    W = x.shape[-1]
-    _full("weight", weight, (W,), torch.float32)
-    return NormDesc(_io(x), int(bits8), x.numel() // W if W else 0, W, eps, 0)
 
 
 def norm_forward(x, weight, *, residual=None, eps: float = 1e-6, bits8: bool = False, h=None, stream=None):
@@ -226,12 +264,15 @@ def norm_forward(x, weight, *, residual=None, eps: float = 1e-6, bits8: bool = F
 
     x: [..., W] float32 or bfloat16, contiguous; weight: [W] float32.
     h = x + residual in x's type (x itself without ``residual``; ``h=residual``
-    updates the stream in place); rstd: [...] float32, for the backward.
-    y = h * rstd * weight in x's type, or with ``bits8`` in float8_e4m3fn, to be
+    updates the stream in place); rstd: [...] float32, for the backward (None
+    with ``bits8``, which has none).  y = h * rstd * weight in x's type, or with ``bits8`` in float8_e4m3fn, to be
     multiplied by scale [...] (float32, max|y| / 448 of its row; else None).
     """
-    _gpu(x=x, weight=weight, residual=residual, h=h)
-    desc = _norm_desc(x, weight, eps, bits8)
+    dev = _device(x, weight=weight, residual=residual, h=h)
+    _, desc, lead, _ = _norm_plan(x.shape, x.dtype, eps, bits8)
+    if not x.is_contiguous():
+        raise ValueError("x must be contiguous")
+    _full("weight", weight, x.shape[-1:], torch.float32)
     if residual is not None:
         _full("residual", residual, x.shape, x.dtype)
         if h is None:
@@ -240,13 +281,15 @@ def norm_forward(x, weight, *, residual=None, eps: float = 1e-6, bits8: bool = F
             _full("h", h, x.shape, x.dtype)
     elif h is not None:
         raise ValueError("h is an output of the residual's addition: give residual too")
-    y = torch.empty(x.shape, dtype=F8 if bits8 else x.dtype, device=x.device)
-    scale = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device) if bits8 else None
-    rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
-    st = _lib.load().e2ttt_norm_forward(ctypes.byref(desc), _p(x), _p(residual), _p(weight), _p(y), _p(scale), _p(h),
-                                        _p(rstd), _stream(stream))
-    if st != 0:
-        raise E2TTTError("e2ttt_norm_forward", st)
+    scale = rstd = None
+    if bits8:
+        y = torch.empty_like(x, dtype=F8)
+        scale = torch.empty(lead, dtype=torch.float32, device=x.device)
+    else:
+        y = torch.empty_like(x)
+        rstd = torch.empty(lead, dtype=torch.float32, device=x.device)
+    _call("e2ttt_norm_forward", dev, stream, desc, x.data_ptr(), _p(residual), weight.data_ptr(), y.data_ptr(),
+          _p(scale), _p(h), _p(rstd))
     return y, scale, (x if residual is None else h), rstd
 
 
@@ -254,19 +297,19 @@ def norm_backward(dy, h, weight, rstd, *, dh=None, workspace=None, stream=None):
     """Gradients through ``norm_forward`` (y in the stream's type): returns
     (dx, dweight).  dx is the gradient of both x and residual; ``dh`` is what
     arrives at h along the residual stream, added to it."""
-    _gpu(dy=dy, h=h, weight=weight, rstd=rstd, dh=dh)
-    desc = _norm_desc(h, weight, 0.0, False)
+    dev = _device(h, dy=dy, weight=weight, rstd=rstd, dh=dh)
+    _, desc, lead, need = _norm_plan(h.shape, h.dtype, 0.0, False)
+    _full("h", h, h.shape, h.dtype)
+    _full("weight", weight, h.shape[-1:], torch.float32)
     _full("dy", dy, h.shape, h.dtype)
-    _full("rstd", rstd, h.shape[:-1], torch.float32)
+    _full("rstd", rstd, lead, torch.float32)
     if dh is not None:
         _full("dh", dh, h.shape, h.dtype)
     dx = torch.empty_like(h)
     dweight = torch.empty_like(weight)
-    ws, n = _workspace("e2ttt_norm_backward_workspace_size", desc, workspace, h.device)
-    st = _lib.load().e2ttt_norm_backward(ctypes.byref(desc), _p(dy), _p(h), _p(weight), _p(rstd), _p(dh), _p(dx),
-                                         _p(dweight), _p(ws), n, _stream(stream))
-    if st != 0:
-        raise E2TTTError("e2ttt_norm_backward", st)
+    ws, n = _workspace(workspace, need, h)
+    _call("e2ttt_norm_backward", dev, stream, desc, dy.data_ptr(), h.data_ptr(), weight.data_ptr(), rstd.data_ptr(),
+          _p(dh), dx.data_ptr(), dweight.data_ptr(), ws, n)
     return dx, dweight
 
 
