@@ -62,8 +62,8 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(AttnBwdArgs a) {
     const int g = lane >> 5, col = lane & 31, G = a.G;
     const int kvh = blockIdx.x % a.K, t = blockIdx.x / a.K;
     Item it;
-    if (!find_item(a.cu, a.S, (int)a.N, t, [&](int, int n) { return (int)(((int64_t)n * G + BM - 1) / BM); }, it)) return;
-    const int r0 = (it.tiles - 1 - it.tile) * BM;
+    if (!find_item(a.cu, a.S, (int)a.N, t, row_cap(a.window, G, BM), [&](int n) { return (n * G + BM - 1) / BM; }, it)) return;
+    const int r0 = it.tile * BM;
     const int rows = it.n * G;
     const int first = div_group(r0, G, a.gmagic);
     const int last = div_group(r0 + BM < rows ? r0 + BM - 1 : rows - 1, G, a.gmagic);
@@ -126,12 +126,7 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(AttnBwdArgs a) {
             copy16(vr, dst + TILE + 1024 * i, voff[i]);
         }
     };
-    unsigned tro[DT][2];
-#pragma unroll
-    for (int dt = 0; dt < DT; ++dt) {
-        tro[dt][0] = tr_offset<DP>(dt, 0, lane);
-        tro[dt][1] = tr_offset<DP>(dt, 1, lane);
-    }
+    const unsigned rb0 = row_base<DP>(col, g), tb0 = tr_base<DP>(lane);
 
     f32x16 acc[DT] = {};
     const int wr0 = r0 + 32 * wave;
@@ -147,15 +142,16 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(AttnBwdArgs a) {
         if (j + 1 < nb) copy_tile(j + 1, stage ^ 1);
         const int p0 = lo + j * BN;
         if (!wlive || p0 > wlast || (a.window > 0 && p0 + BN - 1 <= wfirst - a.window)) continue;
-        const unsigned char *kt = lds[stage][0], *vt = lds[stage][1];
+        const unsigned char *kt = lds[0][0], *vt = lds[0][1];
+        const unsigned rb = rb0 + stage * (2 * TILE), tb = tb0 + stage * (2 * TILE);
         const bool edge = p0 + BN - 1 > wfirst || (a.window > 0 && p0 <= wlast - a.window) || wr0 + 32 > rows;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             f32x16 sc = {}, dp = {};
 #pragma unroll
             for (int s = 0; s < KS; ++s) {
-                sc = mfma32(row_frag<DP>(kt, 32 * h + col, s, g), qf[s], sc);
-                dp = mfma32(row_frag<DP>(vt, 32 * h + col, s, g), df[s], dp);
+                sc = mfma32(row_frag(kt + h * (64 * DP), rb, s), qf[s], sc);
+                dp = mfma32(row_frag(vt + h * (64 * DP), rb, s), df[s], dp);
             }
 #pragma unroll
             for (int i = 0; i < 16; ++i)
@@ -172,41 +168,46 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(AttnBwdArgs a) {
                 const bf16x8 sf = pack_half(sc, s);
 #pragma unroll
                 for (int dt = 0; dt < DT; ++dt)
-                    acc[dt] = mfma32(tr_frag(kt + (2 * h + s) * (32 * DP), tro[dt][0], tro[dt][1]), sf, acc[dt]);
+                    acc[dt] = mfma32(tr_frag<DP>(kt + (2 * h + s) * (32 * DP), tb, dt), sf, acc[dt]);
             }
         }
     }
     if (live) store_row<DT>((__bf16*)a.dq + at * a.D, acc, a.scale, g, a.D);
 }
 
+// 64 keys per workgroup, 2 waves of 32, over tiles of 32 rows: four workgroups
+// share a compute unit, and there are enough of them that the causal shape's
+// uneven work levels out.
+constexpr int BK = 64;
+constexpr int BR = 32;
+
 template <int DP>
-__global__ __launch_bounds__(256, 2) void attn_dkdv_kernel(AttnBwdArgs a) {
-    constexpr int TILE = BN * DP * 2;
+__global__ __launch_bounds__(128, 2) void attn_dkdv_kernel(AttnBwdArgs a) {
+    constexpr int TILE = BR * DP * 2;
     constexpr int KS = DP / 16, DT = DP / 32;
-    using P = CopyPlan<DP>;
+    constexpr int RPI = 512 / DP, NI = BR / 2 / RPI, CH = DP / 8;  // copy instructions per wave and tensor
     __shared__ __attribute__((aligned(1024))) unsigned char lds[2][2][TILE];  // [stage][Q, dout]
-    __shared__ __attribute__((aligned(256))) float stat[2][2][BN];            // [stage][lse, delta]
+    __shared__ __attribute__((aligned(256))) float stat[2][2][BR];            // [stage][lse, delta]
 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int g = lane >> 5, col = lane & 31, G = a.G;
     const int kvh = blockIdx.x % a.K, t = blockIdx.x / a.K;
     Item it;
-    // key blocks in order: the first of a sequence has the most rows
-    if (!find_item(a.cu, a.S, (int)a.N, t, [&](int, int n) { return (n + BM - 1) / BM; }, it)) return;
-    const int k0 = it.tile * BM;
+    if (!find_item(a.cu, a.S, (int)a.N, t, row_cap(a.window, 1, BK), [&](int n) { return (n + BK - 1) / BK; }, it)) return;
+    const int k0 = (it.tiles - 1 - it.tile) * BK;  // the first keys of a sequence have the most rows
     const int rows = it.n * G;
-    const int klast = k0 + BM < it.n ? k0 + BM - 1 : it.n - 1;
-    const int rbeg = (k0 * G) & ~(BN - 1);
-    int64_t re = a.window > 0 ? ((int64_t)klast + a.window) * G : rows;
+    const int klast = k0 + BK < it.n ? k0 + BK - 1 : it.n - 1;
+    const int rbeg = k0 * G / BR * BR;
+    const int64_t re = a.window > 0 ? ((int64_t)klast + a.window) * G : rows;
     const int rend = re < rows ? (int)re : rows;  // rows that see some key of the block: [k0 G, rend)
-    const int nb = (rend - rbeg + BN - 1) / BN;
+    const int nb = (rend - rbeg + BR - 1) / BR;
 
     const int key = k0 + 32 * wave + col;
     const bool live = key < it.n;
     const int64_t ktok = it.tok0 + (live ? key : 0);
     // rows that see this lane's key: [rlo, rhi)
     const int rlo = live ? key * G : 0x7fffffff;
-    int64_t rh = a.window > 0 ? ((int64_t)key + a.window) * G : rows;
+    const int64_t rh = a.window > 0 ? ((int64_t)key + a.window) * G : rows;
     const int rhi = rh < rows ? (int)rh : rows;
 
     bf16x8 kf[KS], vf[KS];
@@ -223,44 +224,74 @@ __global__ __launch_bounds__(256, 2) void attn_dkdv_kernel(AttnBwdArgs a) {
         }
     }
 
-    const int crow = lane / P::CH, cpc = lane % P::CH;
-    const unsigned base = lds_addr(&lds[0][0][0]) + wave * (TILE / 4);
+    const int crow = lane / CH, cpc = lane % CH;
+    const unsigned base = lds_addr(&lds[0][0][0]) + wave * (TILE / 2);
     const unsigned sbase = lds_addr(&stat[0][0][0]);
     const char* qsrc = (const char*)a.q + 2 * (it.tok0 * a.q_tok + (int64_t)kvh * G * a.q_head);
     const int64_t first_row = (int64_t)it.tok0 * a.H + kvh * G;  // row 0 in [N][H] order
     const char* dsrc = (const char*)a.dout + 2 * first_row * a.D;
+    // A group whose size divides the tile starts every tile on a token: a
+    // lane's offsets are the same in all of them, and only the base moves.
+    // Otherwise they come anew from the row number.
+    const bool steady = BR % G == 0 && a.q_head < (1 << 23) / G;
+    unsigned qoff[NI], doff[NI];
+    int64_t toff = 0;
+    {
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+            const int rr = BR / 2 * wave + RPI * i + crow, tk = div_group(rr, G, a.gmagic), hg = rr - tk * G;
+            const int c = cpc ^ swz<DP>(rr);
+            const bool in = 8 * c < a.D && steady;
+            qoff[i] = in ? (unsigned)(2 * (tk * a.q_tok + hg * a.q_head) + 16 * c) : kOutside;
+            doff[i] = in ? (unsigned)(2 * (tk * a.H + hg) * a.D + 16 * c) : kOutside;
+        }
+        const int rr = lane & (BR - 1), tk = div_group(rr, G, a.gmagic);
+        toff = (int64_t)tk * a.H + rr - tk * G;
+    }
     auto copy_tile = [&](int j, int stage) {
         const unsigned dst = base + stage * (2 * TILE);
+        const int t0 = rbeg + j * BR;
+        if (steady) {
+            const int64_t tk = div_group(t0, G, a.gmagic);
+            const u32x4 qr = buffer_rsrc(qsrc + 2 * tk * a.q_tok, (int)kOutside);
+            const u32x4 dr = buffer_rsrc(dsrc + 2 * tk * a.H * a.D, (int)kOutside);
 #pragma unroll
-        for (int i = 0; i < P::NI; ++i) {
-            const int rr = 16 * wave + P::RPI * i + crow;
-            const int r = rbeg + j * BN + rr;
-            const int c = cpc ^ swz<DP>(rr);
-            const char *qp = (const char*)zeros, *dp = (const char*)zeros;
-            if (8 * c < a.D && r < rows) {
-                const int tk = div_group(r, G, a.gmagic), hg = r - tk * G;
-                qp = qsrc + 2 * (tk * a.q_tok + hg * a.q_head) + 16 * c;
-                dp = dsrc + 2 * (int64_t)(tk * a.H + hg) * a.D + 16 * c;
+            for (int i = 0; i < NI; ++i) {
+                const bool in = t0 + BR / 2 * wave + RPI * i + crow < rows;
+                copy16(qr, dst + 1024 * i, in ? qoff[i] : kOutside);
+                copy16(dr, dst + TILE + 1024 * i, in ? doff[i] : kOutside);
             }
-            copy16_at(qp, dst + 1024 * i);
-            copy16_at(dp, dst + TILE + 1024 * i);
+        } else {
+#pragma unroll
+            for (int i = 0; i < NI; ++i) {
+                const int rr = BR / 2 * wave + RPI * i + crow;
+                const int r = t0 + rr, c = cpc ^ swz<DP>(rr);
+                const char *qp = (const char*)zeros, *dp = (const char*)zeros;
+                if (8 * c < a.D && r < rows) {
+                    const int tk = div_group(r, G, a.gmagic), hg = r - tk * G;
+                    qp = qsrc + 2 * (tk * a.q_tok + hg * a.q_head) + 16 * c;
+                    dp = dsrc + 2 * ((int64_t)tk * a.H + hg) * a.D + 16 * c;
+                }
+                copy16_at(qp, dst + 1024 * i);
+                copy16_at(dp, dst + TILE + 1024 * i);
+            }
         }
-        if (wave < 2) {  // wave 0: lse, wave 1: delta, of the tile's 64 rows
-            const int r = rbeg + j * BN + lane;
-            const int tk = r < rows ? div_group(r, G, a.gmagic) : 0, hg = r < rows ? r - tk * G : 0;
-            const float* src = wave == 0 ? a.lse : a.delta;
-            copy4_at(src + first_row + (int64_t)tk * a.H + hg, sbase + stage * (2 * BN * 4) + wave * (BN * 4));
+        if (wave == 0) {  // lanes 0..31 the lse, 32..63 the delta of the tile's rows
+            const int r = t0 + (lane & (BR - 1));
+            int64_t at = toff;
+            if (steady) {
+                at += (int64_t)div_group(t0, G, a.gmagic) * a.H;
+            } else {
+                const int tk = div_group(r, G, a.gmagic);
+                at = (int64_t)tk * a.H + r - tk * G;
+            }
+            copy4_at((lane < BR ? a.lse : a.delta) + first_row + (r < rows ? at : 0), sbase + stage * (2 * BR * 4));
         }
     };
-    unsigned tro[DT][2];
-#pragma unroll
-    for (int dt = 0; dt < DT; ++dt) {
-        tro[dt][0] = tr_offset<DP>(dt, 0, lane);
-        tro[dt][1] = tr_offset<DP>(dt, 1, lane);
-    }
+    const unsigned rb0 = row_base<DP>(col, g), tb0 = tr_base<DP>(lane);
 
     f32x16 dk[DT] = {}, dv[DT] = {};
-    const int wk0 = k0 + 32 * wave;                                        // this wave's keys
+    const int wk0 = k0 + 32 * wave;  // this wave's keys
     const int wklast = wk0 + 31;
     const bool wlive = wk0 < it.n;
 
@@ -270,49 +301,47 @@ __global__ __launch_bounds__(256, 2) void attn_dkdv_kernel(AttnBwdArgs a) {
         wait_vm<0>();
         barrier_lds();
         if (j + 1 < nb) copy_tile(j + 1, stage ^ 1);
-        const int p0 = rbeg + j * BN;
-        if (!wlive || p0 + BN - 1 < wk0 * G) continue;
-        const unsigned char *qt = lds[stage][0], *dt_ = lds[stage][1];
-        const bool edge = p0 < wklast * G || p0 + BN > rows || wklast >= it.n ||
-                          (a.window > 0 && p0 + BN > ((int64_t)wk0 + a.window) * G);
+        const int p0 = rbeg + j * BR;
+        if (!wlive || p0 + BR - 1 < wk0 * G) continue;
+        const unsigned char *qt = lds[0][0], *ot = lds[0][1];
+        const unsigned rb = rb0 + stage * (2 * TILE), tb = tb0 + stage * (2 * TILE);
+        const bool edge = p0 < wklast * G || p0 + BR > rows || wklast >= it.n ||
+                          (a.window > 0 && p0 + BR > ((int64_t)wk0 + a.window) * G);
+        f32x16 sc = {}, dp = {};
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            f32x16 sc = {}, dp = {};
+        for (int s = 0; s < KS; ++s) {
+            sc = mfma32(row_frag(qt, rb, s), kf[s], sc);
+            dp = mfma32(row_frag(ot, rb, s), vf[s], dp);
+        }
 #pragma unroll
-            for (int s = 0; s < KS; ++s) {
-                sc = mfma32(row_frag<DP>(qt, 32 * h + col, s, g), kf[s], sc);
-                dp = mfma32(row_frag<DP>(dt_, 32 * h + col, s, g), vf[s], dp);
+        for (int b = 0; b < 4; ++b) {
+            const f32x4 ls = *(const f32x4*)&stat[stage][0][8 * b + 4 * g];
+            const f32x4 de = *(const f32x4*)&stat[stage][1][8 * b + 4 * g];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int i = 4 * b + e;
+                sc[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[i], a.sl2, -ls[e] * kLog2e));
+                dp[i] = sc[i] * (dp[i] - de[e]);
             }
+        }
+        if (edge) {
 #pragma unroll
-            for (int b = 0; b < 4; ++b) {
-                const f32x4 ls = *(const f32x4*)&stat[stage][0][32 * h + 8 * b + 4 * g];
-                const f32x4 de = *(const f32x4*)&stat[stage][1][32 * h + 8 * b + 4 * g];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int i = 4 * b + e;
-                    sc[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[i], a.sl2, -ls[e] * kLog2e));
-                    dp[i] = sc[i] * (dp[i] - de[e]);
+            for (int i = 0; i < 16; ++i) {
+                const int r = p0 + acc_row(i, g);
+                if (r < rlo || r >= rhi) {
+                    sc[i] = 0.f;
+                    dp[i] = 0.f;
                 }
             }
-            if (edge) {
+        }
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const int r = p0 + 32 * h + acc_row(i, g);
-                    if (r < rlo || r >= rhi) {
-                        sc[i] = 0.f;
-                        dp[i] = 0.f;
-                    }
-                }
-            }
+        for (int s = 0; s < 2; ++s) {
+            const bf16x8 pf = pack_half(sc, s), sf = pack_half(dp, s);
+            const unsigned o = s * (32 * DP);
 #pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                const bf16x8 pf = pack_half(sc, s), sf = pack_half(dp, s);
-                const unsigned o = (2 * h + s) * (32 * DP);
-#pragma unroll
-                for (int dt = 0; dt < DT; ++dt) {
-                    dv[dt] = mfma32(tr_frag(dt_ + o, tro[dt][0], tro[dt][1]), pf, dv[dt]);
-                    dk[dt] = mfma32(tr_frag(qt + o, tro[dt][0], tro[dt][1]), sf, dk[dt]);
-                }
+            for (int dt = 0; dt < DT; ++dt) {
+                dv[dt] = mfma32(tr_frag<DP>(ot + o, tb, dt), pf, dv[dt]);
+                dk[dt] = mfma32(tr_frag<DP>(qt + o, tb, dt), sf, dk[dt]);
             }
         }
     }
@@ -324,12 +353,12 @@ __global__ __launch_bounds__(256, 2) void attn_dkdv_kernel(AttnBwdArgs a) {
 
 template <int DP>
 hipError_t launch(const AttnBwdArgs& a, hipStream_t s) {
-    const int64_t dq_grid = (a.N * a.G / BM + a.S) * a.K, dkv_grid = (a.N / BM + a.S) * a.K;
+    const int64_t dq_grid = (a.N * a.G / BM + a.S) * a.K, dkv_grid = (a.N / BK + a.S) * a.K;
     if (dq_grid > 0x7fffffff) return hipErrorInvalidValue;
     attn_dq_kernel<DP><<<dim3((unsigned)dq_grid), dim3(256), 0, s>>>(a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    attn_dkdv_kernel<DP><<<dim3((unsigned)dkv_grid), dim3(256), 0, s>>>(a);
+    attn_dkdv_kernel<DP><<<dim3((unsigned)dkv_grid), dim3(128), 0, s>>>(a);
     return hipGetLastError();
 }
 

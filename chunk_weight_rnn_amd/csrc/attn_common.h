@@ -47,47 +47,98 @@ __device__ __forceinline__ int div_group(int r, int G, unsigned magic) {
 }
 
 // ------------------------------------------------------------- work items
-// The t-th tile of BM rows, counted over all sequences; a sequence of n tokens
-// has ceil(n G / BM) of them.  Every wave searches for itself, 64 sequences
-// per step, from the offsets in memory (clamped, so that whatever they hold no
-// address leaves the tensors).  False past the last tile.
+// A sequence of n tokens has a number of tiles, of rows or of keys, whose work
+// grows with their index (causal: a later row sees more keys) up to a cap (the
+// window).  The t-th workgroup takes the t-th tile in order of falling work
+// over all sequences, in kClasses steps: a workgroup with much work that starts
+// last would leave the rest of the chip idle.  Every wave searches for itself,
+// from the offsets in memory (clamped, so that whatever they hold no address
+// leaves the tensors); with more than 64 sequences there are many tiles of
+// each kind, and they are taken sequence by sequence.  False past the last tile.
 struct Item {
     int seq, tok0, n;  // sequence, its first token, its length
     int tile, tiles;   // tile within the sequence, tiles of the sequence
 };
+constexpr int kClasses = 16;
 
 __device__ __forceinline__ int clamped(int x, int hi) { return x < 0 ? 0 : (x > hi ? hi : x); }
 
+// Inclusive sum (or maximum, x >= 0) over the lanes up to this one.
+template <bool MAX>
+__device__ __forceinline__ int wave_scan(int x) {
+#define E2TTT_STEP(ctrl, rows)                                                     \
+    {                                                                              \
+        const int y = __builtin_amdgcn_update_dpp(0, x, ctrl, rows, 0xf, false);   \
+        x = MAX ? (x > y ? x : y) : x + y;                                         \
+    }
+    E2TTT_STEP(0x111, 0xf)  // row_shr:1, 2, 4, 8 within 16 lanes
+    E2TTT_STEP(0x112, 0xf)
+    E2TTT_STEP(0x114, 0xf)
+    E2TTT_STEP(0x118, 0xf)
+    E2TTT_STEP(0x142, 0xa)  // row_bcast:15, row_bcast:31
+    E2TTT_STEP(0x143, 0xc)
+#undef E2TTT_STEP
+    return x;
+}
+__device__ __forceinline__ int last_lane(int x) { return __builtin_amdgcn_readlane(x, 63); }
+
+// Tiles of BM rows from which on the window keeps the work the same.
+__device__ __forceinline__ int row_cap(int window, int G, int BM) {
+    const int64_t c = (int64_t)window * G / BM + 1;
+    return window == 0 || c > 0x7fffffff ? 0x7fffffff : (int)c;
+}
+
 template <class F>
-__device__ __forceinline__ bool find_item(const int* __restrict__ cu, int S, int N, int t, F&& tiles_of, Item& it) {
+__device__ __forceinline__ bool find_item(const int* __restrict__ cu, int S, int N, int t, int cap, F&& tiles_of,
+                                          Item& it) {
     const int lane = threadIdx.x & 63;
-    int base = 0;
-    for (int s0 = 0; s0 < S; s0 += 64) {
-        const int s = s0 + lane;
-        int a = 0, n = 0, m = 0;
+    auto load = [&](int s, int& a, int& n, int& m) {
+        a = n = m = 0;
         if (s < S) {
             a = clamped(cu[s], N);
             n = clamped(cu[s + 1], N) - a;
             n = n > 0 ? n : 0;
-            m = tiles_of(s, n);
+            m = tiles_of(n);
         }
-        int incl = m;
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const int y = __shfl_up(incl, d);
-            if (lane >= d) incl += y;
+    };
+    auto take = [&](int s0, int l, int a, int n, int m) {
+        it.seq = s0 + l;
+        it.tok0 = __builtin_amdgcn_readlane(a, l);
+        it.n = __builtin_amdgcn_readlane(n, l);
+        it.tiles = __builtin_amdgcn_readlane(m, l);
+    };
+    int a, n, m;
+    if (S <= 64) {
+        load(lane, a, n, m);
+        const int most = last_lane(wave_scan<true>(m));
+        const int step = ((most < cap ? most : cap) + kClasses - 1) / kClasses;
+        for (int c = kClasses - 1; c >= 0; --c) {
+            const int lo = c * step;
+            int k = m > lo ? m - lo : 0;
+            if (c < kClasses - 1 && k > step) k = step;
+            const int incl = wave_scan<false>(k);
+            const unsigned long long past = __ballot(incl > t);
+            if (past) {
+                const int l = __builtin_ctzll(past);
+                take(0, l, a, n, m);
+                it.tile = lo + __builtin_amdgcn_readlane(incl, l) - 1 - t;
+                return true;
+            }
+            t -= last_lane(incl);
         }
-        const unsigned long long past = __ballot(base + incl > t);
+        return false;
+    }
+    for (int s0 = 0; s0 < S; s0 += 64) {
+        load(s0 + lane, a, n, m);
+        const int incl = wave_scan<false>(m);
+        const unsigned long long past = __ballot(incl > t);
         if (past) {
             const int l = __builtin_ctzll(past);
-            it.seq = s0 + l;
-            it.tok0 = __builtin_amdgcn_readfirstlane(__shfl(a, l));
-            it.n = __builtin_amdgcn_readfirstlane(__shfl(n, l));
-            it.tiles = __builtin_amdgcn_readfirstlane(__shfl(m, l));
-            it.tile = t - base - __builtin_amdgcn_readfirstlane(__shfl(incl, l)) + it.tiles;
+            take(s0, l, a, n, m);
+            it.tile = __builtin_amdgcn_readlane(incl, l) - 1 - t;
             return true;
         }
-        base += __builtin_amdgcn_readfirstlane(__shfl(incl, 63));
+        t -= last_lane(incl);
     }
     return false;
 }
@@ -152,28 +203,36 @@ __device__ __forceinline__ int swz(int t) {
 // 32x32x16 product over it.  Any order does, if both operands follow it.
 __device__ __forceinline__ constexpr int chunk_of(int s, int g) { return ((s >> 1) << 2) | (g << 1) | (s & 1); }
 
-// Row fragment: operand row t, k-step s.
+// Fragments are addressed by one register each, the offset of the stage's tile
+// included, from which every chunk is an exclusive or away: kept per chunk, the
+// addresses would take a dozen registers that the accumulators need.
+//
+// Row fragment, k-step s: operand row t.
 template <int DP>
-__device__ __forceinline__ bf16x8 row_frag(const unsigned char* tile, int t, int s, int g) {
-    return *(const bf16x8*)(tile + t * (2 * DP) + 16 * (chunk_of(s, g) ^ swz<DP>(t)));
+__device__ __forceinline__ unsigned row_base(int t, int g) {
+    return (unsigned)(t * (2 * DP) + 16 * (chunk_of(0, g) ^ swz<DP>(t)));
+}
+__device__ __forceinline__ bf16x8 row_frag(const unsigned char* lds, unsigned rb, int s) {
+    return *(const bf16x8*)(lds + (rb ^ (16 * chunk_of(s, 0))));
 }
 
-// Transpose fragment offsets: operand row = head-dim column 32 dt + lane % 32,
-// operand k 0..3 = tile rows 16 s + 4 (lane / 32) + {0..3} (hi = 0), k 4..7 the
-// same + 8 (hi = 1).  A k-step adds 16 rows, 32 DP bytes, and keeps the
-// swizzle.  This is the row order in which a 32x32 accumulator holds its rows,
-// so an accumulator packed to bf16 is the other operand without any exchange.
+// Transpose fragment dt, 16 tile rows from `lds` on: operand row = head-dim
+// column 32 dt + lane % 32, operand k 0..3 = tile rows 4 (lane / 32) + {0..3},
+// k 4..7 the same + 8.  This is the row order in which a 32x32 accumulator
+// holds its rows, so an accumulator packed to bf16 is the other operand
+// without any exchange.  (Eight rows on flip bit 1 of the swizzle; sixteen rows
+// on keep it.)
 template <int DP>
-__device__ __forceinline__ unsigned tr_offset(int dt, int hi, int lane) {
+__device__ __forceinline__ unsigned tr_base(int lane) {
     const int p = lane & 15, G = lane >> 4;
-    const int r = 4 * (G >> 1) + 8 * hi + (p >> 2);
-    const int chunk = 4 * dt + 2 * (G & 1) + ((p & 3) >> 1);
+    const int r = 4 * (G >> 1) + (p >> 2);
+    const int chunk = 2 * (G & 1) + ((p & 3) >> 1);
     return (unsigned)(r * (2 * DP) + 16 * (chunk ^ swz<DP>(r)) + 8 * (p & 1));
 }
-
-__device__ __forceinline__ bf16x8 tr_frag(const unsigned char* tile, unsigned off0, unsigned off1) {
-    const bf16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_bf16x4_t*)(tile + off0));
-    const bf16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_bf16x4_t*)(tile + off1));
+template <int DP>
+__device__ __forceinline__ bf16x8 tr_frag(const unsigned char* lds, unsigned tb, int dt) {
+    const bf16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_bf16x4_t*)(lds + (tb ^ (64 * dt))));
+    const bf16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_bf16x4_t*)(lds + (tb ^ (64 * dt + 32)) + 16 * DP));
     return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
@@ -247,6 +306,40 @@ __device__ __forceinline__ void barrier_lds() {
     asm volatile("" ::: "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
+}
+
+// ------------------------------------------------------- partial results
+__device__ __forceinline__ float max_or_nan(float x, float y) { return x != x ? x : (y != y ? y : fmaxf(x, y)); }
+__device__ __forceinline__ float wave_max_or_nan(float x) {
+#pragma unroll
+    for (int d = 32; d; d >>= 1) x = max_or_nan(x, __shfl_xor(x, d));
+    return x;
+}
+__device__ __forceinline__ float wave_sum(float x) {
+#pragma unroll
+    for (int d = 32; d; d >>= 1) x += __shfl_xor(x, d);
+    return x;
+}
+
+// Adds n partial rows, two values per lane, with lane i's weight f for row i;
+// eight loads in flight.  Rows of weight 0 saw nothing and hold nothing.
+template <class F>
+__device__ __forceinline__ void join_rows(int n, float f, bool in, F&& row, float& o0, float& o1) {
+    for (int i0 = 0; i0 < n; i0 += 8) {
+        float2 v[8];
+        float w[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            w[e] = i0 + e < n ? __shfl(f, i0 + e) : 0.f;
+            v[e] = float2{0.f, 0.f};
+            if (w[e] != 0.f && in) v[e] = *(const float2*)row(i0 + e);
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            o0 = __builtin_fmaf(w[e], v[e].x, o0);
+            o1 = __builtin_fmaf(w[e], v[e].y, o1);
+        }
+    }
 }
 
 // Blocks that append_block needs (none when nothing is appended).

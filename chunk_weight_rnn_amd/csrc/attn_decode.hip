@@ -53,40 +53,28 @@ __device__ __forceinline__ Seq seq_of(const AttnArgs& a, int s) {
     return q;
 }
 
-__device__ __forceinline__ int scan64(int x, int lane) {
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const int y = __shfl_up(x, d);
-        if (lane >= d) x += y;
-    }
-    return x;
-}
-
-// All units (UNITS) or items of the call.
-template <bool UNITS>
-__device__ __forceinline__ int total_of(const AttnArgs& a, int lane) {
+// All units of the call; q0: the first 64 sequences, a lane each.
+__device__ __forceinline__ int total_units(const AttnArgs& a, const Seq& q0, int lane) {
     int t = 0;
     for (int s0 = 0; s0 < a.S; s0 += 64) {
-        const Seq q = seq_of(a, s0 + lane);
-        t += UNITS ? q.tiles * q.nb * a.K : q.tiles * a.K;
+        const Seq q = s0 == 0 ? q0 : seq_of(a, s0 + lane);
+        t += q.tiles * q.nb * a.K;
     }
-#pragma unroll
-    for (int d = 32; d; d >>= 1) t += __shfl_xor(t, d);
-    return __builtin_amdgcn_readfirstlane(t);
+    return last_lane(wave_scan<false>(t));
 }
 
 // The item that holds unit t of the line (UNITS), or the t-th item.
 template <bool UNITS>
-__device__ __forceinline__ bool find_work(const AttnArgs& a, int t, int lane, Work& w) {
-    int base = 0;
+__device__ __forceinline__ bool find_work(const AttnArgs& a, const Seq& q0, int t, int lane, Work& w) {
+    int base = 0, units = 0;  // of the sequences before this step
     for (int s0 = 0; s0 < a.S; s0 += 64) {
-        const Seq q = seq_of(a, s0 + lane);
-        const int m = UNITS ? q.tiles * q.nb * a.K : q.tiles * a.K;
-        const int incl = scan64(m, lane);
+        const Seq q = s0 == 0 ? q0 : seq_of(a, s0 + lane);
+        const int mu = q.tiles * q.nb * a.K, m = UNITS ? mu : q.tiles * a.K;
+        const int iu = wave_scan<false>(mu), incl = UNITS ? iu : wave_scan<false>(m);
         const unsigned long long past = __ballot(base + incl > t);
         if (past) {
             const int l = __builtin_ctzll(past);
-            auto get = [&](int x) { return __builtin_amdgcn_readfirstlane(__shfl(x, l)); };
+            auto get = [&](int x) { return __builtin_amdgcn_readlane(x, l); };
             w.seq = s0 + l;
             w.tok0 = get(q.tok0);
             w.n = get(q.n);
@@ -98,12 +86,13 @@ __device__ __forceinline__ bool find_work(const AttnArgs& a, int t, int lane, Wo
             const int local = t - first;
             const int item = UNITS ? local / w.nb : local;
             w.block = UNITS ? local - item * w.nb : 0;
-            w.before = UNITS ? first + item * w.nb : 0;
+            w.before = units + get(iu - mu) + item * w.nb;
             w.kvh = item / w.tiles;
             w.rt = item - w.kvh * w.tiles;
             return true;
         }
-        base += __builtin_amdgcn_readfirstlane(__shfl(incl, 63));
+        base += last_lane(incl);
+        units += last_lane(iu);
     }
     return false;
 }
@@ -133,21 +122,17 @@ __global__ __launch_bounds__(256, 1) void attn_decode_kernel(AttnArgs a, int gro
     }
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int g = lane >> 5, col = lane & 31, G = a.G;
+    const Seq q0 = seq_of(a, lane);
     int u, uend;
     if (SPLIT) {
-        const int total = total_of<true>(a, lane), per = share(total, groups);
+        const int total = total_units(a, q0, lane), per = share(total, groups);
         u = blockIdx.x * per < total ? blockIdx.x * per : total;
         uend = u + per < total ? u + per : total;
     } else {
         u = blockIdx.x;
         uend = u + 1;
     }
-    unsigned tro[DT][2];
-#pragma unroll
-    for (int dt = 0; dt < DT; ++dt) {
-        tro[dt][0] = tr_offset<DP>(dt, 0, lane);
-        tro[dt][1] = tr_offset<DP>(dt, 1, lane);
-    }
+    const unsigned rb0 = row_base<DP>(col, g), tb0 = tr_base<DP>(lane);
     const int crow = lane / CH, cpc = lane % CH;
     const unsigned base = lds_addr(&lds[wave][0][0][0]);
     const int mask = (1 << a.pg.shift) - 1;
@@ -155,7 +140,7 @@ __global__ __launch_bounds__(256, 1) void attn_decode_kernel(AttnArgs a, int gro
     bool first_seg = true;
     while (u < uend) {
         Work w;
-        if (!find_work<SPLIT>(a, u, lane, w)) return;
+        if (!find_work<SPLIT>(a, q0, u, lane, w)) return;
         const int b0 = w.block, b1 = SPLIT ? (w.nb < b0 + uend - u ? w.nb : b0 + uend - u) : w.nb;
         const bool whole = b0 == 0 && b1 == w.nb;
 
@@ -228,10 +213,11 @@ __global__ __launch_bounds__(256, 1) void attn_decode_kernel(AttnArgs a, int gro
             }
             const int p0 = w.lo + b * UNIT + BW * wave;
             if (p0 > last) continue;
-            const unsigned char *kt = lds[wave][stage][0], *vt = lds[wave][stage][1];
+            const unsigned char *kt = lds[0][0][0], *vt = lds[0][0][1];
+            const unsigned rb = rb0 + (2 * wave + stage) * (2 * TILE), tb = tb0 + (2 * wave + stage) * (2 * TILE);
             f32x16 sc = {};
 #pragma unroll
-            for (int s = 0; s < KS; ++s) sc = mfma32(row_frag<DP>(kt, col, s, g), qf[s], sc);
+            for (int s = 0; s < KS; ++s) sc = mfma32(row_frag(kt, rb, s), qf[s], sc);
             if (p0 + BW - 1 > first || a.window > 0 || r0 + BM > rows) {
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
@@ -264,7 +250,7 @@ __global__ __launch_bounds__(256, 1) void attn_decode_kernel(AttnArgs a, int gro
                 const bf16x8 pf = pack_half(sc, s);
 #pragma unroll
                 for (int dt = 0; dt < DT; ++dt)
-                    acc[dt] = mfma32(tr_frag(vt + s * (32 * DP), tro[dt][0], tro[dt][1]), pf, acc[dt]);
+                    acc[dt] = mfma32(tr_frag<DP>(vt + s * (32 * DP), tb, dt), pf, acc[dt]);
             }
         }
         l += other_half(l, lane);
@@ -334,42 +320,31 @@ __global__ __launch_bounds__(256, 1) void attn_decode_kernel(AttnArgs a, int gro
 template <int DP>
 __global__ __launch_bounds__(256) void attn_decode_join_kernel(AttnArgs a, int groups) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, G = a.G;
-    const int total = total_of<true>(a, lane), per = share(total, groups);
+    const Seq q0 = seq_of(a, lane);
+    const int total = total_units(a, q0, lane), per = share(total, groups);
     Work w;
-    if (!find_work<false>(a, blockIdx.x, lane, w)) return;
-    // units of the line before this item: those of the sequences before it, and its place in its own
-    int before = 0;
-    for (int s0 = 0; s0 <= w.seq; s0 += 64) {
-        const Seq q = seq_of(a, s0 + lane);
-        before += s0 + lane < w.seq ? q.tiles * q.nb * a.K : 0;
-    }
-#pragma unroll
-    for (int d = 32; d; d >>= 1) before += __shfl_xor(before, d);
-    before += (w.kvh * w.tiles + w.rt) * w.nb;
+    if (!find_work<false>(a, q0, blockIdx.x, lane, w)) return;
+    const int before = w.before;
     const int w0 = before / per, w1 = (before + w.nb - 1) / per;
     if (w0 == w1) return;
     const int rows = w.n * G, r0 = w.rt * BM;
     const int count = rows - r0 < BM ? rows - r0 : BM;
+    const int d = 2 * lane;
     for (int r = wave; r < count; r += 4) {
         auto slot_row = [&](int v) { return (int64_t)(2 * v + (v == w0 && before > v * per ? 1 : 0)) * BM + r; };
+        // a lane per stretch, 64 at a time
         float m = neg_inf();
-        for (int v = w0; v <= w1; ++v) {
-            const float x = a.pl[slot_row(v)];
-            m = x != x ? x : fmaxf(m, x);
-        }
+        for (int v0 = w0; v0 <= w1; v0 += 64)
+            m = max_or_nan(m, wave_max_or_nan(v0 + lane <= w1 ? a.pl[slot_row(v0 + lane)] : neg_inf()));
         float o0 = 0.f, o1 = 0.f, sum = 0.f;
-        const int d = 2 * lane;
-        if (m != neg_inf())
-            for (int v = w0; v <= w1; ++v) {
-                const float x = a.pl[slot_row(v)];
-                const float f = __builtin_amdgcn_exp2f(x - m);
-                sum += f;
-                if (d < a.D) {
-                    const float2 p = *(const float2*)(a.po + slot_row(v) * a.D + d);
-                    o0 += f * p.x;
-                    o1 += f * p.y;
-                }
-            }
+        for (int v0 = w0; v0 <= w1; v0 += 64) {
+            const float x = v0 + lane <= w1 ? a.pl[slot_row(v0 + lane)] : neg_inf();
+            const float f = x == neg_inf() ? 0.f : __builtin_amdgcn_exp2f(x - m);
+            sum += f;
+            const int n = w1 + 1 - v0 < 64 ? w1 + 1 - v0 : 64;
+            join_rows(n, f, d < a.D, [&](int i) { return a.po + slot_row(v0 + i) * a.D + d; }, o0, o1);
+        }
+        sum = wave_sum(sum);
         const float inv = sum > 0.f ? 1.f / sum : sum;
         const int rr = r0 + r, tk = div_group(rr, G, a.gmagic), hd = w.kvh * G + rr - tk * G;
         if (d < a.D) {

@@ -85,8 +85,8 @@ __global__ __launch_bounds__(256, 2) void attn_f32_fwd_kernel(AttnArgs a) {
     b /= a.K;
     const int split = b % a.nsplit, t = b / a.nsplit;
     Item it;
-    if (!find_item(a.cu, a.S, (int)a.N, t, [&](int, int n) { return (int)(((int64_t)n * G + BM - 1) / BM); }, it)) return;
-    const int r0 = (it.tiles - 1 - it.tile) * BM;
+    if (!find_item(a.cu, a.S, (int)a.N, t, row_cap(a.window, G, BM), [&](int n) { return (n * G + BM - 1) / BM; }, it)) return;
+    const int r0 = it.tile * BM;
     const int rows = it.n * G;
     int kept = 0;
     if constexpr (PAGED) kept = kept_tokens(a.pg, it.seq, it.n);
@@ -215,8 +215,8 @@ __global__ __launch_bounds__(256, 2) void attn_f32_dq_kernel(AttnBwdArgs a) {
     const int u = lane >> 4, col = lane & 15, G = a.G;
     const int kvh = blockIdx.x % a.K, t = blockIdx.x / a.K;
     Item it;
-    if (!find_item(a.cu, a.S, (int)a.N, t, [&](int, int n) { return (int)(((int64_t)n * G + BM - 1) / BM); }, it)) return;
-    const int r0 = (it.tiles - 1 - it.tile) * BM;
+    if (!find_item(a.cu, a.S, (int)a.N, t, row_cap(a.window, G, BM), [&](int n) { return (n * G + BM - 1) / BM; }, it)) return;
+    const int r0 = it.tile * BM;
     const int rows = it.n * G;
     const int first = div_group(r0, G, a.gmagic);
     const int last = div_group(r0 + BM < rows ? r0 + BM - 1 : rows - 1, G, a.gmagic);
@@ -311,8 +311,8 @@ __global__ __launch_bounds__(256, 2) void attn_f32_dkdv_kernel(AttnBwdArgs a) {
     const int u = lane >> 4, col = lane & 15, G = a.G;
     const int kvh = blockIdx.x % a.K, t = blockIdx.x / a.K;
     Item it;
-    if (!find_item(a.cu, a.S, (int)a.N, t, [&](int, int n) { return (n + BM - 1) / BM; }, it)) return;
-    const int k0 = it.tile * BM;
+    if (!find_item(a.cu, a.S, (int)a.N, t, row_cap(a.window, 1, BM), [&](int n) { return (n + BM - 1) / BM; }, it)) return;
+    const int k0 = (it.tiles - 1 - it.tile) * BM;  // the first keys of a sequence have the most rows
     const int rows = it.n * G;
     const int klast = k0 + BM < it.n ? k0 + BM - 1 : it.n - 1;
     const int rbeg = k0 * G;

@@ -70,9 +70,8 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(AttnArgs a) {
     const int t = SPLIT ? b / a.nsplit : b;
     Item it;
     const int G = a.G;
-    if (!find_item(a.cu, a.S, (int)a.N, t, [&](int, int n) { return (int)(((int64_t)n * G + BM - 1) / BM); }, it)) return;
-    // the longest rows of a sequence first: its last tile has the most keys
-    const int r0 = (it.tiles - 1 - it.tile) * BM;
+    if (!find_item(a.cu, a.S, (int)a.N, t, row_cap(a.window, G, BM), [&](int n) { return (n * G + BM - 1) / BM; }, it)) return;
+    const int r0 = it.tile * BM;
     const int rows = it.n * G;
     int kept = 0;
     if constexpr (PAGED) {
@@ -180,12 +179,7 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(AttnArgs a) {
         }
     };
 
-    unsigned tro[DT][2];
-#pragma unroll
-    for (int dt = 0; dt < DT; ++dt) {
-        tro[dt][0] = tr_offset<DP>(dt, 0, lane);
-        tro[dt][1] = tr_offset<DP>(dt, 1, lane);
-    }
+    const unsigned rb0 = row_base<DP>(col, g), tb0 = tr_base<DP>(lane);
 
     f32x16 acc[DT] = {};
     float m = neg_inf(), l = 0.f;
@@ -210,12 +204,13 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(AttnArgs a) {
         }
         const int p0 = lo + j * BN;
         if (!wlive || p0 > wlast || (a.window > 0 && p0 + BN - 1 <= wfirst - a.window)) continue;
-        const unsigned char *kt = lds[stage][0], *vt = lds[stage][1];
+        const unsigned char *kt = lds[0][0], *vt = lds[0][1];
+        const unsigned rb = rb0 + stage * (2 * TILE), tb = tb0 + stage * (2 * TILE);
         f32x16 sc[2] = {};
 #pragma unroll
         for (int s = 0; s < KS; ++s)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) sc[h] = mfma32(row_frag<DP>(kt, 32 * h + col, s, g), qf[s], sc[h]);
+            for (int h = 0; h < 2; ++h) sc[h] = mfma32(row_frag(kt + h * (64 * DP), rb, s), qf[s], sc[h]);
         if (p0 + BN - 1 > wfirst || (a.window > 0 && p0 <= wlast - a.window) || wr0 + 32 > rows) {
 #pragma unroll
             for (int h = 0; h < 2; ++h)
@@ -254,7 +249,7 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(AttnArgs a) {
             const bf16x8 pf = pack_half(sc[s >> 1], s & 1);
 #pragma unroll
             for (int dt = 0; dt < DT; ++dt)
-                acc[dt] = mfma32(tr_frag(vt + s * (32 * DP), tro[dt][0], tro[dt][1]), pf, acc[dt]);
+                acc[dt] = mfma32(tr_frag<DP>(vt + s * (32 * DP), tb, dt), pf, acc[dt]);
         }
     }
 
@@ -308,25 +303,14 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
     const int tok = (int)(r / a.H);
     if (tok < clamped(a.cu[0], (int)a.N) || tok >= clamped(a.cu[a.S], (int)a.N)) return;
     const int lane = threadIdx.x & 63;
-    float m = neg_inf();
-    for (int i = 0; i < a.nsplit; ++i) {
-        const float x = a.pl[i * NH + r];
-        m = x != x ? x : fmaxf(m, x);  // NaN stays
-    }
-    float o0 = 0.f, o1 = 0.f, w = 0.f;
+    // a lane per key range (at most 64)
+    const float x = lane < a.nsplit ? a.pl[lane * NH + r] : neg_inf();
+    const float m = wave_max_or_nan(x);
+    const float f = x == neg_inf() ? 0.f : __builtin_amdgcn_exp2f(x - m);
+    const float w = wave_sum(f);
+    float o0 = 0.f, o1 = 0.f;
     const int d = 2 * lane;
-    if (m != neg_inf())
-        for (int i = 0; i < a.nsplit; ++i) {
-            const float x = a.pl[i * NH + r];
-            if (x == neg_inf()) continue;  // this range saw nothing and wrote nothing
-            const float f = __builtin_amdgcn_exp2f(x - m);
-            w += f;
-            if (d < a.D) {
-                const float2 v = *(const float2*)(a.po + (i * NH + r) * a.D + d);
-                o0 += f * v.x;
-                o1 += f * v.y;
-            }
-        }
+    join_rows(a.nsplit, f, d < a.D, [&](int i) { return a.po + (i * NH + r) * a.D + d; }, o0, o1);
     const float inv = w > 0.f ? 1.f / w : w;
     if (d < a.D) {
         T* o = (T*)a.out + r * a.D + d;

@@ -319,6 +319,7 @@ __global__ __launch_bounds__(256) void norm_dw_sum_kernel(const float* part, flo
     const int c = blockIdx.x * 16 + cc;
     float s = 0.f;
     if (c < W)
+#pragma unroll 8
         for (int gi = k; gi < groups; gi += 16) s += part[(int64_t)gi * W + c];
     sh[k][cc] = s;
     __syncthreads();
