@@ -98,8 +98,11 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(AttnBwdArgs a) {
         }
     }
     delta += other_half(delta, lane);
-    if (live && g == 0) a.delta[at] = delta;
     const float lse2 = live ? a.lse[at] * kLog2e : 0.f;
+    if (live && g == 0) {  // what the other kernel's accumulators start from
+        a.stats[at] = -lse2 / a.sl2;
+        a.stats[a.N * a.H + at] = -delta;
+    }
 
     const char* ksrc = (const char*)a.k + 2 * (it.tok0 * a.k_tok + kvh * a.k_head);
     const char* vsrc = (const char*)a.v + 2 * (it.tok0 * a.v_tok + kvh * a.v_head);
@@ -175,21 +178,29 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(AttnBwdArgs a) {
     if (live) store_row<DT>((__bf16*)a.dq + at * a.D, acc, a.scale, g, a.D);
 }
 
-// 64 keys per workgroup, 2 waves of 32, over tiles of 32 rows: four workgroups
-// share a compute unit, and there are enough of them that the causal shape's
-// uneven work levels out.
+// 64 keys per workgroup, over tiles of 64 RW rows: wave (kw, rw) takes 32 keys
+// and 64 rows of each tile, and the RW partial sums of a key are added at the
+// end, in order.  One wave per SIMD with all of its registers: 192 of them hold
+// the sums and the key and value operands, and two 32-row halves in turn let
+// one half's exponentials run beside the other's products.  (Two waves per
+// SIMD with 256 registers each left the compiler four to read fragments into,
+// and every product waited for its own read: 1.8 times the time.)
 constexpr int BK = 64;
-constexpr int BR = 32;
 
-template <int DP>
-__global__ __launch_bounds__(128, 2) void attn_dkdv_kernel(AttnBwdArgs a) {
+template <int DP, int RW>
+__global__ __launch_bounds__(128 * RW, 2) void attn_dkdv_kernel(AttnBwdArgs a) {
+    constexpr int BR = 32 * RW;
     constexpr int TILE = BR * DP * 2;
     constexpr int KS = DP / 16, DT = DP / 32;
-    constexpr int RPI = 512 / DP, NI = BR / 2 / RPI, CH = DP / 8;  // copy instructions per wave and tensor
+    constexpr int RPI = 512 / DP, NI = 16 / RPI, CH = DP / 8;  // copy instructions per wave and tensor, 16 rows
+    constexpr int OLD = DP + 4;                                // row stride of the final sums, floats
     __shared__ __attribute__((aligned(1024))) unsigned char lds[2][2][TILE];  // [stage][Q, dout]
-    __shared__ __attribute__((aligned(256))) float stat[2][2][BR];            // [stage][lse, delta]
+    __shared__ __attribute__((aligned(256))) float stat[2][2][BR];            // [stage][-lse / scale, -delta]
+    __shared__ __attribute__((aligned(16))) unsigned offs[2][128 * RW][NI];   // [Q, dout]: copy offsets of a thread
+    static_assert((RW - 1) * BK * OLD * 4 <= 4 * TILE, "the final sums fit in the stages");
 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int kw = wave & 1, rw = wave >> 1;
     const int g = lane >> 5, col = lane & 31, G = a.G;
     const int kvh = blockIdx.x % a.K, t = blockIdx.x / a.K;
     Item it;
@@ -202,7 +213,7 @@ __global__ __launch_bounds__(128, 2) void attn_dkdv_kernel(AttnBwdArgs a) {
     const int rend = re < rows ? (int)re : rows;  // rows that see some key of the block: [k0 G, rend)
     const int nb = (rend - rbeg + BR - 1) / BR;
 
-    const int key = k0 + 32 * wave + col;
+    const int key = k0 + 32 * kw + col;
     const bool live = key < it.n;
     const int64_t ktok = it.tok0 + (live ? key : 0);
     // rows that see this lane's key: [rlo, rhi)
@@ -224,8 +235,8 @@ __global__ __launch_bounds__(128, 2) void attn_dkdv_kernel(AttnBwdArgs a) {
         }
     }
 
-    const int crow = lane / CH, cpc = lane % CH;
-    const unsigned base = lds_addr(&lds[0][0][0]) + wave * (TILE / 2);
+    const int crow = 16 * wave + lane / CH, cpc = lane % CH;
+    const unsigned base = lds_addr(&lds[0][0][0]) + wave * (16 * DP * 2);
     const unsigned sbase = lds_addr(&stat[0][0][0]);
     const char* qsrc = (const char*)a.q + 2 * (it.tok0 * a.q_tok + (int64_t)kvh * G * a.q_head);
     const int64_t first_row = (int64_t)it.tok0 * a.H + kvh * G;  // row 0 in [N][H] order
@@ -233,38 +244,41 @@ __global__ __launch_bounds__(128, 2) void attn_dkdv_kernel(AttnBwdArgs a) {
     // A group whose size divides the tile starts every tile on a token: a
     // lane's offsets are the same in all of them, and only the base moves.
     // Otherwise they come anew from the row number.
-    const bool steady = BR % G == 0 && a.q_head < (1 << 23) / G;
-    unsigned qoff[NI], doff[NI];
-    int64_t toff = 0;
-    {
+    const bool steady = BR % G == 0 && a.q_head < (1 << 22) / G && a.q_tok < (1 << 30) / BR;
+    // (They wait in the LDS: the accumulators leave no registers for them.)
 #pragma unroll
-        for (int i = 0; i < NI; ++i) {
-            const int rr = BR / 2 * wave + RPI * i + crow, tk = div_group(rr, G, a.gmagic), hg = rr - tk * G;
-            const int c = cpc ^ swz<DP>(rr);
-            const bool in = 8 * c < a.D && steady;
-            qoff[i] = in ? (unsigned)(2 * (tk * a.q_tok + hg * a.q_head) + 16 * c) : kOutside;
-            doff[i] = in ? (unsigned)(2 * (tk * a.H + hg) * a.D + 16 * c) : kOutside;
-        }
-        const int rr = lane & (BR - 1), tk = div_group(rr, G, a.gmagic);
-        toff = (int64_t)tk * a.H + rr - tk * G;
+    for (int i = 0; i < NI; ++i) {
+        const int rr = crow + RPI * i, tk = div_group(rr, G, a.gmagic), hg = rr - tk * G;
+        const int c = cpc ^ swz<DP>(rr);
+        const bool in = 8 * c < a.D && steady;
+        offs[0][threadIdx.x][i] = in ? (unsigned)(2 * (tk * a.q_tok + hg * a.q_head) + 16 * c) : kOutside;
+        offs[1][threadIdx.x][i] = in ? (unsigned)(2 * (tk * a.H + hg) * a.D + 16 * c) : kOutside;
     }
     auto copy_tile = [&](int j, int stage) {
         const unsigned dst = base + stage * (2 * TILE);
-        const int t0 = rbeg + j * BR;
+        const int t0 = rbeg + (nb - 1 - j) * BR;
         if (steady) {
             const int64_t tk = div_group(t0, G, a.gmagic);
             const u32x4 qr = buffer_rsrc(qsrc + 2 * tk * a.q_tok, (int)kOutside);
             const u32x4 dr = buffer_rsrc(dsrc + 2 * tk * a.H * a.D, (int)kOutside);
+            if (t0 + BR <= rows) {
 #pragma unroll
-            for (int i = 0; i < NI; ++i) {
-                const bool in = t0 + BR / 2 * wave + RPI * i + crow < rows;
-                copy16(qr, dst + 1024 * i, in ? qoff[i] : kOutside);
-                copy16(dr, dst + TILE + 1024 * i, in ? doff[i] : kOutside);
+                for (int i = 0; i < NI; ++i) {
+                    copy16(qr, dst + 1024 * i, offs[0][threadIdx.x][i]);
+                    copy16(dr, dst + TILE + 1024 * i, offs[1][threadIdx.x][i]);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < NI; ++i) {
+                    const bool in = t0 + crow + RPI * i < rows;
+                    copy16(qr, dst + 1024 * i, in ? offs[0][threadIdx.x][i] : kOutside);
+                    copy16(dr, dst + TILE + 1024 * i, in ? offs[1][threadIdx.x][i] : kOutside);
+                }
             }
         } else {
 #pragma unroll
             for (int i = 0; i < NI; ++i) {
-                const int rr = BR / 2 * wave + RPI * i + crow;
+                const int rr = crow + RPI * i;
                 const int r = t0 + rr, c = cpc ^ swz<DP>(rr);
                 const char *qp = (const char*)zeros, *dp = (const char*)zeros;
                 if (8 * c < a.D && r < rows) {
@@ -276,79 +290,103 @@ __global__ __launch_bounds__(128, 2) void attn_dkdv_kernel(AttnBwdArgs a) {
                 copy16_at(dp, dst + TILE + 1024 * i);
             }
         }
-        if (wave == 0) {  // lanes 0..31 the lse, 32..63 the delta of the tile's rows
-            const int r = t0 + (lane & (BR - 1));
-            int64_t at = toff;
-            if (steady) {
-                at += (int64_t)div_group(t0, G, a.gmagic) * a.H;
-            } else {
-                const int tk = div_group(r, G, a.gmagic);
-                at = (int64_t)tk * a.H + r - tk * G;
-            }
-            copy4_at((lane < BR ? a.lse : a.delta) + first_row + (r < rows ? at : 0), sbase + stage * (2 * BR * 4));
+        // the statistics of the tile's rows: 64 of them per wave, BR of each kind
+        if (64 * wave < 2 * BR) {
+            const int x = 64 * wave + lane, r = t0 + (x & (BR - 1));
+            const int tk = div_group(r < rows ? r : 0, G, a.gmagic), hg = r < rows ? r - tk * G : 0;
+            copy4_at(a.stats + (x < BR ? 0 : a.N * a.H) + first_row + (int64_t)tk * a.H + hg,
+                     sbase + stage * (2 * BR * 4) + wave * 256);
         }
     };
-    const unsigned rb0 = row_base<DP>(col, g), tb0 = tr_base<DP>(lane);
+    const unsigned rb0 = row_base<DP>(col, g) + rw * (64 * DP), tb0 = tr_base<DP>(lane) + rw * (64 * DP);
 
     f32x16 dk[DT] = {}, dv[DT] = {};
-    const int wk0 = k0 + 32 * wave;  // this wave's keys
+    const int wk0 = k0 + 32 * kw;  // this wave's keys
     const int wklast = wk0 + 31;
     const bool wlive = wk0 < it.n;
 
+    // from the last rows back: the key blocks of a sequence that run at the same
+    // time begin on the same tiles and find them in the L2 cache
     if (nb > 0) copy_tile(0, 0);
     for (int j = 0; j < nb; ++j) {
         const int stage = j & 1;
         wait_vm<0>();
         barrier_lds();
         if (j + 1 < nb) copy_tile(j + 1, stage ^ 1);
-        const int p0 = rbeg + j * BR;
-        if (!wlive || p0 + BR - 1 < wk0 * G) continue;
+        const int p0 = rbeg + (nb - 1 - j) * BR + 32 * rw;
+        if (!wlive || p0 + 31 < wk0 * G || p0 >= rows) continue;
         const unsigned char *qt = lds[0][0], *ot = lds[0][1];
         const unsigned rb = rb0 + stage * (2 * TILE), tb = tb0 + stage * (2 * TILE);
-        const bool edge = p0 < wklast * G || p0 + BR > rows || wklast >= it.n ||
-                          (a.window > 0 && p0 + BR > ((int64_t)wk0 + a.window) * G);
-        f32x16 sc = {}, dp = {};
-#pragma unroll
-        for (int s = 0; s < KS; ++s) {
-            sc = mfma32(row_frag(qt, rb, s), kf[s], sc);
-            dp = mfma32(row_frag(ot, rb, s), vf[s], dp);
-        }
+        const bool edge = p0 < wklast * G || p0 + 32 > rows || wklast >= it.n ||
+                          (a.window > 0 && p0 + 32 > ((int64_t)wk0 + a.window) * G);
+        const float* st = &stat[stage][0][32 * rw + 4 * g];
+        // <q, k> - lse / scale and <dout, v> - delta: the accumulators start
+        // from the rows' statistics
+        f32x16 sc, dp;
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
-            const f32x4 ls = *(const f32x4*)&stat[stage][0][8 * b + 4 * g];
-            const f32x4 de = *(const f32x4*)&stat[stage][1][8 * b + 4 * g];
+            const f32x4 ls = *(const f32x4*)(st + 8 * b), de = *(const f32x4*)(st + BR + 8 * b);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const int i = 4 * b + e;
-                sc[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[i], a.sl2, -ls[e] * kLog2e));
-                dp[i] = sc[i] * (dp[i] - de[e]);
+                sc[4 * b + e] = ls[e];
+                dp[4 * b + e] = de[e];
             }
+        }
+        read_ahead<2 * KS, 4>([&](auto n) { return row_frag(n % 2 ? ot : qt, rb, n / 2); },
+                              [&](auto n, bf16x8 f) {
+                                  if constexpr (n % 2 == 0) sc = mfma32(f, kf[n / 2], sc);
+                                  else dp = mfma32(f, vf[n / 2], dp);
+                              });
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            sc[i] = __builtin_amdgcn_exp2f(sc[i] * a.sl2);
+            dp[i] *= sc[i];
         }
         if (edge) {
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
                 const int r = p0 + acc_row(i, g);
-                if (r < rlo || r >= rhi) {
-                    sc[i] = 0.f;
-                    dp[i] = 0.f;
-                }
+                const bool out = r < rlo || r >= rhi;
+                sc[i] = out ? 0.f : sc[i];
+                dp[i] = out ? 0.f : dp[i];
             }
         }
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            const bf16x8 pf = pack_half(sc, s), sf = pack_half(dp, s);
-            const unsigned o = s * (32 * DP);
-#pragma unroll
-            for (int dt = 0; dt < DT; ++dt) {
-                dv[dt] = mfma32(tr_frag<DP>(ot + o, tb, dt), pf, dv[dt]);
-                dk[dt] = mfma32(tr_frag<DP>(qt + o, tb, dt), sf, dk[dt]);
-            }
-        }
+        const bf16x8 pf[2] = {pack_half(sc, 0), pack_half(sc, 1)}, sf[2] = {pack_half(dp, 0), pack_half(dp, 1)};
+        __builtin_amdgcn_sched_barrier(0);
+        read_ahead<4 * DT, 4>([&](auto n) { return tr_frag<DP>((n % 2 ? qt : ot) + n / (2 * DT) * (32 * DP), tb, n / 2 % DT); },
+                              [&](auto n, bf16x8 f) {
+                                  constexpr int s = n / (2 * DT), dt = n / 2 % DT;
+                                  if constexpr (n % 2 == 0) dv[dt] = mfma32(f, pf[s], dv[dt]);
+                                  else dk[dt] = mfma32(f, sf[s], dk[dt]);
+                              });
     }
-    if (!live) return;
-    const int64_t at = (ktok * a.K + kvh) * a.D;
-    store_row<DT>((__bf16*)a.dk + at, dk, a.scale, g, a.D);
-    store_row<DT>((__bf16*)a.dv + at, dv, 1.f, g, a.D);
+    float* area = (float*)&lds[0][0][0] + (32 * kw + col) * OLD + 4 * g;
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+        f32x16(&x)[DT] = which == 0 ? dv : dk;
+        barrier_lds();  // the stages, or the sums before, have been read
+        if (rw > 0) {
+#pragma unroll
+            for (int dt = 0; dt < DT; ++dt)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    *(f32x4*)(area + (rw - 1) * (BK * OLD) + 32 * dt + 8 * j) =
+                        f32x4{x[dt][4 * j], x[dt][4 * j + 1], x[dt][4 * j + 2], x[dt][4 * j + 3]};
+        }
+        barrier_lds();
+        if (rw > 0) continue;
+#pragma unroll
+        for (int w = 0; w < RW - 1; ++w)
+#pragma unroll
+            for (int dt = 0; dt < DT; ++dt)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const f32x4 y = *(const f32x4*)(area + w * (BK * OLD) + 32 * dt + 8 * j);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) x[dt][4 * j + e] += y[e];
+                }
+        if (live) store_row<DT>((__bf16*)(which == 0 ? a.dv : a.dk) + (ktok * a.K + kvh) * a.D, x, which == 0 ? 1.f : a.scale, g, a.D);
+    }
 }
 
 template <int DP>
@@ -358,7 +396,7 @@ hipError_t launch(const AttnBwdArgs& a, hipStream_t s) {
     attn_dq_kernel<DP><<<dim3((unsigned)dq_grid), dim3(256), 0, s>>>(a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    attn_dkdv_kernel<DP><<<dim3((unsigned)dkv_grid), dim3(128), 0, s>>>(a);
+    attn_dkdv_kernel<DP, 2><<<dim3((unsigned)dkv_grid), dim3(256), 0, s>>>(a);
     return hipGetLastError();
 }
 

@@ -13,6 +13,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "layer_internal.h"
 
 namespace e2ttt {
@@ -44,6 +46,14 @@ __device__ __forceinline__ float other_half(float x, int lane) {
 // Row r's token, r / G (the host bounds r G below 2^32).
 __device__ __forceinline__ int div_group(int r, int G, unsigned magic) {
     return G == 1 ? r : (int)__umulhi((unsigned)r, magic);
+}
+
+template <int N, int I = 0, class F>
+__device__ __forceinline__ void static_for(F&& f) {
+    if constexpr (I < N) {
+        f(std::integral_constant<int, I>{});
+        static_for<N, I + 1>(f);
+    }
 }
 
 // ------------------------------------------------------------- work items
@@ -236,6 +246,20 @@ __device__ __forceinline__ bf16x8 tr_frag(const unsigned char* lds, unsigned tb,
     return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
+// N products with the fragments of each read AHEAD products before it.  (Left
+// to itself the compiler, short of registers, reads every fragment into the
+// same ones and waits for it.)
+template <int N, int AHEAD, class R, class M>
+__device__ __forceinline__ void read_ahead(R&& read, M&& product) {
+    bf16x8 f[AHEAD];
+    static_for<(AHEAD < N ? AHEAD : N)>([&](auto n) { f[n] = read(n); });
+    static_for<N>([&](auto n) {
+        product(n, f[n % AHEAD]);
+        if constexpr (n + AHEAD < N) f[n % AHEAD] = read(std::integral_constant<int, n + AHEAD>{});
+        __builtin_amdgcn_sched_barrier(0);
+    });
+}
+
 // Row of a 32x32 accumulator element i in lane half g.
 __device__ __forceinline__ constexpr int acc_row(int i, int g) { return 8 * (i >> 2) + 4 * g + (i & 3); }
 
@@ -268,7 +292,7 @@ __device__ __forceinline__ u32x4 buffer_rsrc(const void* base, int num_bytes) {
 __device__ __forceinline__ void copy16(u32x4 rsrc, unsigned lds, unsigned voff) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
                  :
-                 : "s"(lds), "v"(voff), "s"(rsrc)
+                 : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(voff), "s"(rsrc)
                  : "memory", "m0");
 }
 
@@ -276,7 +300,7 @@ __device__ __forceinline__ void copy16(u32x4 rsrc, unsigned lds, unsigned voff) 
 __device__ __forceinline__ void copy16_at(const void* p, unsigned lds) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
                  :
-                 : "s"(lds), "v"(p)
+                 : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(p)
                  : "memory", "m0");
 }
 
@@ -284,7 +308,7 @@ __device__ __forceinline__ void copy16_at(const void* p, unsigned lds) {
 __device__ __forceinline__ void copy4_at(const void* p, unsigned lds) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off"
                  :
-                 : "s"(lds), "v"(p)
+                 : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(p)
                  : "memory", "m0");
 }
 

@@ -242,7 +242,7 @@ __global__ __launch_bounds__(256, 2) void attn_f32_dq_kernel(AttnBwdArgs a) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) delta = __builtin_fmaf(df[s][e], of[s][e], delta);
     delta = groups_sum(delta);
-    if (live && u == 0) a.delta[at] = delta;
+    if (live && u == 0) a.stats[at] = delta;
     const float lse2 = live ? a.lse[at] * kLog2e : 0.f;
 
     const float* ksrc = (const float*)a.k + it.tok0 * a.k_tok + kvh * a.k_head;
@@ -354,7 +354,7 @@ __global__ __launch_bounds__(256, 2) void attn_f32_dkdv_kernel(AttnBwdArgs a) {
             if (r < rend) {
                 const int tk = div_group(r, G, a.gmagic), hg = r - tk * G;
                 const int64_t at = first_row + (int64_t)tk * a.H + hg;
-                st = threadIdx.x < BN ? a.lse[at] * kLog2e : a.delta[at];
+                st = threadIdx.x < BN ? a.lse[at] * kLog2e : a.stats[at];
             }
         }
     };

@@ -229,7 +229,7 @@ int e2ttt_attention_forward(const e2ttt_attention_desc* d, const void* q, const 
 
 size_t e2ttt_attention_backward_workspace_size(const e2ttt_attention_desc* d) {
     if (attention_desc_status(d, true) != E2TTT_OK) return kBad;
-    return (size_t)(d->tokens * d->heads) * 4;
+    return (size_t)(d->tokens * d->heads) * 8;
 }
 
 int e2ttt_attention_backward(const e2ttt_attention_desc* d, const void* q, const void* k, const void* v,
@@ -278,7 +278,7 @@ int e2ttt_attention_backward(const e2ttt_attention_desc* d, const void* q, const
     a.window = f.window;
     a.sl2 = f.sl2;
     a.scale = d->scale;
-    a.delta = (float*)ws;
+    a.stats = (float*)ws;
     a.dq = dq;
     a.dk = dk;
     a.dv = dv;

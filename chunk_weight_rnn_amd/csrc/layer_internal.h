@@ -62,7 +62,7 @@ struct AttnBwdArgs {
     unsigned gmagic;
     int window;
     float sl2, scale;
-    float* delta;  // [N][H] workspace
+    float* stats;  // [2][N][H] workspace: bf16 -lse / scale and -delta of each row; fp32 delta alone
     void *dq, *dk, *dv;
 };
 hipError_t launch_attn_bwd_bf16(const AttnBwdArgs& a, hipStream_t s);

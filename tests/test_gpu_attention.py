@@ -93,6 +93,13 @@ def test_long_sequence_of_few_heads(window):
     check([1500], 2, 1, 128, "bf16", window)
 
 
+@pytest.mark.parametrize("H,K,D,window", [(16, 16, 128, 0), (32, 16, 64, 0), (48, 16, 128, 0), (16, 16, 64, 150)])
+def test_many_key_blocks(H, K, D, window):
+    """Enough key blocks to fill the chip, with groups that divide a tile and
+    one that does not."""
+    check([700, 0, 900, 505], H, K, D, "bf16", window)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_many_sequences(dtype):
     """More sequences than a wave has lanes, some empty."""
