@@ -260,6 +260,27 @@ __device__ __forceinline__ void read_ahead(R&& read, M&& product) {
     });
 }
 
+// Largest value of one or two accumulators in this lane (NaN only if all are).
+// The three-operand maximum is written out because fmaxf would first quiet
+// each operand in an instruction of its own.  Every asm depends on an ordinary
+// maximum of both accumulators, so that the compiler has placed the wait for
+// the products before it.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
+    return r;
+}
+__device__ __forceinline__ float max_of(const f32x16& x, const f32x16& y) {
+    const float m = fmaxf(x[0], y[0]);
+    float a = max3(m, x[1], x[2]), b = max3(m, y[1], y[2]);
+#pragma unroll
+    for (int i = 3; i < 15; i += 2) {
+        a = max3(a, x[i], x[i + 1]);
+        b = max3(b, y[i], y[i + 1]);
+    }
+    return fmaxf(max3(a, x[15], y[15]), b);
+}
+
 // Row of a 32x32 accumulator element i in lane half g.
 __device__ __forceinline__ constexpr int acc_row(int i, int g) { return 8 * (i >> 2) + 4 * g + (i & 3); }
 

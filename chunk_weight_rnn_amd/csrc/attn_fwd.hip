@@ -207,10 +207,8 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(AttnArgs a) {
         const unsigned char *kt = lds[0][0], *vt = lds[0][1];
         const unsigned rb = rb0 + stage * (2 * TILE), tb = tb0 + stage * (2 * TILE);
         f32x16 sc[2] = {};
-#pragma unroll
-        for (int s = 0; s < KS; ++s)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) sc[h] = mfma32(row_frag(kt + h * (64 * DP), rb, s), qf[s], sc[h]);
+        read_ahead<2 * KS, 4>([&](auto n) { return row_frag(kt + n % 2 * (64 * DP), rb, n / 2); },
+                              [&](auto n, bf16x8 f) { sc[n % 2] = mfma32(f, qf[n / 2], sc[n % 2]); });
         if (p0 + BN - 1 > wfirst || (a.window > 0 && p0 <= wlast - a.window) || wr0 + 32 > rows) {
 #pragma unroll
             for (int h = 0; h < 2; ++h)
@@ -220,9 +218,7 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(AttnArgs a) {
                     if (p > qpos || p <= qlow) sc[h][i] = neg_inf();
                 }
         }
-        float mx = fmaxf(sc[0][0], sc[1][0]);
-#pragma unroll
-        for (int i = 1; i < 16; ++i) mx = fmaxf(mx, fmaxf(sc[0][i], sc[1][i]));
+        float mx = max_of(sc[0], sc[1]);
         mx = fmaxf(mx, other_half(mx, lane)) * a.sl2;
         if (__any(mx > m + kLazy)) {
             const float mn = fmaxf(m, mx);
