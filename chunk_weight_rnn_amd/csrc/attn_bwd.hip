@@ -24,8 +24,6 @@ namespace {
 constexpr int BM = 128;  // rows (dq) or keys (dkdv) of a workgroup: 4 waves x 32
 constexpr int BN = 64;   // keys or rows of a staged tile
 
-__device__ __align__(256) unsigned char zeros[256];  // read in place of rows outside a sequence
-
 template <int DP>
 struct CopyPlan {
     static constexpr int RPI = 512 / DP;       // rows per copy instruction

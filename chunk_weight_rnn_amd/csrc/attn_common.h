@@ -64,7 +64,9 @@ __device__ __forceinline__ void static_for(F&& f) {
 // last would leave the rest of the chip idle.  Every wave searches for itself,
 // from the offsets in memory (clamped, so that whatever they hold no address
 // leaves the tensors); with more than 64 sequences there are many tiles of
-// each kind, and they are taken sequence by sequence.  False past the last tile.
+// each kind, and they are taken sequence by sequence; so they are with cap = 0,
+// where work is level and neighbours had better share their keys in the cache.
+// False past the last tile.
 struct Item {
     int seq, tok0, n;  // sequence, its first token, its length
     int tile, tiles;   // tile within the sequence, tiles of the sequence
@@ -98,6 +100,8 @@ __device__ __forceinline__ int row_cap(int window, int G, int BM) {
     return window == 0 || c > 0x7fffffff ? 0x7fffffff : (int)c;
 }
 
+constexpr int kInOrder = 0;
+
 template <class F>
 __device__ __forceinline__ bool find_item(const int* __restrict__ cu, int S, int N, int t, int cap, F&& tiles_of,
                                           Item& it) {
@@ -118,7 +122,7 @@ __device__ __forceinline__ bool find_item(const int* __restrict__ cu, int S, int
         it.tiles = __builtin_amdgcn_readlane(m, l);
     };
     int a, n, m;
-    if (S <= 64) {
+    if (S <= 64 && cap > 0) {
         load(lane, a, n, m);
         const int most = last_lane(wave_scan<true>(m));
         const int step = ((most < cap ? most : cap) + kClasses - 1) / kClasses;
@@ -293,6 +297,8 @@ __device__ __forceinline__ bf16x8 pack_half(const f32x16& x, int hs) {
     return r;
 }
 
+static __device__ __align__(256) unsigned char zeros[256];  // read in place of rows outside a sequence
+
 // ------------------------------------------------------- copies to the LDS
 // dword 3 of a raw buffer resource (gfx9 family: 32-bit data format, no swizzle)
 constexpr int RSRC_W3 = 0x00020000;
@@ -352,6 +358,84 @@ __device__ __forceinline__ void barrier_lds() {
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
 }
+
+// Copies T consecutive positions of one (sequence, key head) to the LDS, from
+// the cache's pages and, from position `fresh` on, from the new tokens; this
+// wave its rows row0 + RPI i + crow (one instruction moves RPI rows).
+//
+// Positions start at multiples of T, so within a page the slot of a row is a
+// constant of the lane (pages shorter than T) or a constant plus the tile's
+// place in its page: a tile that lies in the cache as a whole costs one 64-bit
+// multiply-add per address.  The others (a sequence's last, and the first under
+// a window) take the general way, row by row.
+template <int DP, int NI, int T>
+struct PageCopy {
+    static constexpr int RPI = 512 / DP, CH = DP / 8;
+    const char *kc, *vc, *kn, *vn;  // this key head in page 0 and in the sequence's new tokens
+    int fresh, begin, end;          // positions outside [begin, end) are read as zeros
+    int row0;
+    unsigned ko[NI], vo[NI];
+
+    __device__ __forceinline__ void init(const AttnArgs& a, int kvh, int tok0, int kept, int row0_) {
+        const int lane = threadIdx.x & 63, mask = (1 << a.pg.shift) - 1;
+        row0 = row0_;
+        kn = (const char*)a.k + 2 * (tok0 * a.k_tok + kvh * a.k_head);
+        vn = (const char*)a.v + 2 * (tok0 * a.v_tok + kvh * a.v_head);
+        kc = (const char*)a.pg.kc + 2 * kvh * a.pg.k_head;
+        vc = (const char*)a.pg.vc + 2 * kvh * a.pg.v_head;
+        fresh = a.pg.append ? kept : 0x7fffffff;
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+            const int r = row0 + RPI * i + lane / CH, c = (lane % CH) ^ swz<DP>(r);
+            const bool in = 8 * c < a.D;
+            ko[i] = in ? (unsigned)((r & mask) * a.pg.k_slot * 2 + 16 * c) : kOutside;
+            vo[i] = in ? (unsigned)((r & mask) * a.pg.v_slot * 2 + 16 * c) : kOutside;
+        }
+    }
+    // The page of position pos (-1: none that is read).
+    __device__ __forceinline__ int page_of(const AttnArgs& a, const int* table, int pos) const {
+        const int pi = pos >> a.pg.shift;
+        return pos >= begin && pos < end && pos < fresh && pi < a.pg.wide ? table[pi] : -1;
+    }
+    // page(i): the page of this lane's row of instruction i.
+    template <class F>
+    __device__ __forceinline__ void copy(const AttnArgs& a, int p0, unsigned kdst, unsigned vdst, F&& page) const {
+        const int mask = (1 << a.pg.shift) - 1;
+        if (p0 >= begin && p0 + T <= end && p0 + T <= fresh) {
+            const char* kb = kc + (int64_t)(p0 & mask) * a.pg.k_slot * 2;
+            const char* vb = vc + (int64_t)(p0 & mask) * a.pg.v_slot * 2;
+            const unsigned kp = (unsigned)a.pg.k_page * 2, vp = (unsigned)a.pg.v_page * 2;
+#pragma unroll
+            for (int i = 0; i < NI; ++i) {
+                const unsigned p = (unsigned)page(i);
+                const bool ok = p < (unsigned)a.pg.pages && ko[i] != kOutside;
+                copy16_at(ok ? kb + ((uint64_t)p * kp + ko[i]) : (const char*)zeros, kdst + 1024 * i);
+                copy16_at(ok ? vb + ((uint64_t)p * vp + vo[i]) : (const char*)zeros, vdst + 1024 * i);
+            }
+            return;
+        }
+        const int lane = threadIdx.x & 63;
+#pragma unroll 1
+        for (int i = 0; i < NI; ++i) {
+            const int r = row0 + RPI * i + lane / CH, pos = p0 + r;
+            const int64_t c = 16 * ((lane % CH) ^ swz<DP>(r));
+            const int p = page(i);
+            const char *kp = (const char*)zeros, *vp = (const char*)zeros;
+            if (c < 2 * a.D && pos >= begin && pos < end) {
+                if (pos >= fresh) {
+                    kp = kn + 2 * (pos - fresh) * a.k_tok + c;
+                    vp = vn + 2 * (pos - fresh) * a.v_tok + c;
+                } else if ((unsigned)p < (unsigned)a.pg.pages) {
+                    const int64_t slot = pos & mask;
+                    kp = kc + 2 * (p * a.pg.k_page + slot * a.pg.k_slot) + c;
+                    vp = vc + 2 * (p * a.pg.v_page + slot * a.pg.v_slot) + c;
+                }
+            }
+            copy16_at(kp, kdst + 1024 * i);
+            copy16_at(vp, vdst + 1024 * i);
+        }
+    }
+};
 
 // ------------------------------------------------------- partial results
 __device__ __forceinline__ float max_or_nan(float x, float y) { return x != x ? x : (y != y ? y : fmaxf(x, y)); }

@@ -25,8 +25,6 @@ constexpr int BW = 32;     // keys of a unit per wave
 constexpr int UNIT = 128;  // keys of a unit
 constexpr float kLazy = 8.f;  // as in attn_fwd.hip
 
-__device__ __align__(256) unsigned char zeros[256];  // read in place of rows outside a sequence
-
 struct Work {
     int seq, tok0, n, kept;  // sequence
     int kvh, rt, tiles;      // key head, row tile, row tiles of the sequence
@@ -133,9 +131,8 @@ __global__ __launch_bounds__(256, 1) void attn_decode_kernel(AttnArgs a, int gro
         uend = u + 1;
     }
     const unsigned rb0 = row_base<DP>(col, g), tb0 = tr_base<DP>(lane);
-    const int crow = lane / CH, cpc = lane % CH;
+    const int crow = lane / CH;
     const unsigned base = lds_addr(&lds[wave][0][0][0]);
-    const int mask = (1 << a.pg.shift) - 1;
 
     bool first_seg = true;
     while (u < uend) {
@@ -152,8 +149,6 @@ __global__ __launch_bounds__(256, 1) void attn_decode_kernel(AttnArgs a, int gro
         const int qlow = a.window > 0 ? qpos - a.window : -1;
         const int first = w.kept + div_group(r0, G, a.gmagic);
         const int last = w.kept + div_group(r0 + BM < rows ? r0 + BM - 1 : rows - 1, G, a.gmagic);
-        const int begin = a.window > 0 ? first - a.window + 1 : 0, end = last + 1;
-        const int fresh = a.pg.append ? w.kept : 0x7fffffff;
         const int64_t qtok = w.tok0 + tok;
         const int head = w.kvh * G + hg;
 
@@ -165,39 +160,17 @@ __global__ __launch_bounds__(256, 1) void attn_decode_kernel(AttnArgs a, int gro
             bf16x8 z = {};
             qf[s] = live && d < a.D ? *(const bf16x8*)(qp + d) : z;
         }
-        const char* ksrc = (const char*)a.k + 2 * (w.tok0 * a.k_tok + w.kvh * a.k_head);
-        const char* vsrc = (const char*)a.v + 2 * (w.tok0 * a.v_tok + w.kvh * a.v_head);
-        const char* kc = (const char*)a.pg.kc + 2 * w.kvh * a.pg.k_head;
-        const char* vc = (const char*)a.pg.vc + 2 * w.kvh * a.pg.v_head;
+        PageCopy<DP, NI, BW> pc;
+        pc.init(a, w.kvh, w.tok0, w.kept, 0);
+        pc.begin = a.window > 0 ? first - a.window + 1 : 0;
+        pc.end = last + 1;
         const int* table = a.pg.table + (int64_t)w.seq * a.pg.wide;
 
         // the page of key col of this wave's part of unit b
-        auto load_page = [&](int b) {
-            const int pos = w.lo + b * UNIT + BW * wave + col, pi = pos >> a.pg.shift;
-            return b < b1 && pos >= begin && pos < end && pos < fresh && pi < a.pg.wide ? table[pi] : -1;
-        };
+        auto load_page = [&](int b) { return b < b1 ? pc.page_of(a, table, w.lo + b * UNIT + BW * wave + col) : -1; };
         auto copy_part = [&](int b, int stage, int page) {
             const unsigned dst = base + stage * (2 * TILE);
-            const int p0 = w.lo + b * UNIT + BW * wave;
-#pragma unroll
-            for (int i = 0; i < NI; ++i) {
-                const int r = RPI * i + crow;
-                const int pos = p0 + r, pp = __shfl(page, r);
-                const int64_t c = 16 * (cpc ^ swz<DP>(r));
-                const char *kp = (const char*)zeros, *vp = (const char*)zeros;
-                if (c < 2 * a.D && pos >= begin && pos < end) {
-                    if (pos >= fresh) {
-                        kp = ksrc + 2 * (pos - fresh) * a.k_tok + c;
-                        vp = vsrc + 2 * (pos - fresh) * a.v_tok + c;
-                    } else if ((unsigned)pp < (unsigned)a.pg.pages) {
-                        const int64_t slot = pos & mask;
-                        kp = kc + 2 * (pp * a.pg.k_page + slot * a.pg.k_slot) + c;
-                        vp = vc + 2 * (pp * a.pg.v_page + slot * a.pg.v_slot) + c;
-                    }
-                }
-                copy16_at(kp, dst + 1024 * i);
-                copy16_at(vp, dst + TILE + 1024 * i);
-            }
+            pc.copy(a, w.lo + b * UNIT + BW * wave, dst, dst + TILE, [&](int i) { return __shfl(page, RPI * i + crow); });
         };
 
         f32x16 acc[DT] = {};

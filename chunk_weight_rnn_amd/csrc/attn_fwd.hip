@@ -27,17 +27,6 @@ constexpr int BN = 64;   // keys of a tile
 // tiles skip the rescaling of the outputs.
 constexpr float kLazy = 8.f;
 
-__device__ __align__(256) unsigned char zeros[256];  // read in place of rows outside a sequence
-
-// Source of the key/value rows of one (sequence, key head).
-struct Source {
-    const char *k, *v;        // packed rows: position 0
-    const char *kc, *vc;      // paged: this key head in page 0
-    const int* table;         // this sequence's pages
-    int fresh;                // positions >= fresh come from the packed rows (position - fresh)
-    int begin, end;           // positions outside [begin, end) are read as zeros (paged), or past end (packed)
-};
-
 // A wave's part of a tile copy: BN / 4 rows, 1 KiB (1024 / (2 DP) rows) per
 // instruction.
 template <int DP>
@@ -70,7 +59,11 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(AttnArgs a) {
     const int t = SPLIT ? b / a.nsplit : b;
     Item it;
     const int G = a.G;
-    if (!find_item(a.cu, a.S, (int)a.N, t, row_cap(a.window, G, BM), [&](int n) { return (n * G + BM - 1) / BM; }, it)) return;
+    // new tokens all see their whole cache, and split tiles are short: in order
+    // (8 chunks of 256 tokens over a window of 2048: 61 us, by work 75 us);
+    // whole tiles by work (16 packed prompts up to 2048: 122 us in order, 103 us)
+    const int cap = PAGED || SPLIT ? kInOrder : row_cap(a.window, G, BM);
+    if (!find_item(a.cu, a.S, (int)a.N, t, cap, [&](int n) { return (n * G + BM - 1) / BM; }, it)) return;
     const int r0 = it.tile * BM;
     const int rows = it.n * G;
     int kept = 0;
@@ -108,18 +101,8 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(AttnArgs a) {
         }
     }
 
-    Source src;
-    src.k = (const char*)a.k + 2 * (it.tok0 * a.k_tok + kvh * a.k_head);
-    src.v = (const char*)a.v + 2 * (it.tok0 * a.v_tok + kvh * a.v_head);
-    src.begin = a.window > 0 ? first - a.window + 1 : 0;
-    src.end = last + 1;
-    if constexpr (PAGED) {
-        src.kc = (const char*)a.pg.kc + 2 * kvh * a.pg.k_head;
-        src.vc = (const char*)a.pg.vc + 2 * kvh * a.pg.v_head;
-        src.table = a.pg.table + (int64_t)it.seq * a.pg.wide;
-        src.fresh = a.pg.append ? kept : 0x7fffffff;
-    }
-
+    const char* ksrc = (const char*)a.k + 2 * (it.tok0 * a.k_tok + kvh * a.k_head);
+    const char* vsrc = (const char*)a.v + 2 * (it.tok0 * a.v_tok + kvh * a.v_head);
     // copy offsets: row (within this wave's quarter) and chunk of this lane
     const int crow = lane / P::CH, cpc = lane % P::CH;
     unsigned koff[P::NI], voff[P::NI];
@@ -133,44 +116,30 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(AttnArgs a) {
     }
     const unsigned base = lds_addr(&lds[0][0][0]) + wave * (TILE / 4);
 
+    PageCopy<DP, P::NI, BN> pc;
+    const int* table = nullptr;
+    if constexpr (PAGED) {
+        pc.init(a, kvh, it.tok0, kept, 16 * wave);
+        pc.begin = a.window > 0 ? first - a.window + 1 : 0;
+        pc.end = last + 1;
+        table = a.pg.table + (int64_t)it.seq * a.pg.wide;
+    }
     int page[P::NI];  // paged: the next tile's page indices, loaded a tile ahead
     auto load_pages = [&](int j) {
         if constexpr (PAGED) {
 #pragma unroll
-            for (int i = 0; i < P::NI; ++i) {
-                const int pos = lo + j * BN + 16 * wave + P::RPI * i + crow;
-                const int pi = pos >> a.pg.shift;
-                page[i] = pos >= src.begin && pos < src.end && pos < src.fresh && pi < a.pg.wide ? src.table[pi] : -1;
-            }
+            for (int i = 0; i < P::NI; ++i) page[i] = pc.page_of(a, table, lo + j * BN + 16 * wave + P::RPI * i + crow);
         }
     };
     auto copy_tile = [&](int j, int stage) {
         const unsigned dst = base + stage * (2 * TILE);
         const int p0 = lo + j * BN;
         if constexpr (PAGED) {
-#pragma unroll
-            for (int i = 0; i < P::NI; ++i) {
-                const int r = 16 * wave + P::RPI * i + crow;
-                const int pos = p0 + r;
-                const int64_t c = 16 * (cpc ^ swz<DP>(r));
-                const char *kp = (const char*)zeros, *vp = (const char*)zeros;
-                if (c < 2 * a.D && pos >= src.begin && pos < src.end) {
-                    if (pos >= src.fresh) {
-                        kp = src.k + 2 * (pos - src.fresh) * a.k_tok + c;
-                        vp = src.v + 2 * (pos - src.fresh) * a.v_tok + c;
-                    } else if ((unsigned)page[i] < (unsigned)a.pg.pages) {
-                        const int64_t slot = pos & ((1 << a.pg.shift) - 1);
-                        kp = src.kc + 2 * (page[i] * a.pg.k_page + slot * a.pg.k_slot) + c;
-                        vp = src.vc + 2 * (page[i] * a.pg.v_page + slot * a.pg.v_slot) + c;
-                    }
-                }
-                copy16_at(kp, dst + 1024 * i);
-                copy16_at(vp, dst + TILE + 1024 * i);
-            }
+            pc.copy(a, p0, dst, dst + TILE, [&](int i) { return page[i]; });
         } else {
-            const int left = src.end - p0 < BN ? src.end - p0 : BN;  // rows of the tile that exist
-            const u32x4 kr = buffer_rsrc(src.k + (int64_t)p0 * a.k_tok * 2, (int)((left - 1) * a.k_tok * 2) + 2 * a.D);
-            const u32x4 vr = buffer_rsrc(src.v + (int64_t)p0 * a.v_tok * 2, (int)((left - 1) * a.v_tok * 2) + 2 * a.D);
+            const int left = last + 1 - p0 < BN ? last + 1 - p0 : BN;  // rows of the tile that exist
+            const u32x4 kr = buffer_rsrc(ksrc + (int64_t)p0 * a.k_tok * 2, (int)((left - 1) * a.k_tok * 2) + 2 * a.D);
+            const u32x4 vr = buffer_rsrc(vsrc + (int64_t)p0 * a.v_tok * 2, (int)((left - 1) * a.v_tok * 2) + 2 * a.D);
 #pragma unroll
             for (int i = 0; i < P::NI; ++i) {
                 copy16(kr, dst + 1024 * i, koff[i]);

@@ -68,11 +68,11 @@ int paged_desc_status(const e2ttt_paged_desc* d, bool append) {
         return E2TTT_ERR_INVALID_ARG;
     const int64_t es = elem(d->a.io_dtype), D = d->a.D;
     const int64_t s[6] = {d->kc_page, d->kc_head, d->kc_slot, d->vc_page, d->vc_head, d->vc_slot};
-    const int64_t n[3] = {d->pages, d->a.kv_heads, d->page_size}, lim = (int64_t)1 << 40;
+    const int64_t n[3] = {d->pages, d->a.kv_heads, d->page_size}, lim[3] = {1 << 30, (int64_t)1 << 40, 1 << 23};
     for (int i = 0; i < 6; ++i)  // slots that the call writes must not overlap
         if (n[i % 3] > 1 && (!stride_ok(s[i], es) || s[i] < D)) return E2TTT_ERR_INVALID_ARG;
     for (int i = 0; i < 6; ++i)
-        if (n[i % 3] > 1 && s[i] > lim) return E2TTT_ERR_UNSUPPORTED;
+        if (n[i % 3] > 1 && s[i] > lim[i % 3]) return E2TTT_ERR_UNSUPPORTED;  // 32-bit factors of the kernels
     if (d->pages > 0x7fffffff || d->page_size > (1 << 24)) return E2TTT_ERR_UNSUPPORTED;
     if (d->table_width > 0x7fffffff || d->table_width * d->page_size + d->a.tokens + 256 > 0x7fffffff)
         return E2TTT_ERR_UNSUPPORTED;
@@ -107,10 +107,10 @@ void plan(AttnArgs& a, bool f32, int64_t longest) {
     const int bm = attn_fwd_rows(a, f32);
     a.ntiles = (int)(a.N * a.G / bm + a.S);
     a.nsplit = 1;
-    const int64_t items = (a.N * a.G + bm - 1) / bm * a.K;  // at least so many do work
+    const int64_t items = (a.N * a.G / bm + (a.S + 1) / 2) * a.K;  // about so many do work: a sequence's last tile is half full
     if (a.window > 0 && longest > a.window + bm / a.G + 64) longest = a.window + bm / a.G + 64;
     if (items > 0 && items < kCUs) {
-        int64_t n = (2 * kCUs + items - 1) / items;
+        int64_t n = 2 * kCUs / items;  // no more than run at once: a second round of few would double the time
         const int64_t most = (longest + 255) / 256;
         if (n > most) n = most;
         a.nsplit = (int)(n < 1 ? 1 : (n > 64 ? 64 : n));
@@ -343,6 +343,8 @@ int e2ttt_paged_attention(const e2ttt_paged_desc* d, const void* q, const void* 
     a.pg.v_page = d->vc_page;
     a.pg.v_head = d->vc_head;
     a.pg.v_slot = d->vc_slot;
+    if (P == 1) a.pg.k_page = a.pg.v_page = 0;  // strides of a dimension of one are not checked
+    if (ps == 1) a.pg.k_slot = a.pg.v_slot = 0;
     a.pg.table = table;
     a.pg.cached = cached;
     a.pg.wide = (int)d->table_width;
