@@ -365,9 +365,10 @@ __device__ __forceinline__ void barrier_lds() {
 //
 // Positions start at multiples of T, so within a page the slot of a row is a
 // constant of the lane (pages shorter than T) or a constant plus the tile's
-// place in its page: a tile that lies in the cache as a whole costs one 64-bit
-// multiply-add per address.  The others (a sequence's last, and the first under
-// a window) take the general way, row by row.
+// place in its page: a tile that lies in the cache as a whole costs no address
+// arithmetic where it lies in one page, and else one 64-bit multiply-add per
+// address.  The other tiles (a sequence's last, and the first under a window)
+// take the general way, row by row.
 template <int DP, int NI, int T>
 struct PageCopy {
     static constexpr int RPI = 512 / DP, CH = DP / 8;
@@ -405,6 +406,17 @@ struct PageCopy {
             const char* kb = kc + (int64_t)(p0 & mask) * a.pg.k_slot * 2;
             const char* vb = vc + (int64_t)(p0 & mask) * a.pg.v_slot * 2;
             const unsigned kp = (unsigned)a.pg.k_page * 2, vp = (unsigned)a.pg.v_page * 2;
+            if (mask + 1 >= T) {
+                const unsigned p = (unsigned)__builtin_amdgcn_readfirstlane(page(0));
+                const int size = p < (unsigned)a.pg.pages ? (int)kOutside : 0;
+                const u32x4 kr = buffer_rsrc(kb + (uint64_t)p * kp, size), vr = buffer_rsrc(vb + (uint64_t)p * vp, size);
+#pragma unroll
+                for (int i = 0; i < NI; ++i) {
+                    copy16(kr, kdst + 1024 * i, ko[i]);
+                    copy16(vr, vdst + 1024 * i, vo[i]);
+                }
+                return;
+            }
 #pragma unroll
             for (int i = 0; i < NI; ++i) {
                 const unsigned p = (unsigned)page(i);
