@@ -7,15 +7,21 @@
 // the k index of lane group u at step i meaning row 4 u + i.
 //
 // The fp32 MFMA issues at a sixteenth of the bf16 rate, so the products bound
-// these kernels and tiles are simply staged through registers.
+// these kernels and tiles are simply staged through registers.  What is scarce
+// in fp32's small layers is workgroups: four heads over two rows of 2K leave
+// half the chip idle in tiles of 64 rows or keys.  So the four waves of a
+// workgroup share few rows or keys (16) and split the other axis, and add their
+// parts in the LDS at the end.
 #include "attn_common.h"
 
 namespace e2ttt {
 namespace attn {
 namespace {
 
-constexpr int BM = 64;  // rows (or keys, dkdv) of a workgroup: 4 waves x 16
-constexpr int BN = 32;  // keys (or rows, dkdv) of a staged tile
+constexpr int BM = 16;   // rows of a workgroup (forward, dq): 4 waves, 16 keys of a tile each
+constexpr int BN = 64;   // keys of a staged tile
+constexpr int BK = 16;   // keys of a workgroup (dkdv): 8 waves, 16 rows of a tile each
+constexpr int BR = 128;  // rows of a staged tile (dkdv)
 
 __device__ __forceinline__ f32x4 mfma4(float a, float b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0);
@@ -33,11 +39,24 @@ __device__ __forceinline__ float groups_max(float x) {
 
 // A staged tile: rows of DP values, padded by four so that the 16 rows of a
 // fragment start on different banks.
-template <int DP>
+template <int DP, int ROWS, int THREADS>
 struct Tile {
     static constexpr int LD = DP + 4;
-    static constexpr int U = BN * DP / 4 / 256;  // 16-byte units per thread
-    float v[BN * LD];
+    static constexpr int U = ROWS * DP / 4 / THREADS;  // 16-byte units per thread
+    float v[ROWS * LD];
+};
+
+// The fragments of rows 4 u + 0..3 (from `tile` on) by columns, all of them at
+// once: operand of k-step i and column tile dt.
+template <int DP>
+struct ColFrags {
+    float v[4][DP / 16];
+    __device__ __forceinline__ void load(const float* tile, int u, int col) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int dt = 0; dt < DP / 16; ++dt) v[i][dt] = tile[(4 * u + i) * (DP + 4) + 16 * dt + col];
+    }
 };
 
 // Row fragment of k-steps 4 s .. 4 s + 3: columns 16 s + 4 u + 0..3.
@@ -68,9 +87,10 @@ __device__ __forceinline__ void store_cols(float* o, const f32x4 (&acc)[DT], flo
 
 template <int DP, bool PAGED>
 __global__ __launch_bounds__(256, 2) void attn_f32_fwd_kernel(AttnArgs a) {
-    using TL = Tile<DP>;
+    using TL = Tile<DP, BN, 256>;
     constexpr int S4 = DP / 16;
     __shared__ TL kt, vt;
+    __shared__ float stat[2][4][BM];
     int b = blockIdx.x;
     if constexpr (PAGED) {
         const int tiles = a.ntiles * a.nsplit * a.K;
@@ -98,7 +118,7 @@ __global__ __launch_bounds__(256, 2) void attn_f32_fwd_kernel(AttnArgs a) {
     const int per = (nb + a.nsplit - 1) / a.nsplit;
     const int j0 = split * per, j1 = j0 + per < nb ? j0 + per : nb;
 
-    const int row = r0 + 16 * wave + col;
+    const int row = r0 + col;
     const bool live = row < rows;
     const int tok = live ? div_group(row, G, a.gmagic) : 0, hg = live ? row - tok * G : 0;
     const int qpos = live ? kept + tok : -1;
@@ -150,25 +170,23 @@ __global__ __launch_bounds__(256, 2) void attn_f32_fwd_kernel(AttnArgs a) {
         }
         __syncthreads();
         if (j + 1 < j1) load_tile(j + 1);
-        const int p0 = lo + j * BN;
-        f32x4 sc[2] = {};
+        const int w0 = 16 * wave, p0 = lo + j * BN + w0;
+        ColFrags<DP> vf;
+        vf.load(vt.v + w0 * TL::LD, u, col);
+        f32x4 sc = {};
 #pragma unroll
-        for (int s = 0; s < S4; ++s)
+        for (int s = 0; s < S4; ++s) {
+            const f32x4 kf = row4<DP>(kt.v, w0 + col, s, u);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const f32x4 kf = row4<DP>(kt.v, 16 * h + col, s, u);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) sc[h] = mfma4(kf[e], qf[s][e], sc[h]);
-            }
+            for (int e = 0; e < 4; ++e) sc = mfma4(kf[e], qf[s][e], sc);
+        }
         float mx = neg_inf();
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int p = p0 + 16 * h + 4 * u + i;
-                if (p > qpos || p <= qlow) sc[h][i] = neg_inf();
-                mx = fmaxf(mx, sc[h][i]);
-            }
+        for (int i = 0; i < 4; ++i) {
+            const int p = p0 + 4 * u + i;
+            if (p > qpos || p <= qlow) sc[i] = neg_inf();
+            mx = fmaxf(mx, sc[i]);
+        }
         mx = groups_max(mx) * a.sl2;
         const float mn = fmaxf(m, mx);
         const float mu = mn == neg_inf() ? 0.f : mn;
@@ -178,22 +196,45 @@ __global__ __launch_bounds__(256, 2) void attn_f32_fwd_kernel(AttnArgs a) {
 #pragma unroll
         for (int dt = 0; dt < S4; ++dt) acc[dt] *= f;
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int i = 0; i < 4; ++i) {
+            sc[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[i], a.sl2, -mu));
+            l += sc[i];
+        }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                sc[h][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[h][i], a.sl2, -mu));
-                l += sc[h][i];
-            }
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int dt = 0; dt < S4; ++dt)
-                    acc[dt] = mfma4(vt.v[(16 * h + 4 * u + i) * TL::LD + 16 * dt + col], sc[h][i], acc[dt]);
+            for (int dt = 0; dt < S4; ++dt) acc[dt] = mfma4(vf.v[i][dt], sc[i], acc[dt]);
     }
     l = groups_sum(l);
-    if (!live) return;
+    // the four waves together
+    __syncthreads();
+    float* area = kt.v + (16 * wave + col) * TL::LD + 4 * u;
+    if (u == 0) {
+        stat[0][wave][col] = m;
+        stat[1][wave][col] = l;
+    }
+#pragma unroll
+    for (int dt = 0; dt < S4; ++dt) *(f32x4*)(area + 16 * dt) = acc[dt];
+    __syncthreads();
+    if (wave > 0 || !live) return;
+    {
+        float mw[4], mn = neg_inf();
+#pragma unroll
+        for (int w = 0; w < 4; ++w) mn = fmaxf(mn, mw[w] = stat[0][w][col]);
+        const float mu = mn == neg_inf() ? 0.f : mn;
+        l = 0.f;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            const float f = __builtin_amdgcn_exp2f(mw[w] - mu);
+            l += stat[1][w][col] * f;
+#pragma unroll
+            for (int dt = 0; dt < S4; ++dt) {
+                const f32x4 x = *(const f32x4*)(area + 16 * w * TL::LD + 16 * dt) * f;
+                acc[dt] = w == 0 ? x : acc[dt] + x;
+            }
+        }
+        m = mn;
+    }
     const float inv = l > 0.f ? 1.f / l : l;  // a row that sees nothing gives 0; NaN stays
     const float lse2 = l > 0.f ? m + __builtin_amdgcn_logf(l) : (l == 0.f ? neg_inf() : l);
     if (a.nsplit > 1) {
@@ -208,7 +249,7 @@ __global__ __launch_bounds__(256, 2) void attn_f32_fwd_kernel(AttnArgs a) {
 
 template <int DP>
 __global__ __launch_bounds__(256, 2) void attn_f32_dq_kernel(AttnBwdArgs a) {
-    using TL = Tile<DP>;
+    using TL = Tile<DP, BN, 256>;
     constexpr int S4 = DP / 16;
     __shared__ TL kt, vt;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -223,7 +264,7 @@ __global__ __launch_bounds__(256, 2) void attn_f32_dq_kernel(AttnBwdArgs a) {
     const int begin = a.window > 0 && first - a.window + 1 > 0 ? first - a.window + 1 : 0;
     const int lo = begin & ~(BN - 1);
     const int nb = (last - lo) / BN + 1;
-    const int row = r0 + 16 * wave + col;
+    const int row = r0 + col;
     const bool live = row < rows;
     const int tok = live ? div_group(row, G, a.gmagic) : 0, hg = live ? row - tok * G : 0;
     const int qpos = live ? tok : -1;
@@ -242,7 +283,7 @@ __global__ __launch_bounds__(256, 2) void attn_f32_dq_kernel(AttnBwdArgs a) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) delta = __builtin_fmaf(df[s][e], of[s][e], delta);
     delta = groups_sum(delta);
-    if (live && u == 0) a.stats[at] = delta;
+    if (live && u == 0 && wave == 0) a.stats[at] = delta;
     const float lse2 = live ? a.lse[at] * kLog2e : 0.f;
 
     const float* ksrc = (const float*)a.k + it.tok0 * a.k_tok + kvh * a.k_head;
@@ -272,54 +313,62 @@ __global__ __launch_bounds__(256, 2) void attn_f32_dq_kernel(AttnBwdArgs a) {
         }
         __syncthreads();
         if (j + 1 < nb) load_tile(j + 1);
-        const int p0 = lo + j * BN;
+        const int w0 = 16 * wave, p0 = lo + j * BN + w0;
+        ColFrags<DP> kc;
+        kc.load(kt.v + w0 * TL::LD, u, col);
+        f32x4 sc = {}, dp = {};
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            f32x4 sc = {}, dp = {};
+        for (int s = 0; s < S4; ++s) {
+            const f32x4 kf = row4<DP>(kt.v, w0 + col, s, u), vf = row4<DP>(vt.v, w0 + col, s, u);
 #pragma unroll
-            for (int s = 0; s < S4; ++s) {
-                const f32x4 kf = row4<DP>(kt.v, 16 * h + col, s, u), vf = row4<DP>(vt.v, 16 * h + col, s, u);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    sc = mfma4(kf[e], qf[s][e], sc);
-                    dp = mfma4(vf[e], df[s][e], dp);
-                }
+            for (int e = 0; e < 4; ++e) {
+                sc = mfma4(kf[e], qf[s][e], sc);
+                dp = mfma4(vf[e], df[s][e], dp);
             }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int p = p0 + 16 * h + 4 * u + i;
-                const float ds = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[i], a.sl2, -lse2)) * (dp[i] - delta);
-                sc[i] = p > qpos || p <= qlow ? 0.f : ds;
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int dt = 0; dt < S4; ++dt)
-                    acc[dt] = mfma4(kt.v[(16 * h + 4 * u + i) * TL::LD + 16 * dt + col], sc[i], acc[dt]);
         }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int p = p0 + 4 * u + i;
+            const float ds = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[i], a.sl2, -lse2)) * (dp[i] - delta);
+            sc[i] = p > qpos || p <= qlow ? 0.f : ds;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int dt = 0; dt < S4; ++dt) acc[dt] = mfma4(kc.v[i][dt], sc[i], acc[dt]);
     }
-    if (live) store_cols<DP, S4>((float*)a.dq + at * a.D, acc, a.scale, u, a.D);
+    __syncthreads();
+    float* area = kt.v + (16 * wave + col) * TL::LD + 4 * u;
+#pragma unroll
+    for (int dt = 0; dt < S4; ++dt) *(f32x4*)(area + 16 * dt) = acc[dt];
+    __syncthreads();
+    if (wave > 0 || !live) return;
+#pragma unroll
+    for (int w = 1; w < 4; ++w)
+#pragma unroll
+        for (int dt = 0; dt < S4; ++dt) acc[dt] += *(const f32x4*)(area + 16 * w * TL::LD + 16 * dt);
+    store_cols<DP, S4>((float*)a.dq + at * a.D, acc, a.scale, u, a.D);
 }
 
 template <int DP>
-__global__ __launch_bounds__(256, 2) void attn_f32_dkdv_kernel(AttnBwdArgs a) {
-    using TL = Tile<DP>;
+__global__ __launch_bounds__(512, 2) void attn_f32_dkdv_kernel(AttnBwdArgs a) {
+    using TL = Tile<DP, BR, 512>;
     constexpr int S4 = DP / 16;
     __shared__ TL qt, dt_;
-    __shared__ __attribute__((aligned(16))) float stat[2][BN];  // lse (base 2), delta
+    __shared__ __attribute__((aligned(16))) float stat[2][BR];  // lse (base 2), delta
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int u = lane >> 4, col = lane & 15, G = a.G;
     const int kvh = blockIdx.x % a.K, t = blockIdx.x / a.K;
     Item it;
-    if (!find_item(a.cu, a.S, (int)a.N, t, row_cap(a.window, 1, BM), [&](int n) { return (n + BM - 1) / BM; }, it)) return;
-    const int k0 = (it.tiles - 1 - it.tile) * BM;  // the first keys of a sequence have the most rows
+    if (!find_item(a.cu, a.S, (int)a.N, t, row_cap(a.window, 1, BK), [&](int n) { return (n + BK - 1) / BK; }, it)) return;
+    const int k0 = (it.tiles - 1 - it.tile) * BK;  // the first keys of a sequence have the most rows
     const int rows = it.n * G;
-    const int klast = k0 + BM < it.n ? k0 + BM - 1 : it.n - 1;
-    const int rbeg = k0 * G;
+    const int klast = k0 + BK < it.n ? k0 + BK - 1 : it.n - 1;
+    const int rbeg = k0 * G & ~(BR - 1);
     const int64_t re = a.window > 0 ? ((int64_t)klast + a.window) * G : rows;
     const int rend = re < rows ? (int)re : rows;
-    const int nb = (rend - rbeg + BN - 1) / BN;
-    const int key = k0 + 16 * wave + col;
+    const int nb = (rend - rbeg + BR - 1) / BR;
+    const int key = k0 + col;
     const bool live = key < it.n;
     const int64_t ktok = it.tok0 + (live ? key : 0);
     const int rlo = live ? key * G : 0x7fffffff;
@@ -338,8 +387,8 @@ __global__ __launch_bounds__(256, 2) void attn_f32_dkdv_kernel(AttnBwdArgs a) {
     auto load_tile = [&](int j) {
 #pragma unroll
         for (int i = 0; i < TL::U; ++i) {
-            const int x = i * 256 + threadIdx.x;
-            const int r = rbeg + j * BN + x / (DP / 4), c = x % (DP / 4) * 4;
+            const int x = i * 512 + threadIdx.x;
+            const int r = rbeg + (nb - 1 - j) * BR + x / (DP / 4), c = x % (DP / 4) * 4;
             f32x4 z = {};
             qr[i] = dr[i] = z;
             if (r < rend && c < a.D) {
@@ -348,66 +397,80 @@ __global__ __launch_bounds__(256, 2) void attn_f32_dkdv_kernel(AttnBwdArgs a) {
                 dr[i] = *(const f32x4*)(dsrc + ((int64_t)tk * a.H + hg) * a.D + c);
             }
         }
-        if (threadIdx.x < 2 * BN) {
-            const int r = rbeg + j * BN + (threadIdx.x & (BN - 1));
+        if (threadIdx.x < 2 * BR) {
+            const int r = rbeg + (nb - 1 - j) * BR + (threadIdx.x & (BR - 1));
             st = 0.f;
             if (r < rend) {
                 const int tk = div_group(r, G, a.gmagic), hg = r - tk * G;
                 const int64_t at = first_row + (int64_t)tk * a.H + hg;
-                st = threadIdx.x < BN ? a.lse[at] * kLog2e : a.stats[at];
+                st = threadIdx.x < BR ? a.lse[at] * kLog2e : a.stats[at];
             }
         }
     };
     f32x4 dk[S4] = {}, dv[S4] = {};
-    if (nb > 0) load_tile(0);
+    if (nb > 0) load_tile(0);  // from the last rows back, as in attn_bwd.hip
     for (int j = 0; j < nb; ++j) {
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < TL::U; ++i) {
-            const int x = i * 256 + threadIdx.x;
+            const int x = i * 512 + threadIdx.x;
             const int o = x / (DP / 4) * TL::LD + x % (DP / 4) * 4;
             *(f32x4*)(qt.v + o) = qr[i];
             *(f32x4*)(dt_.v + o) = dr[i];
         }
-        if (threadIdx.x < 2 * BN) (&stat[0][0])[threadIdx.x] = st;
+        if (threadIdx.x < 2 * BR) (&stat[0][0])[threadIdx.x] = st;
         __syncthreads();
         if (j + 1 < nb) load_tile(j + 1);
-        const int p0 = rbeg + j * BN;
+        const int w0 = 16 * wave, p0 = rbeg + (nb - 1 - j) * BR + w0;
+        ColFrags<DP> qc, dc;
+        qc.load(qt.v + w0 * TL::LD, u, col);
+        dc.load(dt_.v + w0 * TL::LD, u, col);
+        f32x4 sc = {}, dp = {};
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            f32x4 sc = {}, dp = {};
+        for (int s = 0; s < S4; ++s) {
+            const f32x4 qf = row4<DP>(qt.v, w0 + col, s, u), df = row4<DP>(dt_.v, w0 + col, s, u);
 #pragma unroll
-            for (int s = 0; s < S4; ++s) {
-                const f32x4 qf = row4<DP>(qt.v, 16 * h + col, s, u), df = row4<DP>(dt_.v, 16 * h + col, s, u);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    sc = mfma4(qf[e], kf[s][e], sc);
-                    dp = mfma4(df[e], vf[s][e], dp);
-                }
+            for (int e = 0; e < 4; ++e) {
+                sc = mfma4(qf[e], kf[s][e], sc);
+                dp = mfma4(df[e], vf[s][e], dp);
             }
-            const f32x4 ls = *(const f32x4*)&stat[0][16 * h + 4 * u], de = *(const f32x4*)&stat[1][16 * h + 4 * u];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int r = p0 + 16 * h + 4 * u + i;
-                const bool out = r < rlo || r >= rhi;
-                const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[i], a.sl2, -ls[i]));
-                sc[i] = out ? 0.f : p;
-                dp[i] = out ? 0.f : p * (dp[i] - de[i]);
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int dt = 0; dt < S4; ++dt) {
-                    const int o = (16 * h + 4 * u + i) * TL::LD + 16 * dt + col;
-                    dv[dt] = mfma4(dt_.v[o], sc[i], dv[dt]);
-                    dk[dt] = mfma4(qt.v[o], dp[i], dk[dt]);
-                }
         }
+        const f32x4 ls = *(const f32x4*)&stat[0][w0 + 4 * u], de = *(const f32x4*)&stat[1][w0 + 4 * u];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = p0 + 4 * u + i;
+            const bool out = r < rlo || r >= rhi;
+            const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[i], a.sl2, -ls[i]));
+            sc[i] = out ? 0.f : p;
+            dp[i] = out ? 0.f : p * (dp[i] - de[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int dt = 0; dt < S4; ++dt) {
+                dv[dt] = mfma4(dc.v[i][dt], sc[i], dv[dt]);
+                dk[dt] = mfma4(qc.v[i][dt], dp[i], dk[dt]);
+            }
     }
-    if (!live) return;
-    const int64_t at = (ktok * a.K + kvh) * a.D;
-    store_cols<DP, S4>((float*)a.dk + at, dk, a.scale, u, a.D);
-    store_cols<DP, S4>((float*)a.dv + at, dv, 1.f, u, a.D);
+    // the eight parts of the rows together, in order
+    __syncthreads();
+    const int o = (16 * wave + col) * TL::LD + 4 * u;
+#pragma unroll
+    for (int dt = 0; dt < S4; ++dt) {
+        *(f32x4*)(qt.v + o + 16 * dt) = dk[dt];
+        *(f32x4*)(dt_.v + o + 16 * dt) = dv[dt];
+    }
+    __syncthreads();
+    for (int x = threadIdx.x; x < 2 * BK * (DP / 4); x += 512) {
+        const int which = x / (BK * (DP / 4)), kk = x / (DP / 4) % BK, d = x % (DP / 4) * 4;
+        if (k0 + kk >= it.n || d >= a.D) continue;
+        const float* src = (which ? dt_.v : qt.v) + kk * TL::LD + d;
+        f32x4 y = *(const f32x4*)src;
+#pragma unroll
+        for (int w = 1; w < 8; ++w) y += *(const f32x4*)(src + 16 * w * TL::LD);
+        float* dst = (which ? (float*)a.dv : (float*)a.dk) + (((int64_t)it.tok0 + k0 + kk) * a.K + kvh) * a.D + d;
+        *(f32x4*)dst = which ? y : y * a.scale;
+    }
 }
 
 template <int DP>
@@ -425,12 +488,12 @@ hipError_t launch_fwd(const AttnArgs& a, hipStream_t s) {
 
 template <int DP>
 hipError_t launch_bwd(const AttnBwdArgs& a, hipStream_t s) {
-    const int64_t dq_grid = (a.N * a.G / BM + a.S) * a.K, dkv_grid = (a.N / BM + a.S) * a.K;
-    if (dq_grid > 0x7fffffff) return hipErrorInvalidValue;
+    const int64_t dq_grid = (a.N * a.G / BM + a.S) * a.K, dkv_grid = (a.N / BK + a.S) * a.K;
+    if (dq_grid > 0x7fffffff || dkv_grid > 0x7fffffff) return hipErrorInvalidValue;
     attn_f32_dq_kernel<DP><<<dim3((unsigned)dq_grid), dim3(256), 0, s>>>(a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    attn_f32_dkdv_kernel<DP><<<dim3((unsigned)dkv_grid), dim3(256), 0, s>>>(a);
+    attn_f32_dkdv_kernel<DP><<<dim3((unsigned)dkv_grid), dim3(512), 0, s>>>(a);
     return hipGetLastError();
 }
 

@@ -182,7 +182,7 @@ bool norm_supported(const e2ttt_norm_desc* d) { return d->width <= 65536 && d->r
 
 }  // namespace
 
-int attn_fwd_rows(const AttnArgs&, bool f32) { return f32 ? 64 : 128; }
+int attn_fwd_rows(const AttnArgs&, bool f32) { return f32 ? 16 : 128; }
 
 }  // namespace e2ttt
 
