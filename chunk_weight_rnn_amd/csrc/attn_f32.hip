@@ -46,6 +46,11 @@ struct Tile {
     float v[ROWS * LD];
 };
 
+// Buffers of a tile: with two, one barrier per tile is enough.  At a head
+// dimension of 128 two would leave room for only one workgroup per compute unit.
+template <int DP>
+constexpr int kBuffers = DP == 64 ? 2 : 1;
+
 // The fragments of rows 4 u + 0..3 (from `tile` on) by columns, all of them at
 // once: operand of k-step i and column tile dt.
 template <int DP>
@@ -89,7 +94,8 @@ template <int DP, bool PAGED>
 __global__ __launch_bounds__(256, 2) void attn_f32_fwd_kernel(AttnArgs a) {
     using TL = Tile<DP, BN, 256>;
     constexpr int S4 = DP / 16;
-    __shared__ TL kt, vt;
+    constexpr int NB = kBuffers<DP>;
+    __shared__ TL kts[NB], vts[NB];
     __shared__ float stat[2][4][BM];
     int b = blockIdx.x;
     if constexpr (PAGED) {
@@ -160,7 +166,8 @@ __global__ __launch_bounds__(256, 2) void attn_f32_fwd_kernel(AttnArgs a) {
     float m = neg_inf(), l = 0.f;
     if (j0 < j1) load_tile(j0);
     for (int j = j0; j < j1; ++j) {
-        __syncthreads();
+        TL &kt = kts[NB == 2 ? j & 1 : 0], &vt = vts[NB == 2 ? j & 1 : 0];
+        if (NB == 1) __syncthreads();
 #pragma unroll
         for (int i = 0; i < TL::U; ++i) {
             const int x = i * 256 + threadIdx.x;
@@ -173,13 +180,17 @@ __global__ __launch_bounds__(256, 2) void attn_f32_fwd_kernel(AttnArgs a) {
         const int w0 = 16 * wave, p0 = lo + j * BN + w0;
         ColFrags<DP> vf;
         vf.load(vt.v + w0 * TL::LD, u, col);
-        f32x4 sc = {};
+        f32x4 sc = {}, so = {};  // two chains, so that no product waits for the one before it
 #pragma unroll
         for (int s = 0; s < S4; ++s) {
             const f32x4 kf = row4<DP>(kt.v, w0 + col, s, u);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) sc = mfma4(kf[e], qf[s][e], sc);
+            for (int e = 0; e < 4; e += 2) {
+                sc = mfma4(kf[e], qf[s][e], sc);
+                so = mfma4(kf[e + 1], qf[s][e + 1], so);
+            }
         }
+        sc += so;
         float mx = neg_inf();
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -208,7 +219,7 @@ __global__ __launch_bounds__(256, 2) void attn_f32_fwd_kernel(AttnArgs a) {
     l = groups_sum(l);
     // the four waves together
     __syncthreads();
-    float* area = kt.v + (16 * wave + col) * TL::LD + 4 * u;
+    float* area = kts[0].v + (16 * wave + col) * TL::LD + 4 * u;
     if (u == 0) {
         stat[0][wave][col] = m;
         stat[1][wave][col] = l;
@@ -251,7 +262,8 @@ template <int DP>
 __global__ __launch_bounds__(256, 2) void attn_f32_dq_kernel(AttnBwdArgs a) {
     using TL = Tile<DP, BN, 256>;
     constexpr int S4 = DP / 16;
-    __shared__ TL kt, vt;
+    constexpr int NB = kBuffers<DP>;
+    __shared__ TL kts[NB], vts[NB];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int u = lane >> 4, col = lane & 15, G = a.G;
     const int kvh = blockIdx.x % a.K, t = blockIdx.x / a.K;
@@ -303,7 +315,8 @@ __global__ __launch_bounds__(256, 2) void attn_f32_dq_kernel(AttnBwdArgs a) {
     f32x4 acc[S4] = {};
     load_tile(0);
     for (int j = 0; j < nb; ++j) {
-        __syncthreads();
+        TL &kt = kts[NB == 2 ? j & 1 : 0], &vt = vts[NB == 2 ? j & 1 : 0];
+        if (NB == 1) __syncthreads();
 #pragma unroll
         for (int i = 0; i < TL::U; ++i) {
             const int x = i * 256 + threadIdx.x;
@@ -338,7 +351,7 @@ __global__ __launch_bounds__(256, 2) void attn_f32_dq_kernel(AttnBwdArgs a) {
             for (int dt = 0; dt < S4; ++dt) acc[dt] = mfma4(kc.v[i][dt], sc[i], acc[dt]);
     }
     __syncthreads();
-    float* area = kt.v + (16 * wave + col) * TL::LD + 4 * u;
+    float* area = kts[0].v + (16 * wave + col) * TL::LD + 4 * u;
 #pragma unroll
     for (int dt = 0; dt < S4; ++dt) *(f32x4*)(area + 16 * dt) = acc[dt];
     __syncthreads();
@@ -354,8 +367,9 @@ template <int DP>
 __global__ __launch_bounds__(512, 2) void attn_f32_dkdv_kernel(AttnBwdArgs a) {
     using TL = Tile<DP, BR, 512>;
     constexpr int S4 = DP / 16;
-    __shared__ TL qt, dt_;
-    __shared__ __attribute__((aligned(16))) float stat[2][BR];  // lse (base 2), delta
+    constexpr int NB = kBuffers<DP>;
+    __shared__ TL qts[NB], dts[NB];
+    __shared__ __attribute__((aligned(16))) float stats[NB][2][BR];  // lse (base 2), delta
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int u = lane >> 4, col = lane & 15, G = a.G;
     const int kvh = blockIdx.x % a.K, t = blockIdx.x / a.K;
@@ -410,7 +424,9 @@ __global__ __launch_bounds__(512, 2) void attn_f32_dkdv_kernel(AttnBwdArgs a) {
     f32x4 dk[S4] = {}, dv[S4] = {};
     if (nb > 0) load_tile(0);  // from the last rows back, as in attn_bwd.hip
     for (int j = 0; j < nb; ++j) {
-        __syncthreads();
+        TL &qt = qts[NB == 2 ? j & 1 : 0], &dt_ = dts[NB == 2 ? j & 1 : 0];
+        float(&stat)[2][BR] = stats[NB == 2 ? j & 1 : 0];
+        if (NB == 1) __syncthreads();
 #pragma unroll
         for (int i = 0; i < TL::U; ++i) {
             const int x = i * 512 + threadIdx.x;
@@ -457,14 +473,14 @@ __global__ __launch_bounds__(512, 2) void attn_f32_dkdv_kernel(AttnBwdArgs a) {
     const int o = (16 * wave + col) * TL::LD + 4 * u;
 #pragma unroll
     for (int dt = 0; dt < S4; ++dt) {
-        *(f32x4*)(qt.v + o + 16 * dt) = dk[dt];
-        *(f32x4*)(dt_.v + o + 16 * dt) = dv[dt];
+        *(f32x4*)(qts[0].v + o + 16 * dt) = dk[dt];
+        *(f32x4*)(dts[0].v + o + 16 * dt) = dv[dt];
     }
     __syncthreads();
     for (int x = threadIdx.x; x < 2 * BK * (DP / 4); x += 512) {
         const int which = x / (BK * (DP / 4)), kk = x / (DP / 4) % BK, d = x % (DP / 4) * 4;
         if (k0 + kk >= it.n || d >= a.D) continue;
-        const float* src = (which ? dt_.v : qt.v) + kk * TL::LD + d;
+        const float* src = (which ? dts[0].v : qts[0].v) + kk * TL::LD + d;
         f32x4 y = *(const f32x4*)src;
 #pragma unroll
         for (int w = 1; w < 8; ++w) y += *(const f32x4*)(src + 16 * w * TL::LD);
