@@ -9,7 +9,10 @@
 // partial result goes to the workspace and a second launch joins it.  A
 // workgroup is one per compute unit, 4 waves that each stream their own 32
 // keys of a unit through two LDS stages of their own (no barrier until the
-// item ends): 64 KiB in flight per compute unit.
+// item ends).  A stage is refilled as soon as it has been used, so that a wave
+// waits with both in flight, 128 KiB per compute unit; page indices go through
+// the LDS too, two units ahead, because a wait for one in a register would be a
+// wait for every copy before it.
 //
 // The products are the same as in attn_fwd.hip, S^T = K Q^T and O^T += V^T P^T
 // on 32x32 tiles; a group of 4 heads fills 4 of the 32 columns, which costs
@@ -19,6 +22,8 @@
 namespace e2ttt {
 namespace attn {
 namespace {
+
+__device__ const int no_page = -1;
 
 constexpr int BM = 32;     // rows of an item
 constexpr int BW = 32;     // keys of a unit per wave
@@ -112,7 +117,8 @@ __global__ __launch_bounds__(256, 1) void attn_decode_kernel(AttnArgs a, int gro
     constexpr int OLD = DP + 4;                  // row stride of the merge area, floats
     __shared__ __attribute__((aligned(1024))) unsigned char lds[4][2][2][TILE];  // [wave][stage][K, V]
     __shared__ float stat[4][2][BM];                                             // [wave][m, l]
-    static_assert(4 * BM * OLD * 4 <= (int)sizeof(lds) , "the merge area fits in the stages");
+    __shared__ __attribute__((aligned(256))) int pages[4][4][64];                // [wave][unit % 4][key]
+    static_assert(4 * BM * OLD * 4 <= (int)sizeof(lds), "the merge area fits in the stages");
 
     if ((int)blockIdx.x >= groups) {
         append_block<__bf16>(a, blockIdx.x - groups);
@@ -166,64 +172,79 @@ __global__ __launch_bounds__(256, 1) void attn_decode_kernel(AttnArgs a, int gro
         pc.end = last + 1;
         const int* table = a.pg.table + (int64_t)w.seq * a.pg.wide;
 
-        // the page of key col of this wave's part of unit b
-        auto load_page = [&](int b) { return b < b1 ? pc.page_of(a, table, w.lo + b * UNIT + BW * wave + col) : -1; };
-        auto copy_part = [&](int b, int stage, int page) {
-            const unsigned dst = base + stage * (2 * TILE);
-            pc.copy(a, w.lo + b * UNIT + BW * wave, dst, dst + TILE, [&](int i) { return __shfl(page, RPI * i + crow); });
+        // This wave's part of unit b, in two steps: the pages of its keys, and
+        // two units later the keys and values themselves.  Each is always the
+        // same number of copies, which the waits below count.
+        auto copy_pages = [&](int b) {
+            const int pos = w.lo + b * UNIT + BW * wave + col, pi = pos >> a.pg.shift;
+            const bool in = b < b1 && pos >= pc.begin && pos < pc.end && pos < pc.fresh && pi < a.pg.wide;
+            copy4_at(in ? table + pi : &no_page, lds_addr(&pages[wave][b & 3][0]));
+        };
+        auto copy_part = [&](int b) {
+            const unsigned dst = base + (b & 1) * (2 * TILE);
+            const int* pg = &pages[wave][b & 3][crow];
+            pc.copy(a, w.lo + b * UNIT + BW * wave, dst, dst + TILE, [&](int i) { return pg[RPI * i]; });
         };
 
         f32x16 acc[DT] = {};
         float m = neg_inf(), l = 0.f;
-        copy_part(b0, 0, load_page(b0));
-        int page = load_page(b0 + 1);
+        copy_pages(b0);
+        copy_pages(b0 + 1);
+        wait_vm<0>();
+        copy_part(b0);
+        copy_pages(b0 + 2);
+        if (b0 + 1 < b1) copy_part(b0 + 1);
+        copy_pages(b0 + 3);
         for (int b = b0; b < b1; ++b) {
-            const int stage = (b - b0) & 1;
-            wait_vm<0>();
-            if (b + 1 < b1) {
-                copy_part(b + 1, stage ^ 1, page);
-                page = load_page(b + 2);
-            }
+            const int stage = b & 1;
+            // all but the next unit's copies and the page copy after them
+            if (b + 1 < b1) wait_vm<2 * NI + 1>();
+            else wait_vm<0>();
             const int p0 = w.lo + b * UNIT + BW * wave;
-            if (p0 > last) continue;
-            const unsigned char *kt = lds[0][0][0], *vt = lds[0][0][1];
-            const unsigned rb = rb0 + (2 * wave + stage) * (2 * TILE), tb = tb0 + (2 * wave + stage) * (2 * TILE);
-            f32x16 sc = {};
+            if (p0 <= last) {
+                const unsigned char *kt = lds[0][0][0], *vt = lds[0][0][1];
+                const unsigned rb = rb0 + (2 * wave + stage) * (2 * TILE), tb = tb0 + (2 * wave + stage) * (2 * TILE);
+                f32x16 sc = {};
 #pragma unroll
-            for (int s = 0; s < KS; ++s) sc = mfma32(row_frag(kt, rb, s), qf[s], sc);
-            if (p0 + BW - 1 > first || a.window > 0 || r0 + BM > rows) {
+                for (int s = 0; s < KS; ++s) sc = mfma32(row_frag(kt, rb, s), qf[s], sc);
+                if (p0 + BW - 1 > first || a.window > 0 || r0 + BM > rows) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const int p = p0 + acc_row(i, g);
+                        if (p > qpos || p <= qlow) sc[i] = neg_inf();
+                    }
+                }
+                float mx = sc[0];
+#pragma unroll
+                for (int i = 1; i < 16; ++i) mx = fmaxf(mx, sc[i]);
+                mx = fmaxf(mx, other_half(mx, lane)) * a.sl2;
+                if (__any(mx > m + kLazy)) {
+                    const float mn = fmaxf(m, mx);
+                    const float f = mn == neg_inf() ? 1.f : __builtin_amdgcn_exp2f(m - mn);
+                    m = mn;
+                    l *= f;
+#pragma unroll
+                    for (int dt = 0; dt < DT; ++dt)
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) acc[dt][i] *= f;
+                }
+                const float mu = m == neg_inf() ? 0.f : m;
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                    const int p = p0 + acc_row(i, g);
-                    if (p > qpos || p <= qlow) sc[i] = neg_inf();
+                    sc[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[i], a.sl2, -mu));
+                    l += sc[i];
+                }
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
+                    const bf16x8 pf = pack_half(sc, s);
+#pragma unroll
+                    for (int dt = 0; dt < DT; ++dt)
+                        acc[dt] = mfma32(tr_frag<DP>(vt + s * (32 * DP), tb, dt), pf, acc[dt]);
                 }
             }
-            float mx = sc[0];
-#pragma unroll
-            for (int i = 1; i < 16; ++i) mx = fmaxf(mx, sc[i]);
-            mx = fmaxf(mx, other_half(mx, lane)) * a.sl2;
-            if (__any(mx > m + kLazy)) {
-                const float mn = fmaxf(m, mx);
-                const float f = mn == neg_inf() ? 1.f : __builtin_amdgcn_exp2f(m - mn);
-                m = mn;
-                l *= f;
-#pragma unroll
-                for (int dt = 0; dt < DT; ++dt)
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) acc[dt][i] *= f;
-            }
-            const float mu = m == neg_inf() ? 0.f : m;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                sc[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[i], a.sl2, -mu));
-                l += sc[i];
-            }
-#pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                const bf16x8 pf = pack_half(sc, s);
-#pragma unroll
-                for (int dt = 0; dt < DT; ++dt)
-                    acc[dt] = mfma32(tr_frag<DP>(vt + s * (32 * DP), tb, dt), pf, acc[dt]);
+            if (b + 2 < b1) {
+                copy_part(b + 2);
+                copy_pages(b + 4);
             }
         }
         l += other_half(l, lane);
