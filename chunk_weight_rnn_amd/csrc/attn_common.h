@@ -463,7 +463,8 @@ __device__ __forceinline__ float wave_sum(float x) {
 }
 
 // Adds n partial rows, two values per lane, with lane i's weight f for row i;
-// eight loads in flight.  Rows of weight 0 saw nothing and hold nothing.
+// eight loads in flight, beside the loads that the weights come from.  Rows of
+// weight 0 saw nothing, and what is read of them is not used.
 template <class F>
 __device__ __forceinline__ void join_rows(int n, float f, bool in, F&& row, float& o0, float& o1) {
     for (int i0 = 0; i0 < n; i0 += 8) {
@@ -471,14 +472,14 @@ __device__ __forceinline__ void join_rows(int n, float f, bool in, F&& row, floa
         float w[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            w[e] = i0 + e < n ? __shfl(f, i0 + e) : 0.f;
             v[e] = float2{0.f, 0.f};
-            if (w[e] != 0.f && in) v[e] = *(const float2*)row(i0 + e);
+            if (i0 + e < n && in) v[e] = *(const float2*)row(i0 + e);
         }
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            o0 = __builtin_fmaf(w[e], v[e].x, o0);
-            o1 = __builtin_fmaf(w[e], v[e].y, o1);
+            w[e] = i0 + e < n ? __shfl(f, i0 + e) : 0.f;
+            o0 = w[e] != 0.f ? __builtin_fmaf(w[e], v[e].x, o0) : o0;
+            o1 = w[e] != 0.f ? __builtin_fmaf(w[e], v[e].y, o1) : o1;
         }
     }
 }

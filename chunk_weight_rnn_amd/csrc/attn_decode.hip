@@ -100,13 +100,8 @@ __device__ __forceinline__ bool find_work(const AttnArgs& a, const Seq& q0, int 
     return false;
 }
 
-// Units per workgroup: equal shares, at least `kLeast` (shorter stretches
-// would cost more in joining than they save).
-constexpr int kLeast = 2;
-__device__ __forceinline__ int share(int total, int groups) {
-    const int per = (total + groups - 1) / groups;
-    return per < kLeast ? kLeast : per;
-}
+// Units per workgroup: equal shares.
+__device__ __forceinline__ int share(int total, int groups) { return total > 0 ? (total + groups - 1) / groups : 1; }
 
 template <int DP, bool SPLIT>
 __global__ __launch_bounds__(256, 1) void attn_decode_kernel(AttnArgs a, int groups) {

@@ -48,7 +48,7 @@ hipError_t launch_attn_fwd_f32(const AttnArgs& a, hipStream_t s);
 // Few new tokens per sequence over a paged cache; nsplit > 1: the keys of all
 // items shared out evenly over kDecodeGroups workgroups, po / pl
 // [2 kDecodeGroups][32][D] / [2 kDecodeGroups][32].
-constexpr int kDecodeGroups = 512;
+constexpr int kDecodeGroups = 256;
 hipError_t launch_attn_decode_bf16(const AttnArgs& a, hipStream_t s);
 hipError_t launch_attn_join(const AttnArgs& a, bool f32, hipStream_t s);
 

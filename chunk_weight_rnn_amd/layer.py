@@ -19,6 +19,7 @@ from ._lib import AttentionDesc, E2TTTError, NormDesc, PagedDesc
 _IO = {torch.float32: 0, torch.bfloat16: 1}
 _BAD = ctypes.c_size_t(-1).value
 F8 = torch.float8_e4m3fn
+_functions: dict = {}
 
 
 def _device(first, **others) -> int:
@@ -35,11 +36,13 @@ def _device(first, **others) -> int:
 def _call(fn: str, dev: int, stream, *args):
     """Calls the library on `stream` (default: the current stream of the
     tensors' device, which is made current for the call if it is not)."""
-    if dev != torch.cuda.current_device():
+    if dev != torch._C._cuda_getDevice():
         with torch.cuda.device(dev):
             return _call(fn, dev, stream, *args)
-    s = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
-    st = getattr(_lib.load(), fn)(*args, s)
+    f = _functions.get(fn)
+    if f is None:
+        f = _functions[fn] = getattr(_lib.load(), fn)
+    st = f(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
     if st != 0:
         raise E2TTTError(fn, st)
 
@@ -113,8 +116,8 @@ def _attention_desc(q, k, v, cu, window, scale, kv_heads):
 @lru_cache(maxsize=512)
 def _attention_plan(q, k, v, cu, window, scale):
     d = _attention_desc(q, k, v, cu, window, scale, None)
-    return (d, ctypes.byref(d), _size("e2ttt_attention_workspace_size", d),
-            _size("e2ttt_attention_backward_workspace_size", d))
+    return (tuple(q[0]), ctypes.byref(d), _size("e2ttt_attention_workspace_size", d),
+            _size("e2ttt_attention_backward_workspace_size", d), d)
 
 
 @lru_cache(maxsize=512)
@@ -131,7 +134,7 @@ def _paged_plan(q, k, v, kc, vc, table, cu, window, scale):
         raise ValueError("table must have shape (sequences, width)")
     s, t = kc[1], vc[1]
     d = PagedDesc(a, P, ps, table[0][1], s[0], s[1], s[2], t[0], t[1], t[2])
-    return d, ctypes.byref(d), _size("e2ttt_paged_workspace_size", d)
+    return tuple(q[0]), ctypes.byref(d), _size("e2ttt_paged_workspace_size", d), d
 
 
 @lru_cache(maxsize=512)
@@ -144,7 +147,13 @@ def _norm_plan(shape, dtype, eps, bits8):
     for n in shape[:-1]:
         rows *= n
     d = NormDesc(_IO[dtype], int(bits8), rows, shape[-1], eps, 0)
-    return d, ctypes.byref(d), shape[:-1], _size("e2ttt_norm_backward_workspace_size", d)
+    return tuple(shape[:-1]), ctypes.byref(d), _size("e2ttt_norm_backward_workspace_size", d), d
+
+
+def _row_values(lead, x):
+    if len(lead) == 1:  # sizes as numbers of their own are quicker than a tuple
+        return torch.empty(lead[0], dtype=torch.float32, device=x.device)
+    return torch.empty(lead, dtype=torch.float32, device=x.device)
 
 
 def _workspace(workspace, n, like):
@@ -170,16 +179,15 @@ def attention_forward(q, k, v, cu_seqlens, *, window: int = 0, scale: float | No
     softmax sum, which the backward needs.
     """
     dev = _device(q, k=k, v=v, cu_seqlens=cu_seqlens, out=out, lse=lse)
-    _, desc, need, _ = _attention_plan(_layout(q), _layout(k), _layout(v), _layout(cu_seqlens), window, scale)
-    shape = q.shape
+    (N, H, D), desc, need, _, _ = _attention_plan(_layout(q), _layout(k), _layout(v), _layout(cu_seqlens), window, scale)
     if out is None:
-        out = torch.empty(shape, dtype=q.dtype, device=q.device)
+        out = torch.empty(N, H, D, dtype=q.dtype, device=q.device)
     else:
-        _full("out", out, shape, q.dtype)
+        _full("out", out, (N, H, D), q.dtype)
     if lse is None:
-        lse = torch.empty(shape[:2], dtype=torch.float32, device=q.device)
+        lse = torch.empty(N, H, dtype=torch.float32, device=q.device)
     else:
-        _full("lse", lse, shape[:2], torch.float32)
+        _full("lse", lse, (N, H), torch.float32)
     ws, n = _workspace(workspace, need, q)
     _call("e2ttt_attention_forward", dev, stream, desc, q.data_ptr(), k.data_ptr(), v.data_ptr(),
           cu_seqlens.data_ptr(), out.data_ptr(), lse.data_ptr(), ws, n)
@@ -191,11 +199,10 @@ def attention_backward(q, k, v, out, lse, dout, cu_seqlens, *, window: int = 0, 
     """Gradients of <dout, out> through ``attention_forward``, from its inputs
     and outputs; returns a dict with keys q, k, v (the I/O dtype, contiguous)."""
     dev = _device(q, k=k, v=v, out=out, lse=lse, dout=dout, cu_seqlens=cu_seqlens)
-    _, desc, _, need = _attention_plan(_layout(q), _layout(k), _layout(v), _layout(cu_seqlens), window, scale)
-    shape = q.shape
-    _full("out", out, shape, q.dtype)
-    _full("dout", dout, shape, q.dtype)
-    _full("lse", lse, shape[:2], torch.float32)
+    (N, H, D), desc, _, need, _ = _attention_plan(_layout(q), _layout(k), _layout(v), _layout(cu_seqlens), window, scale)
+    _full("out", out, (N, H, D), q.dtype)
+    _full("dout", dout, (N, H, D), q.dtype)
+    _full("lse", lse, (N, H), torch.float32)
     g = {n: torch.empty(t.shape, dtype=q.dtype, device=q.device) for n, t in (("q", q), ("k", k), ("v", v))}
     ws, n = _workspace(workspace, need, q)
     _call("e2ttt_attention_backward", dev, stream, desc, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
@@ -243,15 +250,15 @@ def paged_attention(q, k, v, k_cache, v_cache, table, cu_seqlens, cached, *, win
         raise ValueError("k and v must both be given, or neither")
     dev = _device(q, k=k, v=v, k_cache=k_cache, v_cache=v_cache, table=table, cu_seqlens=cu_seqlens, cached=cached,
                   out=out)
-    _, desc, need = _paged_plan(_layout(q), _layout(k), _layout(v), _layout(k_cache), _layout(v_cache), _layout(table),
+    (N, H, D), desc, need, _ = _paged_plan(_layout(q), _layout(k), _layout(v), _layout(k_cache), _layout(v_cache), _layout(table),
                                 _layout(cu_seqlens), window, scale)
     S = cu_seqlens.shape[0] - 1
     _int32("table", table, (S, table.shape[1]))
     _int32("cached", cached, (S,))
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        out = torch.empty(N, H, D, dtype=q.dtype, device=q.device)
     else:
-        _full("out", out, q.shape, q.dtype)
+        _full("out", out, (N, H, D), q.dtype)
     ws, n = _workspace(workspace, need, q)
     _call("e2ttt_paged_attention", dev, stream, desc, q.data_ptr(), _p(k), _p(v), k_cache.data_ptr(),
           v_cache.data_ptr(), table.data_ptr(), cu_seqlens.data_ptr(), cached.data_ptr(), out.data_ptr(), ws, n)
@@ -269,7 +276,7 @@ def norm_forward(x, weight, *, residual=None, eps: float = 1e-6, bits8: bool = F
     multiplied by scale [...] (float32, max|y| / 448 of its row; else None).
     """
     dev = _device(x, weight=weight, residual=residual, h=h)
-    _, desc, lead, _ = _norm_plan(x.shape, x.dtype, eps, bits8)
+    lead, desc, _, _ = _norm_plan(x.shape, x.dtype, eps, bits8)
     if not x.is_contiguous():
         raise ValueError("x must be contiguous")
     _full("weight", weight, x.shape[-1:], torch.float32)
@@ -284,10 +291,10 @@ def norm_forward(x, weight, *, residual=None, eps: float = 1e-6, bits8: bool = F
     scale = rstd = None
     if bits8:
         y = torch.empty_like(x, dtype=F8)
-        scale = torch.empty(lead, dtype=torch.float32, device=x.device)
+        scale = _row_values(lead, x)
     else:
         y = torch.empty_like(x)
-        rstd = torch.empty(lead, dtype=torch.float32, device=x.device)
+        rstd = _row_values(lead, x)
     _call("e2ttt_norm_forward", dev, stream, desc, x.data_ptr(), _p(residual), weight.data_ptr(), y.data_ptr(),
           _p(scale), _p(h), _p(rstd))
     return y, scale, (x if residual is None else h), rstd
@@ -298,7 +305,7 @@ def norm_backward(dy, h, weight, rstd, *, dh=None, workspace=None, stream=None):
     (dx, dweight).  dx is the gradient of both x and residual; ``dh`` is what
     arrives at h along the residual stream, added to it."""
     dev = _device(h, dy=dy, weight=weight, rstd=rstd, dh=dh)
-    _, desc, lead, need = _norm_plan(h.shape, h.dtype, 0.0, False)
+    lead, desc, need, _ = _norm_plan(h.shape, h.dtype, 0.0, False)
     _full("h", h, h.shape, h.dtype)
     _full("weight", weight, h.shape[-1:], torch.float32)
     _full("dy", dy, h.shape, h.dtype)

@@ -160,6 +160,20 @@ def test_autograd_and_differences():
     assert torch.equal(lx.grad, e2.norm_backward(dy, x, w, rs)[0])
 
 
+def test_any_leading_dimensions():
+    import chunk_weight_rnn_amd as e2
+    x, r, w, _, _ = make(12, 64, "bf16", True)
+    y, _, h, rstd = e2.norm_forward(x, w, residual=r)
+    for lead in ((3, 4), (2, 3, 2), (12,)):
+        a = e2.norm_forward(x.view(*lead, 64), w, residual=r.view(*lead, 64))
+        assert a[0].shape == (*lead, 64) and a[3].shape == lead
+        assert torch.equal(a[0].view(12, 64), y) and torch.equal(a[3].view(12), rstd)
+    a = e2.norm_forward(x[0], w, residual=r[0])
+    assert a[3].shape == () and torch.equal(a[0], y[0])
+    a = e2.norm_forward(x[0], w, residual=r[0], bits8=True)
+    assert a[1].shape == () and a[3] is None
+
+
 def test_no_rows():
     import chunk_weight_rnn_amd as e2
     x = torch.empty(0, 64, device="cuda")
