@@ -126,16 +126,14 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(AttnArgs a) {
     }
     int page[P::NI];  // paged: the next tile's page indices, loaded a tile ahead
     auto load_pages = [&](int j) {
-        if constexpr (PAGED) {
-#pragma unroll
-            for (int i = 0; i < P::NI; ++i) page[i] = pc.page_of(a, table, lo + j * BN + 16 * wave + P::RPI * i + crow);
-        }
+        if constexpr (PAGED) pc.load_pages(a, table, lo + j * BN, page);
     };
     auto copy_tile = [&](int j, int stage) {
         const unsigned dst = base + stage * (2 * TILE);
         const int p0 = lo + j * BN;
         if constexpr (PAGED) {
-            pc.copy(a, p0, dst, dst + TILE, [&](int i) { return page[i]; });
+            pc.template copy<false>(a, p0, dst, [&](int i) { return page[i]; });
+            pc.template copy<true>(a, p0, dst + TILE, [&](int i) { return page[i]; });
         } else {
             const int left = last + 1 - p0 < BN ? last + 1 - p0 : BN;  // rows of the tile that exist
             const u32x4 kr = buffer_rsrc(ksrc + (int64_t)p0 * a.k_tok * 2, (int)((left - 1) * a.k_tok * 2) + 2 * a.D);
