@@ -255,32 +255,54 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(AttnArgs a) {
         }
 }
 
-// Joins the partial results of a split call: one wave per (token, head),
-//   out = sum_i 2^(pl_i - m) po_i / sum_i 2^(pl_i - m).
+// Joins the partial results of a split call,
+//   out = sum_i 2^(pl_i - m) po_i / sum_i 2^(pl_i - m),
+// half a wave per (token, head) with four values per lane; lane i of the half
+// holds the weight of key range i (at most 32).
 template <typename T>
 __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
-    const int64_t r = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    typedef T out4 __attribute__((ext_vector_type(4)));
+    const int64_t r = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
     const int64_t NH = a.N * a.H;
-    if (r >= NH) return;
+    const int lane = threadIdx.x & 63, g = lane >> 5, i = lane & 31, d = 4 * i;
     // a token outside every sequence has no partial results
     const int tok = (int)(r / a.H);
-    if (tok < clamped(a.cu[0], (int)a.N) || tok >= clamped(a.cu[a.S], (int)a.N)) return;
-    const int lane = threadIdx.x & 63;
-    // a lane per key range (at most 64)
-    const float x = lane < a.nsplit ? a.pl[lane * NH + r] : neg_inf();
-    const float m = wave_max_or_nan(x);
+    const bool live = r < NH && tok >= clamped(a.cu[0], (int)a.N) && tok < clamped(a.cu[a.S], (int)a.N);
+    const bool in = live && d < a.D;
+    const float x = live && i < a.nsplit ? a.pl[i * NH + r] : neg_inf();
+    // the partial rows come beside the weights; those of weight 0 are not used
+    f32x4 v[8], o = {};
+    auto load = [&](int s0) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            f32x4 z = {};
+            v[e] = in && s0 + e < a.nsplit ? *(const f32x4*)(a.po + ((s0 + e) * NH + r) * a.D + d) : z;
+        }
+    };
+    load(0);
+    float m = x;
+#pragma unroll
+    for (int k = 16; k; k >>= 1) m = max_or_nan(m, __shfl_xor(m, k));
     const float f = x == neg_inf() ? 0.f : __builtin_amdgcn_exp2f(x - m);
-    const float w = wave_sum(f);
-    float o0 = 0.f, o1 = 0.f;
-    const int d = 2 * lane;
-    join_rows(a.nsplit, f, d < a.D, [&](int i) { return a.po + (i * NH + r) * a.D + d; }, o0, o1);
-    const float inv = w > 0.f ? 1.f / w : w;
-    if (d < a.D) {
-        T* o = (T*)a.out + r * a.D + d;
-        o[0] = (T)(o0 * inv);
-        o[1] = (T)(o1 * inv);
+    float w = f;
+#pragma unroll
+    for (int k = 16; k; k >>= 1) w += __shfl_xor(w, k);
+    for (int s0 = 0; s0 < a.nsplit; s0 += 8) {
+        if (s0 > 0) load(s0);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float fe = __shfl(f, 32 * g + ((s0 + e) & 31));
+            if (s0 + e < a.nsplit && fe != 0.f) o += v[e] * fe;
+        }
     }
-    if (a.lse && lane == 0) a.lse[r] = w == 0.f ? neg_inf() : (m + __builtin_amdgcn_logf(w)) * kLn2;
+    const float inv = w > 0.f ? 1.f / w : w;
+    if (in) {
+        out4 y;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[e] = (T)(o[e] * inv);
+        *(out4*)((T*)a.out + r * a.D + d) = y;
+    }
+    if (live && a.lse && i == 0) a.lse[r] = w == 0.f ? neg_inf() : (m + __builtin_amdgcn_logf(w)) * kLn2;
 }
 
 template <int DP>
@@ -309,7 +331,7 @@ hipError_t launch_attn_fwd_bf16(const AttnArgs& a, hipStream_t s) {
 }
 
 hipError_t launch_attn_join(const AttnArgs& a, bool f32, hipStream_t s) {
-    const int64_t grid = (a.N * a.H + 3) / 4;
+    const int64_t grid = (a.N * a.H + 7) / 8;
     if (grid == 0) return hipSuccess;
     if (grid > 0x7fffffff) return hipErrorInvalidValue;
     if (f32)
