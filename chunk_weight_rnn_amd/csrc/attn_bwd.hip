@@ -97,10 +97,6 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(AttnBwdArgs a) {
     }
     delta += other_half(delta, lane);
     const float lse2 = live ? a.lse[at] * kLog2e : 0.f;
-    if (live && g == 0) {  // what the other kernel's accumulators start from
-        a.stats[at] = -lse2 / a.sl2;
-        a.stats[a.N * a.H + at] = -delta;
-    }
 
     const char* ksrc = (const char*)a.k + 2 * (it.tok0 * a.k_tok + kvh * a.k_head);
     const char* vsrc = (const char*)a.v + 2 * (it.tok0 * a.v_tok + kvh * a.v_head);
@@ -135,45 +131,75 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(AttnBwdArgs a) {
     const int wlast = div_group(wr0 + 31 < rows ? wr0 + 31 : rows - 1, G, a.gmagic);
     const bool wlive = wr0 < rows;
 
-    copy_tile(0, 0);
-    for (int j = 0; j < nb; ++j) {
-        const int stage = j & 1;
-        wait_vm<0>();
-        barrier_lds();
-        if (j + 1 < nb) copy_tile(j + 1, stage ^ 1);
+    // whether this wave's rows see anything of tile j
+    auto sees = [&](int j) {
         const int p0 = lo + j * BN;
-        if (!wlive || p0 > wlast || (a.window > 0 && p0 + BN - 1 <= wfirst - a.window)) continue;
-        const unsigned char *kt = lds[0][0], *vt = lds[0][1];
-        const unsigned rb = rb0 + stage * (2 * TILE), tb = tb0 + stage * (2 * TILE);
-        const bool edge = p0 + BN - 1 > wfirst || (a.window > 0 && p0 <= wlast - a.window) || wr0 + 32 > rows;
+        return wlive && p0 <= wlast && !(a.window > 0 && p0 + BN - 1 <= wfirst - a.window);
+    };
+    // sc = p (dp - minus) of half h of tile j, zero where masked
+    f32x16 sc;
+    auto gradients = [&](int j, int h, float minus) {
+        const int p0 = lo + j * BN;
+        const unsigned rb = rb0 + (j & 1) * (2 * TILE);
+        f32x16 dp = {};
+        sc = f32x16{};
+        read_ahead<2 * KS, 4>([&](auto n) { return row_frag(lds[0][n % 2] + h * (64 * DP), rb, n / 2); },
+                              [&](auto n, bf16x8 f) {
+                                  if constexpr (n % 2 == 0) sc = mfma32(f, qf[n / 2], sc);
+                                  else dp = mfma32(f, df[n / 2], dp);
+                              });
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            f32x16 sc = {}, dp = {};
+        for (int i = 0; i < 16; ++i)
+            sc[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[i], a.sl2, -lse2)) * (dp[i] - minus);
+        if (p0 + BN - 1 > wfirst || (a.window > 0 && p0 <= wlast - a.window) || wr0 + 32 > rows) {
 #pragma unroll
-            for (int s = 0; s < KS; ++s) {
-                sc = mfma32(row_frag(kt + h * (64 * DP), rb, s), qf[s], sc);
-                dp = mfma32(row_frag(vt + h * (64 * DP), rb, s), df[s], dp);
-            }
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-                sc[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[i], a.sl2, -lse2)) * (dp[i] - delta);
-            if (edge) {
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const int p = p0 + 32 * h + acc_row(i, g);
-                    if (p > qpos || p <= qlow) sc[i] = 0.f;
-                }
-            }
-#pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                const bf16x8 sf = pack_half(sc, s);
-#pragma unroll
-                for (int dt = 0; dt < DT; ++dt)
-                    acc[dt] = mfma32(tr_frag<DP>(kt + (2 * h + s) * (32 * DP), tb, dt), sf, acc[dt]);
+            for (int i = 0; i < 16; ++i) {
+                const int p = p0 + 32 * h + acc_row(i, g);
+                if (p > qpos || p <= qlow) sc[i] = 0.f;
             }
         }
+    };
+
+    copy_tile(0, 0);
+    if (nb <= 2) {
+        // Rows that see few keys: delta = sum_j p_ij dp_ij, from the same fp32
+        // products.  <dout, out> takes out as it was rounded to bf16, an error
+        // that matters where few keys leave out about as large as a value; over
+        // more keys out shrinks, and the error with it.
+        if (nb == 2) copy_tile(1, 1);
+        wait_vm<0>();
+        barrier_lds();
+        delta = 0.f;
+#pragma unroll 1
+        for (int jh = 0; jh < 2 * nb; ++jh) {
+            if (!sees(jh >> 1)) continue;
+            gradients(jh >> 1, jh & 1, 0.f);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) delta += sc[i];
+        }
+        delta += other_half(delta, lane);
     }
-    if (live) store_row<DT>((__bf16*)a.dq + at * a.D, acc, a.scale, g, a.D);
+    for (int j = 0; j < nb; ++j) {
+        wait_vm<0>();
+        barrier_lds();
+        if (j + 1 < nb) copy_tile(j + 1, (j + 1) & 1);
+        if (!sees(j)) continue;
+        const unsigned char* kt = lds[0][0];
+        const unsigned tb = tb0 + (j & 1) * (2 * TILE);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            gradients(j, h, delta);
+            const bf16x8 sf[2] = {pack_half(sc, 0), pack_half(sc, 1)};
+            read_ahead<2 * DT, 4>([&](auto n) { return tr_frag<DP>(kt + (2 * h + n / DT) * (32 * DP), tb, n % DT); },
+                                  [&](auto n, bf16x8 f) { acc[n % DT] = mfma32(f, sf[n / DT], acc[n % DT]); });
+        }
+    }
+    if (!live) return;
+    if (g == 0) {  // what the other kernel's accumulators start from
+        a.stats[at] = -lse2 / a.sl2;
+        a.stats[a.N * a.H + at] = -delta;
+    }
+    store_row<DT>((__bf16*)a.dq + at * a.D, acc, a.scale, g, a.D);
 }
 
 // 64 keys per workgroup, over tiles of 64 RW rows: wave (kw, rw) takes 32 keys
