@@ -194,6 +194,25 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(AttnBwdArgs a) {
                                   [&](auto n, bf16x8 f) { acc[n % DT] = mfma32(f, sf[n / DT], acc[n % DT]); });
         }
     }
+    // a wave on the edge of the mask whose sums are not finite (attn_common.h)
+    if (wlive && (lo + nb * BN > wfirst + 1 || (a.window > 0 && lo <= wlast - a.window))) {
+        const float bad = not_finite(acc);
+        if (__any(bad != bad && lse2 == lse2 && delta == delta)) {
+#pragma unroll
+            for (int dt = 0; dt < DT; ++dt) acc[dt] = f32x16{};
+            int ln = lane;  // opaque, so that nothing is shared with the loop above
+            asm volatile("" : "+v"(ln));
+            const char* qp = (const char*)a.q + 2 * (qtok * a.q_tok + (int64_t)head * a.q_head);
+            const char* op = (const char*)a.dout + 2 * at * a.D;
+#pragma unroll 1
+            for (int p = lo; p <= wlast; ++p) {
+                const char* kp = ksrc + (int64_t)p * a.k_tok * 2;
+                const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(dot_rows<DP>(kp, qp, a.D, ln), a.sl2, -lse2));
+                const float y = x * (dot_rows<DP>(vsrc + (int64_t)p * a.v_tok * 2, op, a.D, ln) - delta);
+                add_row<DP>(acc, kp, p > qpos || p <= qlow ? 0.f : to_bf16(y), a.D, ln);
+            }
+        }
+    }
     if (!live) return;
     if (g == 0) {  // what the other kernel's accumulators start from
         a.stats[at] = -lse2 / a.sl2;
@@ -383,6 +402,40 @@ __global__ __launch_bounds__(128 * RW, 2) void attn_dkdv_kernel(AttnBwdArgs a) {
                                   if constexpr (n % 2 == 0) dv[dt] = mfma32(f, pf[s], dv[dt]);
                                   else dk[dt] = mfma32(f, sf[s], dk[dt]);
                               });
+    }
+    // Sums that are not finite (attn_common.h): every block has its keys' own
+    // rows on the edge of the mask.  (Everything is computed and loaded anew
+    // from an opaque lane number: what this path shared with the loop above
+    // would cost that registers, and a spilled fragment there waits for every
+    // copy in flight.)
+    if (wlive) {
+        const float bad = not_finite(dk) + not_finite(dv);
+        if (__any(bad != bad)) {
+            int ln = threadIdx.x & 63;
+            asm volatile("" : "+v"(ln));
+            const int ky = k0 + 32 * kw + (ln & 31);
+            const bool lv = ky < it.n;
+            const int lo = lv ? ky * G : 0x7fffffff;
+            const int64_t h64 = a.window > 0 ? ((int64_t)ky + a.window) * G : rows;
+            const int hi = h64 < rows ? (int)h64 : rows;
+            const char* kp = (const char*)a.k + 2 * ((it.tok0 + (lv ? ky : 0)) * a.k_tok + (int64_t)kvh * a.k_head);
+            const char* vp = (const char*)a.v + 2 * ((it.tok0 + (lv ? ky : 0)) * a.v_tok + (int64_t)kvh * a.v_head);
+#pragma unroll
+            for (int dt = 0; dt < DT; ++dt) dk[dt] = dv[dt] = f32x16{};
+#pragma unroll 1
+            for (int r = rbeg; r < rend; ++r) {
+                if (((r - rbeg) / 32) % RW != rw) continue;
+                const int tk = div_group(r, G, a.gmagic), hg = r - tk * G;
+                const int64_t at = first_row + (int64_t)tk * a.H + hg;
+                const char* qp = qsrc + 2 * (tk * a.q_tok + hg * a.q_head);
+                const char* op = (const char*)a.dout + 2 * at * a.D;
+                const float x = __builtin_amdgcn_exp2f((dot_rows<DP>(qp, kp, a.D, ln) + a.stats[at]) * a.sl2);
+                const float y = x * (dot_rows<DP>(op, vp, a.D, ln) + a.stats[a.N * a.H + at]);
+                const bool out = r < lo || r >= hi;
+                add_row<DP>(dv, op, out ? 0.f : to_bf16(x), a.D, ln);
+                add_row<DP>(dk, qp, out ? 0.f : to_bf16(y), a.D, ln);
+            }
+        }
     }
     float* area = (float*)&lds[0][0][0] + (32 * kw + col) * OLD + 4 * g;
 #pragma unroll

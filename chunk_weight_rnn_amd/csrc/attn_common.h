@@ -304,6 +304,58 @@ __device__ __forceinline__ bf16x8 pack_half(const f32x16& x, int hs) {
 
 static __device__ __align__(256) unsigned char zeros[256];  // read in place of rows outside a sequence
 
+// ------------------------------------------- NaN and Inf in masked places
+// A masked key has weight 0, but the matrix unit computes 0 * NaN: a NaN or Inf
+// in a key or value would reach rows that do not see it, wherever both lie in
+// one tile.  Rows outside a sequence and positions that no row of a tile sees
+// are zeros in the LDS; what is left are the tiles on the edge of a mask.  So a
+// wave that walked over such a tile looks at its sums, and if one of them is not
+// finite, and only then, it computes its sums again, term by term from memory
+// and without the masked terms.
+
+// NaN if a value is not finite, else zero.
+template <int DT, class V>
+__device__ __forceinline__ float not_finite(const V (&acc)[DT]) {
+    float t = 0.f;
+#pragma unroll
+    for (int dt = 0; dt < DT; ++dt)
+#pragma unroll
+        for (int i = 0; i < (int)(sizeof(V) / 4); ++i) t = __builtin_fmaf(acc[dt][i], 0.f, t);
+    return t;
+}
+
+// <row, mine>: mine is this lane's column's own row; each lane half takes half
+// of the chunks.
+template <int DP>
+__device__ __forceinline__ float dot_rows(const char* row, const char* mine, int D, int lane) {
+    float t = 0.f;
+#pragma unroll 1
+    for (int c = lane >> 5; c < D / 8; c += 2) {
+        const bf16x8 x = *(const bf16x8*)(row + 16 * c), y = *(const bf16x8*)(mine + 16 * c);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) t = __builtin_fmaf((float)x[e], (float)y[e], t);
+    }
+    return t + other_half(t, lane);
+}
+
+// acc += w row, where w is not zero.
+template <int DP>
+__device__ __forceinline__ void add_row(f32x16 (&acc)[DP / 32], const char* row, float w, int D, int lane) {
+#pragma unroll
+    for (int dt = 0; dt < DP / 32; ++dt)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int d = 32 * dt + 8 * j + 4 * (lane >> 5);
+            if (w == 0.f || d >= D) continue;
+            const bf16x4 x = *(const bf16x4*)(row + 2 * d);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[dt][4 * j + e] = __builtin_fmaf(w, (float)x[e], acc[dt][4 * j + e]);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+}
+
+__device__ __forceinline__ float to_bf16(float x) { return (float)(__bf16)x; }
+
 // ------------------------------------------------------- copies to the LDS
 // dword 3 of a raw buffer resource (gfx9 family: 32-bit data format, no swizzle)
 constexpr int RSRC_W3 = 0x00020000;
@@ -415,6 +467,16 @@ struct PageCopy {
         }
 #pragma unroll
         for (int i = 0; i < NI; ++i) page[i] = page_of(a, table, p0 + row0 + RPI * i + (int)(threadIdx.x & 63) / CH);
+    }
+    // The key or value of one position.
+    template <bool V>
+    __device__ __forceinline__ const char* row(const AttnArgs& a, const int* table, int pos) const {
+        if (pos < begin || pos >= end) return (const char*)zeros;
+        if (pos >= fresh) return (V ? vn : kn) + 2 * (pos - fresh) * (V ? a.v_tok : a.k_tok);
+        const int p = page_of(a, table, pos);
+        if ((unsigned)p >= (unsigned)a.pg.pages) return (const char*)zeros;
+        const int64_t slot = pos & ((1 << a.pg.shift) - 1);
+        return (V ? vc : kc) + 2 * (p * (V ? a.pg.v_page : a.pg.k_page) + slot * (V ? a.pg.v_slot : a.pg.k_slot));
     }
     // Keys (V = false) or values from position p0 on; page(i): the page of this
     // lane's row of instruction i.

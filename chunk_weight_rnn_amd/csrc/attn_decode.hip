@@ -244,6 +244,22 @@ __global__ __launch_bounds__(256, 1) void attn_decode_kernel(AttnArgs a, int gro
             }
         }
         l += other_half(l, lane);
+        // rows of more than one position whose sums are not finite (attn_common.h)
+        if (first != last) {
+            const float bad = not_finite(acc);
+            if (__any(bad != bad && l == l)) {
+                const float mu = m == neg_inf() ? 0.f : m;
+#pragma unroll
+                for (int dt = 0; dt < DT; ++dt) acc[dt] = f32x16{};
+#pragma unroll 1
+                for (int i = b0 * BW; i < b1 * BW; ++i) {
+                    const int p = w.lo + i / BW * UNIT + BW * wave + i % BW;
+                    const char *kp = pc.template row<false>(a, table, p), *vp = pc.template row<true>(a, table, p);
+                    const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(dot_rows<DP>(kp, (const char*)qp, a.D, lane), a.sl2, -mu));
+                    add_row<DP>(acc, vp, p > qpos || p <= qlow ? 0.f : to_bf16(x), a.D, lane);
+                }
+            }
+        }
 
         // the four waves together
         if (g == 0) {

@@ -81,6 +81,35 @@ __device__ __forceinline__ void load_row(f32x4 (&f)[DP / 16], const float* p, bo
     }
 }
 
+// <row, f> for this lane's column, and acc += w row where w is not zero: the
+// terms of sums that are not finite (attn_common.h).
+template <int S4>
+__device__ __forceinline__ float dot_row4(const float* row, const f32x4 (&f)[S4], int u, int D) {
+    float t = 0.f;
+#pragma unroll
+    for (int s = 0; s < S4; ++s) {
+        const int d = 16 * s + 4 * u;
+        if (d >= D) continue;
+        const f32x4 x = *(const f32x4*)(row + d);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) t = __builtin_fmaf(x[e], f[s][e], t);
+        __builtin_amdgcn_sched_barrier(0);  // a rare path: few registers rather than overlap
+    }
+    return groups_sum(t);
+}
+template <int S4>
+__device__ __forceinline__ void add_row4(f32x4 (&acc)[S4], const float* row, float w, int u, int D) {
+#pragma unroll
+    for (int dt = 0; dt < S4; ++dt) {
+        const int d = 16 * dt + 4 * u;
+        if (w == 0.f || d >= D) continue;
+        const f32x4 x = *(const f32x4*)(row + d);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[dt][e] = __builtin_fmaf(w, x[e], acc[dt][e]);
+        __builtin_amdgcn_sched_barrier(0);
+    }
+}
+
 template <int DP, int DT>
 __device__ __forceinline__ void store_cols(float* o, const f32x4 (&acc)[DT], float f, int u, int D) {
 #pragma unroll
@@ -138,27 +167,33 @@ __global__ __launch_bounds__(256, 2) void attn_f32_fwd_kernel(AttnArgs a) {
     const float* ksrc = (const float*)a.k + it.tok0 * a.k_tok + kvh * a.k_head;
     const float* vsrc = (const float*)a.v + it.tok0 * a.v_tok + kvh * a.v_head;
     const int fresh = PAGED ? (a.pg.append ? kept : 0x7fffffff) : 0;
+    // key and value of a position; null where it is read as zeros
+    auto rows_of = [&](int pos, const float*& kp, const float*& vp) {
+        kp = vp = nullptr;
+        if (pos < begin || pos > last) return;
+        if (!PAGED || pos >= fresh) {
+            kp = ksrc + (int64_t)(pos - fresh) * a.k_tok;
+            vp = vsrc + (int64_t)(pos - fresh) * a.v_tok;
+            return;
+        }
+        const int pi = pos >> a.pg.shift;
+        const int page = pi < a.pg.wide ? a.pg.table[(int64_t)it.seq * a.pg.wide + pi] : -1;
+        if ((unsigned)page >= (unsigned)a.pg.pages) return;
+        const int64_t slot = pos & ((1 << a.pg.shift) - 1);
+        kp = (const float*)a.pg.kc + page * a.pg.k_page + kvh * a.pg.k_head + slot * a.pg.k_slot;
+        vp = (const float*)a.pg.vc + page * a.pg.v_page + kvh * a.pg.v_head + slot * a.pg.v_slot;
+    };
     f32x4 kr[TL::U], vr[TL::U];
     auto load_tile = [&](int j) {
 #pragma unroll
         for (int i = 0; i < TL::U; ++i) {
             const int x = i * 256 + threadIdx.x;
-            const int pos = lo + j * BN + x / (DP / 4), c = x % (DP / 4) * 4;
+            const int c = x % (DP / 4) * 4;
+            const float *kp, *vp;
+            rows_of(lo + j * BN + x / (DP / 4), kp, vp);
             f32x4 z = {};
-            kr[i] = vr[i] = z;
-            if (pos < begin || pos > last || c >= a.D) continue;
-            if (!PAGED || pos >= fresh) {
-                kr[i] = *(const f32x4*)(ksrc + (int64_t)(pos - fresh) * a.k_tok + c);
-                vr[i] = *(const f32x4*)(vsrc + (int64_t)(pos - fresh) * a.v_tok + c);
-            } else {
-                const int pi = pos >> a.pg.shift;
-                const int page = pi < a.pg.wide ? a.pg.table[(int64_t)it.seq * a.pg.wide + pi] : -1;
-                if ((unsigned)page < (unsigned)a.pg.pages) {
-                    const int64_t slot = pos & ((1 << a.pg.shift) - 1);
-                    kr[i] = *(const f32x4*)((const float*)a.pg.kc + page * a.pg.k_page + kvh * a.pg.k_head + slot * a.pg.k_slot + c);
-                    vr[i] = *(const f32x4*)((const float*)a.pg.vc + page * a.pg.v_page + kvh * a.pg.v_head + slot * a.pg.v_slot + c);
-                }
-            }
+            kr[i] = kp && c < a.D ? *(const f32x4*)(kp + c) : z;
+            vr[i] = vp && c < a.D ? *(const f32x4*)(vp + c) : z;
         }
     };
 
@@ -217,6 +252,26 @@ __global__ __launch_bounds__(256, 2) void attn_f32_fwd_kernel(AttnArgs a) {
             for (int dt = 0; dt < S4; ++dt) acc[dt] = mfma4(vf.v[i][dt], sc[i], acc[dt]);
     }
     l = groups_sum(l);
+    // keys of this wave, position by position, where its sums are not finite
+    auto wave_keys = [&](int first_tile, int tiles, auto&& f) {
+#pragma unroll 1
+        for (int i = first_tile * 16; i < tiles * 16; ++i) f(lo + i / 16 * BN + 16 * wave + i % 16);
+    };
+    if (j0 < j1 && first != last) {
+        const float bad = not_finite(acc);
+        if (__any(bad != bad && l == l)) {
+            const float mu = m == neg_inf() ? 0.f : m;
+#pragma unroll
+            for (int dt = 0; dt < S4; ++dt) acc[dt] = f32x4{};
+            wave_keys(j0, j1, [&](int p) {
+                const float *kp, *vp;
+                rows_of(p, kp, vp);
+                if (!kp) return;
+                const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(dot_row4(kp, qf, u, a.D), a.sl2, -mu));
+                add_row4(acc, vp, p > qpos || p <= qlow ? 0.f : x, u, a.D);
+            });
+        }
+    }
     // the four waves together
     __syncthreads();
     float* area = kts[0].v + (16 * wave + col) * TL::LD + 4 * u;
@@ -350,6 +405,22 @@ __global__ __launch_bounds__(256, 2) void attn_f32_dq_kernel(AttnBwdArgs a) {
 #pragma unroll
             for (int dt = 0; dt < S4; ++dt) acc[dt] = mfma4(kc.v[i][dt], sc[i], acc[dt]);
     }
+    if (first != last) {  // sums that are not finite, as in the forward
+        const float bad = not_finite(acc);
+        if (__any(bad != bad && lse2 == lse2 && delta == delta)) {
+#pragma unroll
+            for (int dt = 0; dt < S4; ++dt) acc[dt] = f32x4{};
+#pragma unroll 1
+            for (int i = 0; i < nb * 16; ++i) {
+                const int p = lo + i / 16 * BN + 16 * wave + i % 16;
+                if (p < begin || p > last) continue;
+                const float* kp = ksrc + p * a.k_tok;
+                const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(dot_row4(kp, qf, u, a.D), a.sl2, -lse2));
+                const float y = x * (dot_row4(vsrc + p * a.v_tok, df, u, a.D) - delta);
+                add_row4(acc, kp, p > qpos || p <= qlow ? 0.f : y, u, a.D);
+            }
+        }
+    }
     __syncthreads();
     float* area = kts[0].v + (16 * wave + col) * TL::LD + 4 * u;
 #pragma unroll
@@ -467,6 +538,24 @@ __global__ __launch_bounds__(512, 2) void attn_f32_dkdv_kernel(AttnBwdArgs a) {
                 dv[dt] = mfma4(dc.v[i][dt], sc[i], dv[dt]);
                 dk[dt] = mfma4(qc.v[i][dt], dp[i], dk[dt]);
             }
+    }
+    const float bad = not_finite(dk) + not_finite(dv);
+    if (__any(bad != bad)) {  // as in the forward
+#pragma unroll
+        for (int dt = 0; dt < S4; ++dt) dk[dt] = dv[dt] = f32x4{};
+#pragma unroll 1
+        for (int i = 0; i < nb * 16; ++i) {
+            const int r = rbeg + i / 16 * BR + 16 * wave + i % 16;
+            if (r >= rend) continue;
+            const int tk = div_group(r, G, a.gmagic), hg = r - tk * G;
+            const int64_t at = first_row + (int64_t)tk * a.H + hg;
+            const float *qp = qsrc + tk * a.q_tok + hg * a.q_head, *op = (const float*)a.dout + at * a.D;
+            const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(dot_row4(qp, kf, u, a.D), a.sl2, -a.lse[at] * kLog2e));
+            const float y = x * (dot_row4(op, vf, u, a.D) - a.stats[at]);
+            const bool out = r < rlo || r >= rhi;
+            add_row4(dv, op, out ? 0.f : x, u, a.D);
+            add_row4(dk, qp, out ? 0.f : y, u, a.D);
+        }
     }
     // the eight parts of the rows together, in order
     __syncthreads();

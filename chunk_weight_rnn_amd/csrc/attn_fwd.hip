@@ -37,7 +37,7 @@ struct CopyPlan {
 };
 
 template <int DP, bool PAGED, bool SPLIT>
-__global__ __launch_bounds__(256, 2) void attn_fwd_kernel(AttnArgs a) {
+__global__ __launch_bounds__(256, DP == 64 ? 4 : 2) void attn_fwd_kernel(AttnArgs a) {
     constexpr int TILE = BN * DP * 2;
     constexpr int KS = DP / 16, DT = DP / 32;
     using P = CopyPlan<DP>;
@@ -217,6 +217,30 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(AttnArgs a) {
     }
 
     l += other_half(l, lane);
+    // a wave on the edge of the mask whose scores are fine and whose sums are not
+    if (wlive && j0 < j1 && (lo + j1 * BN > wfirst + 1 || (a.window > 0 && lo + j0 * BN <= wlast - a.window))) {
+        const float bad = not_finite(acc);
+        if (__any(bad != bad && l == l)) {
+            const int end = lo + j1 * BN < wlast + 1 ? lo + j1 * BN : wlast + 1;
+            const float mu = m == neg_inf() ? 0.f : m;
+#pragma unroll
+            for (int dt = 0; dt < DT; ++dt) acc[dt] = f32x16{};
+            const char* qp = (const char*)a.q + 2 * (qtok * a.q_tok + (int64_t)head * a.q_head);
+#pragma unroll 1
+            for (int p = lo + j0 * BN; p < end; ++p) {
+                const char *kp, *vp;
+                if constexpr (PAGED) {
+                    kp = pc.template row<false>(a, table, p);
+                    vp = pc.template row<true>(a, table, p);
+                } else {
+                    kp = ksrc + (int64_t)p * a.k_tok * 2;
+                    vp = vsrc + (int64_t)p * a.v_tok * 2;
+                }
+                const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(dot_rows<DP>(kp, qp, a.D, lane), a.sl2, -mu));
+                add_row<DP>(acc, vp, p > qpos || p <= qlow ? 0.f : to_bf16(x), a.D, lane);
+            }
+        }
+    }
     if (!live) return;
     const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // a row that sees nothing gives 0; NaN stays
     if (SPLIT) {

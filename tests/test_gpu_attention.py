@@ -171,6 +171,53 @@ def test_a_sequence_does_not_reach_its_neighbours():
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("H,K,D,window", [(4, 2, 64, 0), (2, 2, 128, 50), (8, 1, 96, 0)])
+@pytest.mark.parametrize("what", ["v_nan", "v_inf", "k_nan", "q_nan", "dout_inf"])
+def test_not_finite_values_in_masked_places(what, H, K, D, window, dtype):
+    """A NaN or Inf reaches the results that depend on it and no others: what
+    the masked terms would bring stays out, exactly as without them."""
+    import chunk_weight_rnn_amd as e2
+    n, at = 190, 100
+    note(f"not finite: {what} H={H} K={K} D={D} window={window} {dtype}")
+    q, k, v, dout = make([n], H, K, D, dtype, seed=3, view=False)
+    cu = offsets([n])
+    x = {"v_nan": v, "v_inf": v, "k_nan": k, "q_nan": q, "dout_inf": dout}[what]
+    x[at, 0, 5] = float("inf") if what.endswith("inf") else float("nan")
+    out, lse = e2.attention_forward(q, k, v, cu, window=window)
+    g = e2.attention_backward(q, k, v, out, lse, dout, cu, window=window)
+    x[at, 0, 5] = 1.0  # what does not depend on the value may be compared with any other
+    val, bnd = ref.packed(f64(q), f64(k), f64(v), [n], window, D ** -0.5, dtype, f64(dout))
+    # what each result depends on, by position
+    i = np.arange(n)
+    sees = (i >= at) & ((i < at + window) if window else True)   # queries that see position `at`
+    seen = (i <= at) & ((i > at - window) if window else True)   # keys that it sees
+    G = H // K
+    clean = {}
+    if what[0] in "vk":
+        hit = np.zeros((n, H), bool)
+        hit[sees, :G] = True
+        clean["out"] = ~hit
+        clean["dq"] = ~hit
+        # a key's gradients come from every row that sees it and is hit
+        key_hit = np.array([any(sees[r] for r in range(j, min(n, j + window) if window else n)) for j in range(n)])
+        clean["dk"] = clean["dv"] = ~np.stack([key_hit if h == 0 else np.zeros(n, bool) for h in range(K)], 1)
+        if what[0] == "v":
+            clean["dv"] = np.ones((n, K), bool)  # dv does not depend on v
+    else:
+        hit = np.zeros((n, H), bool)
+        hit[at, 0] = True
+        clean["out"] = ~hit if what == "q_nan" else np.ones((n, H), bool)
+        clean["dq"] = ~hit
+        clean["dk"] = clean["dv"] = ~np.stack([seen if h == 0 else np.zeros(n, bool) for h in range(K)], 1)
+    for name, t in (("out", out), ("dq", g["q"]), ("dk", g["k"]), ("dv", g["v"])):
+        c = clean[name]
+        got = f64(t)
+        assert np.isfinite(got[c]).all(), f"{what}: {name} is not finite where it should be"
+        assert (np.abs(got[c] - val[name][c]) <= bnd[name][c]).all(), f"{what}: {name}"
+    assert not np.isfinite(f64(out)[at, 0]).all() or what == "dout_inf"
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_autograd_and_differences(dtype):
     """attention() under torch.autograd gives attention_backward's gradients; in
     fp32 they also match central differences of the forward along a random

@@ -118,6 +118,25 @@ def test_new_tokens_already_in_the_cache(dtype):
     check([50, 0, 200], [1, 20, 64], 4, 2, 64, 16, dtype, append=False)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("new", [3, 100])
+def test_not_finite_new_tokens_do_not_reach_earlier_ones(new, dtype):
+    """A NaN in one new token's value or key leaves the rows before it as they are."""
+    import chunk_weight_rnn_amd as e2
+    for which in ("k", "v"):
+        m = make([70], [new], 4, 2, 64, 16, dtype)
+        run = lambda: e2.paged_attention(m["q"], m["k"], m["v"], m["kc"], m["vc"], m["table"], m["cu"], m["cached"])
+        want = run()
+        m[which][new // 2, 0, 7] = float("nan")
+        got = run()
+        note(f"not finite: new={new} {dtype} {which}")
+        assert torch.isnan(got[new // 2:, :2]).any(-1).all()  # the two query heads of that key head
+        assert torch.isfinite(got[:new // 2]).all() and torch.isfinite(got[:, 2:]).all()
+        # the same sums, term by term where the fast ones were not finite
+        assert (got[:new // 2].float() - want[:new // 2].float()).abs().max() <= 2 ** -6
+        assert torch.equal(got[:, 2:], want[:, 2:])
+
+
 def test_many_sequences():
     check([(i * 37) % 90 for i in range(140)], [1 + (i % 3 == 0) for i in range(140)], 2, 1, 32, 16, "bf16")
 
