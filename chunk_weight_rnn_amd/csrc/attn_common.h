@@ -250,21 +250,16 @@ __device__ __forceinline__ bf16x8 tr_frag(const unsigned char* lds, unsigned tb,
     return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
-// N products with the fragments of each read AHEAD products before it, and
-// between(n) after the n-th, in this order.  (Left to itself the compiler, short
-// of registers, reads every fragment into the same ones and waits for it.)
-struct Nothing {
-    template <class T>
-    __device__ __forceinline__ void operator()(T) const {}
-};
-template <int N, int AHEAD, class R, class M, class B = Nothing>
-__device__ __forceinline__ void read_ahead(R&& read, M&& product, B&& between = Nothing{}) {
+// N products with the fragments of each read AHEAD products before it, in this
+// order.  (Left to itself the compiler, short of registers, reads every fragment
+// into the same ones and waits for it.)
+template <int N, int AHEAD, class R, class M>
+__device__ __forceinline__ void read_ahead(R&& read, M&& product) {
     bf16x8 f[AHEAD];
     static_for<(AHEAD < N ? AHEAD : N)>([&](auto n) { f[n] = read(n); });
     static_for<N>([&](auto n) {
         product(n, f[n % AHEAD]);
         if constexpr (n + AHEAD < N) f[n % AHEAD] = read(std::integral_constant<int, n + AHEAD>{});
-        between(n);
         __builtin_amdgcn_sched_barrier(0);
     });
 }
@@ -478,29 +473,32 @@ struct PageCopy {
         const int64_t slot = pos & ((1 << a.pg.shift) - 1);
         return (V ? vc : kc) + 2 * (p * (V ? a.pg.v_page : a.pg.k_page) + slot * (V ? a.pg.v_slot : a.pg.k_slot));
     }
-    // Keys (V = false) or values from position p0 on; page(i): the page of this
-    // lane's row of instruction i.
-    template <bool V, class F>
-    __device__ __forceinline__ void copy(const AttnArgs& a, int p0, unsigned dst, F&& page) const {
+    // Keys and values from position p0 on; page(i): the page of this lane's row
+    // of instruction i.
+    template <class F>
+    __device__ __forceinline__ void copy(const AttnArgs& a, int p0, unsigned kdst, unsigned vdst, F&& page) const {
         const int mask = (1 << a.pg.shift) - 1;
-        const int64_t slot_stride = V ? a.pg.v_slot : a.pg.k_slot, page_stride = V ? a.pg.v_page : a.pg.k_page;
-        const char* cache = V ? vc : kc;
-        const unsigned(&off)[NI] = V ? vo : ko;
         if (p0 >= begin && p0 + T <= end && p0 + T <= fresh) {
-            const char* cb = cache + (int64_t)(p0 & mask) * slot_stride * 2;
-            const unsigned ps = (unsigned)page_stride * 2;
+            const char* kb = kc + (int64_t)(p0 & mask) * a.pg.k_slot * 2;
+            const char* vb = vc + (int64_t)(p0 & mask) * a.pg.v_slot * 2;
+            const unsigned kp = (unsigned)a.pg.k_page * 2, vp = (unsigned)a.pg.v_page * 2;
             if (mask + 1 >= T) {
                 const unsigned p = (unsigned)__builtin_amdgcn_readfirstlane(page(0));
-                const u32x4 r = buffer_rsrc(cb + (uint64_t)p * ps, p < (unsigned)a.pg.pages ? (int)kOutside : 0);
+                const int size = p < (unsigned)a.pg.pages ? (int)kOutside : 0;
+                const u32x4 kr = buffer_rsrc(kb + (uint64_t)p * kp, size), vr = buffer_rsrc(vb + (uint64_t)p * vp, size);
 #pragma unroll
-                for (int i = 0; i < NI; ++i) copy16(r, dst + 1024 * i, off[i]);
+                for (int i = 0; i < NI; ++i) {
+                    copy16(kr, kdst + 1024 * i, ko[i]);
+                    copy16(vr, vdst + 1024 * i, vo[i]);
+                }
                 return;
             }
 #pragma unroll
             for (int i = 0; i < NI; ++i) {
                 const unsigned p = (unsigned)page(i);
-                const bool ok = p < (unsigned)a.pg.pages && off[i] != kOutside;
-                copy16_at(ok ? cb + ((uint64_t)p * ps + off[i]) : (const char*)zeros, dst + 1024 * i);
+                const bool ok = p < (unsigned)a.pg.pages && ko[i] != kOutside;
+                copy16_at(ok ? kb + ((uint64_t)p * kp + ko[i]) : (const char*)zeros, kdst + 1024 * i);
+                copy16_at(ok ? vb + ((uint64_t)p * vp + vo[i]) : (const char*)zeros, vdst + 1024 * i);
             }
             return;
         }
@@ -510,14 +508,19 @@ struct PageCopy {
             const int r = row0 + RPI * i + lane / CH, pos = p0 + r;
             const int64_t c = 16 * ((lane % CH) ^ swz<DP>(r));
             const int p = page(i);
-            const char* src = (const char*)zeros;
+            const char *kp = (const char*)zeros, *vp = (const char*)zeros;
             if (c < 2 * a.D && pos >= begin && pos < end) {
-                if (pos >= fresh)
-                    src = (V ? vn : kn) + 2 * (pos - fresh) * (V ? a.v_tok : a.k_tok) + c;
-                else if ((unsigned)p < (unsigned)a.pg.pages)
-                    src = cache + 2 * (p * page_stride + (int64_t)(pos & mask) * slot_stride) + c;
+                if (pos >= fresh) {
+                    kp = kn + 2 * (pos - fresh) * a.k_tok + c;
+                    vp = vn + 2 * (pos - fresh) * a.v_tok + c;
+                } else if ((unsigned)p < (unsigned)a.pg.pages) {
+                    const int64_t slot = pos & mask;
+                    kp = kc + 2 * (p * a.pg.k_page + slot * a.pg.k_slot) + c;
+                    vp = vc + 2 * (p * a.pg.v_page + slot * a.pg.v_slot) + c;
+                }
             }
-            copy16_at(src, dst + 1024 * i);
+            copy16_at(kp, kdst + 1024 * i);
+            copy16_at(vp, vdst + 1024 * i);
         }
     }
 };

@@ -178,8 +178,7 @@ __global__ __launch_bounds__(256, 1) void attn_decode_kernel(AttnArgs a, int gro
         auto copy_part = [&](int b) {
             const unsigned dst = base + (b & 1) * (2 * TILE);
             const int* pg = &pages[wave][b & 3][crow];
-            pc.template copy<false>(a, w.lo + b * UNIT + BW * wave, dst, [&](int i) { return pg[RPI * i]; });
-            pc.template copy<true>(a, w.lo + b * UNIT + BW * wave, dst + TILE, [&](int i) { return pg[RPI * i]; });
+            pc.copy(a, w.lo + b * UNIT + BW * wave, dst, dst + TILE, [&](int i) { return pg[RPI * i]; });
         };
 
         f32x16 acc[DT] = {};

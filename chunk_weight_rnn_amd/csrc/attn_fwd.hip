@@ -132,8 +132,7 @@ __global__ __launch_bounds__(256, DP == 64 ? 4 : 2) void attn_fwd_kernel(AttnArg
         const unsigned dst = base + stage * (2 * TILE);
         const int p0 = lo + j * BN;
         if constexpr (PAGED) {
-            pc.template copy<false>(a, p0, dst, [&](int i) { return page[i]; });
-            pc.template copy<true>(a, p0, dst + TILE, [&](int i) { return page[i]; });
+            pc.copy(a, p0, dst, dst + TILE, [&](int i) { return page[i]; });
         } else {
             const int left = last + 1 - p0 < BN ? last + 1 - p0 : BN;  // rows of the tile that exist
             const u32x4 kr = buffer_rsrc(ksrc + (int64_t)p0 * a.k_tok * 2, (int)((left - 1) * a.k_tok * 2) + 2 * a.D);
