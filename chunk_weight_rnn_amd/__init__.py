@@ -36,7 +36,8 @@ from .layer import (attention, attention_backward, attention_forward, norm_backw
                     rms_norm)
 
 __all__ = ["attention", "attention_forward", "attention_backward", "paged_attention", "rms_norm", "norm_forward",
-           "norm_backward", "chunk_forward", "chunk_forward_noalloc", "chunk_backward", "chunk_update", "training_workspace", "logscan", "workspace_size", "param_count", "path", "validate", "E2TTTError",
+           "norm_backward", "chunk_forward", "chunk_forward_noalloc", "chunk_backward", "chunk_update",
+           "training_workspace", "logscan", "workspace_size", "param_count", "path", "validate", "E2TTTError",
            "library"]
 
 

@@ -2,9 +2,11 @@
 include/e2ttt_layer.h.
 
 Argument marshalling only, as in the package's ``__init__``: the work runs in
-the HIP kernels behind the C ABI on the current stream (or ``stream``), with
-tensors that the caller owns; outputs and workspaces that are not given are
-allocated through torch.  CPU tensors raise.
+the HIP kernels behind the C ABI on the current stream, with tensors that the
+caller owns; outputs and workspaces that are not given are allocated through
+torch.  With ``stream`` the call runs as under ``torch.cuda.stream(stream)``:
+what it allocates belongs to that stream, so that no other work reuses a
+workspace before the kernels are done with it.  CPU tensors raise.
 """
 from __future__ import annotations
 
@@ -12,6 +14,7 @@ import ctypes
 from functools import lru_cache
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import _lib
 from ._lib import AttentionDesc, E2TTTError, NormDesc, PagedDesc
@@ -33,16 +36,16 @@ def _device(first, **others) -> int:
     return dev
 
 
-def _call(fn: str, dev: int, stream, *args):
-    """Calls the library on `stream` (default: the current stream of the
-    tensors' device, which is made current for the call if it is not)."""
+def _call(fn: str, dev: int, *args):
+    """Calls the library on the current stream of the tensors' device, which is
+    made current for the call if it is not."""
     if dev != torch._C._cuda_getDevice():
         with torch.cuda.device(dev):
-            return _call(fn, dev, stream, *args)
+            return _call(fn, dev, *args)
     f = _functions.get(fn)
     if f is None:
         f = _functions[fn] = getattr(_lib.load(), fn)
-    st = f(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
+    st = f(*args, torch._C._cuda_getCurrentRawStream(dev))
     if st != 0:
         raise E2TTTError(fn, st)
 
@@ -178,6 +181,9 @@ def attention_forward(q, k, v, cu_seqlens, *, window: int = 0, scale: float | No
     default.  out: [N, H, D]; lse: [N, H] float32, the log of each row's
     softmax sum, which the backward needs.
     """
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return attention_forward(q, k, v, cu_seqlens, window=window, scale=scale, out=out, lse=lse, workspace=workspace)
     dev = _device(q, k=k, v=v, cu_seqlens=cu_seqlens, out=out, lse=lse)
     (N, H, D), desc, need, _, _ = _attention_plan(_layout(q), _layout(k), _layout(v), _layout(cu_seqlens), window, scale)
     if out is None:
@@ -189,7 +195,7 @@ def attention_forward(q, k, v, cu_seqlens, *, window: int = 0, scale: float | No
     else:
         _full("lse", lse, (N, H), torch.float32)
     ws, n = _workspace(workspace, need, q)
-    _call("e2ttt_attention_forward", dev, stream, desc, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+    _call("e2ttt_attention_forward", dev, desc, q.data_ptr(), k.data_ptr(), v.data_ptr(),
           cu_seqlens.data_ptr(), out.data_ptr(), lse.data_ptr(), ws, n)
     return out, lse
 
@@ -198,6 +204,10 @@ def attention_backward(q, k, v, out, lse, dout, cu_seqlens, *, window: int = 0, 
                        workspace=None, stream=None):
     """Gradients of <dout, out> through ``attention_forward``, from its inputs
     and outputs; returns a dict with keys q, k, v (the I/O dtype, contiguous)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return attention_backward(q, k, v, out, lse, dout, cu_seqlens, window=window, scale=scale,
+                                      workspace=workspace)
     dev = _device(q, k=k, v=v, out=out, lse=lse, dout=dout, cu_seqlens=cu_seqlens)
     (N, H, D), desc, _, need, _ = _attention_plan(_layout(q), _layout(k), _layout(v), _layout(cu_seqlens), window, scale)
     _full("out", out, (N, H, D), q.dtype)
@@ -205,7 +215,7 @@ def attention_backward(q, k, v, out, lse, dout, cu_seqlens, *, window: int = 0, 
     _full("lse", lse, (N, H), torch.float32)
     g = {n: torch.empty(t.shape, dtype=q.dtype, device=q.device) for n, t in (("q", q), ("k", k), ("v", v))}
     ws, n = _workspace(workspace, need, q)
-    _call("e2ttt_attention_backward", dev, stream, desc, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
+    _call("e2ttt_attention_backward", dev, desc, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
           lse.data_ptr(), dout.data_ptr(), cu_seqlens.data_ptr(), g["q"].data_ptr(), g["k"].data_ptr(),
           g["v"].data_ptr(), ws, n)
     return g
@@ -220,6 +230,7 @@ class _Attention(torch.autograd.Function):
         return out
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dout):
         q, k, v, out, lse, cu_seqlens = ctx.saved_tensors
         window, scale = ctx.opts
@@ -246,12 +257,16 @@ def paged_attention(q, k, v, k_cache, v_cache, table, cu_seqlens, cached, *, win
     before the call.  New token i of sequence s is at position cached[s] + i.
     With k = v = None the cache holds the new tokens already.
     """
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return paged_attention(q, k, v, k_cache, v_cache, table, cu_seqlens, cached, window=window, scale=scale,
+                                   out=out, workspace=workspace)
     if (k is None) != (v is None):
         raise ValueError("k and v must both be given, or neither")
     dev = _device(q, k=k, v=v, k_cache=k_cache, v_cache=v_cache, table=table, cu_seqlens=cu_seqlens, cached=cached,
                   out=out)
-    (N, H, D), desc, need, _ = _paged_plan(_layout(q), _layout(k), _layout(v), _layout(k_cache), _layout(v_cache), _layout(table),
-                                _layout(cu_seqlens), window, scale)
+    (N, H, D), desc, need, _ = _paged_plan(_layout(q), _layout(k), _layout(v), _layout(k_cache), _layout(v_cache),
+                                           _layout(table), _layout(cu_seqlens), window, scale)
     S = cu_seqlens.shape[0] - 1
     _int32("table", table, (S, table.shape[1]))
     _int32("cached", cached, (S,))
@@ -260,7 +275,7 @@ def paged_attention(q, k, v, k_cache, v_cache, table, cu_seqlens, cached, *, win
     else:
         _full("out", out, (N, H, D), q.dtype)
     ws, n = _workspace(workspace, need, q)
-    _call("e2ttt_paged_attention", dev, stream, desc, q.data_ptr(), _p(k), _p(v), k_cache.data_ptr(),
+    _call("e2ttt_paged_attention", dev, desc, q.data_ptr(), _p(k), _p(v), k_cache.data_ptr(),
           v_cache.data_ptr(), table.data_ptr(), cu_seqlens.data_ptr(), cached.data_ptr(), out.data_ptr(), ws, n)
     return out
 
@@ -272,9 +287,13 @@ def norm_forward(x, weight, *, residual=None, eps: float = 1e-6, bits8: bool = F
     x: [..., W] float32 or bfloat16, contiguous; weight: [W] float32.
     h = x + residual in x's type (x itself without ``residual``; ``h=residual``
     updates the stream in place); rstd: [...] float32, for the backward (None
-    with ``bits8``, which has none).  y = h * rstd * weight in x's type, or with ``bits8`` in float8_e4m3fn, to be
-    multiplied by scale [...] (float32, max|y| / 448 of its row; else None).
+    with ``bits8``, which has none).  y = h * rstd * weight in x's type, or with
+    ``bits8`` in float8_e4m3fn, to be multiplied by scale [...] (float32,
+    max|y| / 448 of its row; else None).
     """
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return norm_forward(x, weight, residual=residual, eps=eps, bits8=bits8, h=h)
     dev = _device(x, weight=weight, residual=residual, h=h)
     lead, desc, _, _ = _norm_plan(x.shape, x.dtype, eps, bits8)
     if not x.is_contiguous():
@@ -295,7 +314,7 @@ def norm_forward(x, weight, *, residual=None, eps: float = 1e-6, bits8: bool = F
     else:
         y = torch.empty_like(x)
         rstd = _row_values(lead, x)
-    _call("e2ttt_norm_forward", dev, stream, desc, x.data_ptr(), _p(residual), weight.data_ptr(), y.data_ptr(),
+    _call("e2ttt_norm_forward", dev, desc, x.data_ptr(), _p(residual), weight.data_ptr(), y.data_ptr(),
           _p(scale), _p(h), _p(rstd))
     return y, scale, (x if residual is None else h), rstd
 
@@ -304,6 +323,9 @@ def norm_backward(dy, h, weight, rstd, *, dh=None, workspace=None, stream=None):
     """Gradients through ``norm_forward`` (y in the stream's type): returns
     (dx, dweight).  dx is the gradient of both x and residual; ``dh`` is what
     arrives at h along the residual stream, added to it."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return norm_backward(dy, h, weight, rstd, dh=dh, workspace=workspace)
     dev = _device(h, dy=dy, weight=weight, rstd=rstd, dh=dh)
     lead, desc, need, _ = _norm_plan(h.shape, h.dtype, 0.0, False)
     _full("h", h, h.shape, h.dtype)
@@ -315,7 +337,7 @@ def norm_backward(dy, h, weight, rstd, *, dh=None, workspace=None, stream=None):
     dx = torch.empty_like(h)
     dweight = torch.empty_like(weight)
     ws, n = _workspace(workspace, need, h)
-    _call("e2ttt_norm_backward", dev, stream, desc, dy.data_ptr(), h.data_ptr(), weight.data_ptr(), rstd.data_ptr(),
+    _call("e2ttt_norm_backward", dev, desc, dy.data_ptr(), h.data_ptr(), weight.data_ptr(), rstd.data_ptr(),
           _p(dh), dx.data_ptr(), dweight.data_ptr(), ws, n)
     return dx, dweight
 
@@ -330,6 +352,7 @@ class _Norm(torch.autograd.Function):
         return (y, h) if ctx.has_residual else (y,)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy, dh=None):
         h, weight, rstd = ctx.saved_tensors
         dy = torch.zeros_like(h) if dy is None else dy

@@ -13,7 +13,7 @@
  * by the caller; the library never allocates, frees or synchronises; work is
  * queued on `stream`; arguments are validated on the host before any device
  * call and the status is returned; no exception crosses the ABI; NaN and Inf
- * propagate.  Statuses and types are those of e2ttt.h.  Every result is the
+ * reach the results that depend on them and, masked, no other.  Statuses and types are those of e2ttt.h.  Every result is the
  * same bit for bit from call to call (no floating-point atomics).
  * What a device tensor holds (offsets, lengths, page indices) cannot be
  * checked on the host: the kernels clamp it, so that bad values give wrong
