@@ -297,7 +297,7 @@ __device__ __forceinline__ bf16x8 pack_half(const f32x16& x, int hs) {
     return r;
 }
 
-static __device__ __align__(256) unsigned char zeros[256];  // read in place of rows outside a sequence
+static __device__ __align__(256) unsigned char zeros[512];  // read in place of rows outside a sequence
 
 // ------------------------------------------- NaN and Inf in masked places
 // A masked key has weight 0, but the matrix unit computes 0 * NaN: a NaN or Inf

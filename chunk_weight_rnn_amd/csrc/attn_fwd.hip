@@ -19,7 +19,7 @@ namespace e2ttt {
 namespace attn {
 namespace {
 
-constexpr int BM = 128;  // rows of a tile: 4 waves x 32
+constexpr int BM = kFwdRows;  // 4 waves x 32
 constexpr int BN = 64;   // keys of a tile
 
 // The running maximum is only raised when a row exceeds it by this many

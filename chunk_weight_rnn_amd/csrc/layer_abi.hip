@@ -104,7 +104,7 @@ AttnArgs make_args(const e2ttt_attention_desc& d) {
 // units idle, the keys of each are split into ranges of at least 256 that run
 // side by side; about two workgroups per compute unit are wanted.
 void plan(AttnArgs& a, bool f32, int64_t longest) {
-    const int bm = attn_fwd_rows(a, f32);
+    const int bm = f32 ? kF32Rows : kFwdRows;
     a.ntiles = (int)(a.N * a.G / bm + a.S);
     a.nsplit = 1;
     const int64_t items = (a.N * a.G + bm - 1) / bm * a.K;  // at least so many do work
@@ -184,9 +184,6 @@ bool norm_desc_ok(const e2ttt_norm_desc* d) {
 bool norm_supported(const e2ttt_norm_desc* d) { return d->width <= 65536 && d->rows <= 0x7fffffff; }
 
 }  // namespace
-
-int attn_fwd_rows(const AttnArgs&, bool f32) { return f32 ? 16 : 128; }
-
 }  // namespace e2ttt
 
 using namespace e2ttt;
@@ -230,9 +227,17 @@ int e2ttt_attention_forward(const e2ttt_attention_desc* d, const void* q, const 
     return run_forward(a, f32, (hipStream_t)stream);
 }
 
+static size_t stats_bytes(const e2ttt_attention_desc& d) {
+    return ((size_t)(d.tokens * d.heads) * 8 + kWsAlign - 1) / kWsAlign * kWsAlign;
+}
+
 size_t e2ttt_attention_backward_workspace_size(const e2ttt_attention_desc* d) {
     if (attention_desc_status(d, true) != E2TTT_OK) return kBad;
-    return (size_t)(d->tokens * d->heads) * 8;
+    const size_t stats = stats_bytes(*d);
+    if (d->io_dtype != E2TTT_F32) return stats;
+    int dq, dkv;
+    attn_f32_parts(d->tokens, d->heads / d->kv_heads, d->kv_heads, d->D, &dq, &dkv);
+    return stats + 4 * (size_t)(d->tokens * d->D) * ((dq > 1 ? dq * d->heads : 0) + (dkv > 1 ? 2 * dkv * d->kv_heads : 0));
 }
 
 int e2ttt_attention_backward(const e2ttt_attention_desc* d, const void* q, const void* k, const void* v,
@@ -282,6 +287,8 @@ int e2ttt_attention_backward(const e2ttt_attention_desc* d, const void* q, const
     a.sl2 = f.sl2;
     a.scale = d->scale;
     a.stats = (float*)ws;
+    attn_f32_parts(N, f.G, K, D, &a.dq_parts, &a.dkv_parts);
+    a.part = (float*)((char*)ws + stats_bytes(*d));
     a.dq = dq;
     a.dk = dk;
     a.dv = dv;

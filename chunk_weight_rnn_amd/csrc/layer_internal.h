@@ -41,8 +41,8 @@ struct AttnArgs {
     PagedKV pg;
 };
 
-// Rows of one tile of the forward kernels, and key ranges a call is split into.
-int attn_fwd_rows(const AttnArgs& a, bool f32);
+constexpr int kFwdRows = 128;  // rows of a tile of the forward, bf16
+constexpr int kF32Rows = 16;   // and fp32
 hipError_t launch_attn_fwd_bf16(const AttnArgs& a, hipStream_t s);
 hipError_t launch_attn_fwd_f32(const AttnArgs& a, hipStream_t s);
 // Few new tokens per sequence over a paged cache; nsplit > 1: the keys of all
@@ -64,7 +64,12 @@ struct AttnBwdArgs {
     float sl2, scale;
     float* stats;  // [2][N][H] workspace: bf16 -lse / scale and -delta of each row; fp32 delta alone
     void *dq, *dk, *dv;
+    // fp32: workgroups that share a tile of rows (dq) or a block of keys (dk, dv);
+    // > 1: their sums [dq_parts][N][H][D] and [dkv_parts][2][N][K][D], joined after
+    int dq_parts, dkv_parts;
+    float* part;
 };
+void attn_f32_parts(int64_t N, int64_t G, int64_t K, int64_t D, int* dq, int* dkv);
 hipError_t launch_attn_bwd_bf16(const AttnBwdArgs& a, hipStream_t s);
 hipError_t launch_attn_bwd_f32(const AttnBwdArgs& a, hipStream_t s);
 
