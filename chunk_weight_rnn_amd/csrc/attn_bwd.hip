@@ -15,14 +15,21 @@
 // Scores are recomputed in the orientation in which p and ds leave the MFMA as
 // the next product's operand (attn_common.h): S^T with a query per lane for
 // dq, S with a key per lane for dk and dv.
+//
+// 12 packed sequences of up to 2K, 16 heads of 128 over 4: dq 110 us (three
+// products, 350 Tflop/s), dk and dv 178 us (four, 290).  Bound by each wave's own
+// chain: two waves per SIMD, the registers' limit, hide the exponentials, the
+// packing and the LDS reads of the next operands only in part.
 #include "attn_common.h"
 
 namespace e2ttt {
 namespace attn {
 namespace {
 
-constexpr int BM = 128;  // rows (dq) or keys (dkdv) of a workgroup: 4 waves x 32
-constexpr int BN = 64;   // keys or rows of a staged tile
+constexpr int BM = 128;  // rows of a workgroup (dq): 4 waves x 32
+constexpr int BN = 64;   // keys of a staged tile (dq)
+constexpr int BK = 64;   // keys of a workgroup (dkdv)
+constexpr int BR = 64;   // rows of a staged tile (dkdv)
 
 template <int DP>
 struct CopyPlan {
@@ -49,6 +56,8 @@ __device__ __forceinline__ void store_row(__bf16* o, const f32x16 (&acc)[DT], fl
         }
 }
 
+// 128 rows per workgroup over tiles of 64 keys, as the forward.  delta is computed
+// from dout and out where the row's operands are loaded.
 template <int DP>
 __global__ __launch_bounds__(256, 2) void attn_dq_kernel(AttnBwdArgs a) {
     constexpr int TILE = BN * DP * 2;
@@ -221,26 +230,21 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(AttnBwdArgs a) {
     store_row<DT>((__bf16*)a.dq + at * a.D, acc, a.scale, g, a.D);
 }
 
-// 64 keys per workgroup, over tiles of 64 RW rows: wave (kw, rw) takes 32 keys
-// and 64 rows of each tile, and the RW partial sums of a key are added at the
-// end, in order.  One wave per SIMD with all of its registers: 192 of them hold
-// the sums and the key and value operands, and two 32-row halves in turn let
-// one half's exponentials run beside the other's products.  (Two waves per
-// SIMD with 256 registers each left the compiler four to read fragments into,
-// and every product waited for its own read: 1.8 times the time.)
-constexpr int BK = 64;
-
-template <int DP, int RW>
-__global__ __launch_bounds__(128 * RW, 2) void attn_dkdv_kernel(AttnBwdArgs a) {
-    constexpr int BR = 32 * RW;
+// 64 keys per workgroup, over tiles of 64 rows: wave (kw, rw) takes 32 keys and
+// 32 rows of each tile, and the two partial sums of a key are added at the end, in
+// order.  The sums and the key and value operands take 192 of a wave's 256
+// registers, so fragments are read four products ahead (read_ahead): left to the
+// compiler every product waits for its own read, 1.8 times the time.
+template <int DP>
+__global__ __launch_bounds__(256, 2) void attn_dkdv_kernel(AttnBwdArgs a) {
     constexpr int TILE = BR * DP * 2;
     constexpr int KS = DP / 16, DT = DP / 32;
     constexpr int RPI = 512 / DP, NI = 16 / RPI, CH = DP / 8;  // copy instructions per wave and tensor, 16 rows
     constexpr int OLD = DP + 4;                                // row stride of the final sums, floats
     __shared__ __attribute__((aligned(1024))) unsigned char lds[2][2][TILE];  // [stage][Q, dout]
     __shared__ __attribute__((aligned(256))) float stat[2][2][BR];            // [stage][-lse / scale, -delta]
-    __shared__ __attribute__((aligned(16))) unsigned offs[2][128 * RW][NI];   // [Q, dout]: copy offsets of a thread
-    static_assert((RW - 1) * BK * OLD * 4 <= 4 * TILE, "the final sums fit in the stages");
+    __shared__ __attribute__((aligned(16))) unsigned offs[2][256][NI];   // [Q, dout]: copy offsets of a thread
+    static_assert(BK * OLD * 4 <= 4 * TILE, "the final sums fit in the stages");
 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int kw = wave & 1, rw = wave >> 1;
@@ -424,7 +428,7 @@ __global__ __launch_bounds__(128 * RW, 2) void attn_dkdv_kernel(AttnBwdArgs a) {
             for (int dt = 0; dt < DT; ++dt) dk[dt] = dv[dt] = f32x16{};
 #pragma unroll 1
             for (int r = rbeg; r < rend; ++r) {
-                if (((r - rbeg) / 32) % RW != rw) continue;
+                if (((r - rbeg) / 32) % 2 != rw) continue;
                 const int tk = div_group(r, G, a.gmagic), hg = r - tk * G;
                 const int64_t at = first_row + (int64_t)tk * a.H + hg;
                 const char* qp = qsrc + 2 * (tk * a.q_tok + hg * a.q_head);
@@ -447,21 +451,18 @@ __global__ __launch_bounds__(128 * RW, 2) void attn_dkdv_kernel(AttnBwdArgs a) {
             for (int dt = 0; dt < DT; ++dt)
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    *(f32x4*)(area + (rw - 1) * (BK * OLD) + 32 * dt + 8 * j) =
-                        f32x4{x[dt][4 * j], x[dt][4 * j + 1], x[dt][4 * j + 2], x[dt][4 * j + 3]};
+                    *(f32x4*)(area + 32 * dt + 8 * j) = f32x4{x[dt][4 * j], x[dt][4 * j + 1], x[dt][4 * j + 2], x[dt][4 * j + 3]};
         }
         barrier_lds();
         if (rw > 0) continue;
 #pragma unroll
-        for (int w = 0; w < RW - 1; ++w)
+        for (int dt = 0; dt < DT; ++dt)
 #pragma unroll
-            for (int dt = 0; dt < DT; ++dt)
+            for (int j = 0; j < 4; ++j) {
+                const f32x4 y = *(const f32x4*)(area + 32 * dt + 8 * j);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const f32x4 y = *(const f32x4*)(area + w * (BK * OLD) + 32 * dt + 8 * j);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) x[dt][4 * j + e] += y[e];
-                }
+                for (int e = 0; e < 4; ++e) x[dt][4 * j + e] += y[e];
+            }
         if (live) store_row<DT>((__bf16*)(which == 0 ? a.dv : a.dk) + (ktok * a.K + kvh) * a.D, x, which == 0 ? 1.f : a.scale, g, a.D);
     }
 }
@@ -473,7 +474,7 @@ hipError_t launch(const AttnBwdArgs& a, hipStream_t s) {
     attn_dq_kernel<DP><<<dim3((unsigned)dq_grid), dim3(256), 0, s>>>(a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    attn_dkdv_kernel<DP, 2><<<dim3((unsigned)dkv_grid), dim3(256), 0, s>>>(a);
+    attn_dkdv_kernel<DP><<<dim3((unsigned)dkv_grid), dim3(256), 0, s>>>(a);
     return hipGetLastError();
 }
 

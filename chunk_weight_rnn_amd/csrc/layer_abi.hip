@@ -122,8 +122,10 @@ void plan(AttnArgs& a, bool f32, int64_t longest) {
 
 // A paged call of few rows per sequence on average goes to the decoding kernel
 // (bf16), which needs one launch where no context can be longer than
-// kOneLaunch keys, and two where the keys are shared out.
-constexpr int64_t kOneLaunch = 1024;
+// kOneLaunch keys, and two where the keys are shared out (one token, 16 heads of
+// 128 over 4: at a context of 500 keys 12.5 us in one and 13.4 in two, at 1000
+// 19.5 and 13.2; 16 sequences at 1000 19.8 and 16.1).
+constexpr int64_t kOneLaunch = 640;
 void plan_paged(AttnArgs& a, bool f32, int64_t longest) {
     const int64_t units = (longest + a.N + 127) / 128, tiles = a.N * a.G / 32 + a.S;
     if (!f32 && a.N * a.G <= 32 * (int64_t)a.S && tiles * a.K <= 0x7fffffff / (units + 1)) {
@@ -387,7 +389,7 @@ int e2ttt_norm_forward(const e2ttt_norm_desc* d, const void* x, const void* resi
 
 size_t e2ttt_norm_backward_workspace_size(const e2ttt_norm_desc* d) {
     if (!norm_desc_ok(d) || !norm_supported(d)) return kBad;
-    return d->rows == 0 ? 0 : (size_t)norm_bwd_groups(d->rows, d->width) * d->width * 4;
+    return d->rows == 0 ? 0 : (size_t)norm_bwd_groups(d->rows) * d->width * 4;
 }
 
 int e2ttt_norm_backward(const e2ttt_norm_desc* d, const void* dy, const void* h, const float* weight,
