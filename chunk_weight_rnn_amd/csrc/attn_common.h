@@ -402,11 +402,18 @@ __device__ __forceinline__ void wait_vm() {
     asm volatile("" ::: "memory");
 }
 
-// Workgroup barrier that waits for this wave's LDS accesses, not for its
-// copies in flight.
-__device__ __forceinline__ void barrier_lds() {
+// Waits for this wave's LDS accesses, not for its copies in flight.  A stage may
+// be refilled only after it: the compiler does not know where a copy writes, so
+// by itself it keeps a fragment's read before its product, not before the copy.
+__device__ __forceinline__ void wait_lds() {
+    asm volatile("" ::: "memory");
     __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
     asm volatile("" ::: "memory");
+}
+
+// Workgroup barrier after that wait.
+__device__ __forceinline__ void barrier_lds() {
+    wait_lds();
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
 }

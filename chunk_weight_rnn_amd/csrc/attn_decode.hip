@@ -243,6 +243,7 @@ __global__ __launch_bounds__(256, 1) void attn_decode_kernel(AttnArgs a, int gro
                 }
             }
             if (b + 2 < b1) {
+                wait_lds();  // the stage has been read
                 copy_part(b + 2);
                 copy_pages(b + 4);
             }
