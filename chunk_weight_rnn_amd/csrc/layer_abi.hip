@@ -108,7 +108,8 @@ void plan(AttnArgs& a, bool f32, int64_t longest) {
     a.ntiles = (int)(a.N * a.G / bm + a.S);
     a.nsplit = 1;
     const int64_t items = (a.N * a.G + bm - 1) / bm * a.K;  // at least so many do work
-    if (a.window > 0 && longest > a.window + bm / a.G + 64) longest = a.window + bm / a.G + 64;
+    const int64_t seen = (int64_t)a.window + bm / a.G + 64;  // positions that a tile's rows see, at most
+    if (a.window > 0 && longest > seen) longest = seen;
     if (items > 0 && items < kCUs) {
         // 8 chunks of up to 256 tokens over a window of 2048, 208 tiles: 76 us
         // whole, 56 in 2 ranges, 46 in 3, 52 in 4 (and 13 for the join); one
@@ -131,7 +132,7 @@ void plan_paged(AttnArgs& a, bool f32, int64_t longest) {
     if (!f32 && a.N * a.G <= 32 * (int64_t)a.S && tiles * a.K <= 0x7fffffff / (units + 1)) {
         a.decode = 1;
         a.ntiles = (int)tiles;
-        if (a.window > 0 && longest > a.window + 64) longest = a.window + 64;
+        if (a.window > 0 && longest > (int64_t)a.window + 64) longest = (int64_t)a.window + 64;
         a.nsplit = longest <= kOneLaunch ? 1 : 2;
         return;
     }
