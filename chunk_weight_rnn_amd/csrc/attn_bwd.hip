@@ -67,6 +67,10 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(AttnBwdArgs a) {
 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int g = lane >> 5, col = lane & 31, G = a.G;
+    if (const int past = (int)(blockIdx.x + a.clear) - (int)gridDim.x; past >= 0) {  // no rows: outside every sequence
+        fill_outside(a.cu, a.S, a.N, a.dq, (int64_t)a.H * a.D * 2, 0, past, a.clear);
+        return;
+    }
     const int kvh = blockIdx.x % a.K, t = blockIdx.x / a.K;
     Item it;
     if (!find_item(a.cu, a.S, (int)a.N, t, row_cap(a.window, G, BM), [&](int n) { return (n * G + BM - 1) / BM; }, it)) return;
@@ -249,6 +253,11 @@ __global__ __launch_bounds__(256, 2) void attn_dkdv_kernel(AttnBwdArgs a) {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int kw = wave & 1, rw = wave >> 1;
     const int g = lane >> 5, col = lane & 31, G = a.G;
+    if (const int past = (int)(blockIdx.x + a.clear) - (int)gridDim.x; past >= 0) {
+        fill_outside(a.cu, a.S, a.N, a.dk, (int64_t)a.K * a.D * 2, 0, past, a.clear);
+        fill_outside(a.cu, a.S, a.N, a.dv, (int64_t)a.K * a.D * 2, 0, past, a.clear);
+        return;
+    }
     const int kvh = blockIdx.x % a.K, t = blockIdx.x / a.K;
     Item it;
     if (!find_item(a.cu, a.S, (int)a.N, t, row_cap(a.window, 1, BK), [&](int n) { return (n + BK - 1) / BK; }, it)) return;
@@ -469,7 +478,7 @@ __global__ __launch_bounds__(256, 2) void attn_dkdv_kernel(AttnBwdArgs a) {
 
 template <int DP>
 hipError_t launch(const AttnBwdArgs& a, hipStream_t s) {
-    const int64_t dq_grid = (a.N * a.G / BM + a.S) * a.K, dkv_grid = (a.N / BK + a.S) * a.K;
+    const int64_t dq_grid = (a.N * a.G / BM + a.S) * a.K + a.clear, dkv_grid = (a.N / BK + a.S) * a.K + a.clear;
     if (dq_grid > 0x7fffffff) return hipErrorInvalidValue;
     attn_dq_kernel<DP><<<dim3((unsigned)dq_grid), dim3(256), 0, s>>>(a);
     hipError_t e = hipGetLastError();

@@ -157,6 +157,29 @@ __device__ __forceinline__ bool find_item(const int* __restrict__ cu, int S, int
     return false;
 }
 
+// Block b of `blocks`: the rows of tokens outside every sequence, which see
+// nothing, in a tensor of `bytes` per token; `what` in every four of them.
+__device__ __forceinline__ void fill_outside(const int* __restrict__ cu, int S, int64_t N, void* p, int64_t bytes,
+                                             unsigned what, int b, int blocks) {
+    const int64_t lo = clamped(cu[0], (int)N), end = clamped(cu[S], (int)N), hi = end > lo ? end : lo;
+    const int64_t words = bytes / 4, count = (lo + N - hi) * words, skip = (hi - lo) * words;
+    unsigned* w = (unsigned*)p;
+    if (words % 4 == 0 && (uintptr_t)p % 16 == 0) {
+        for (int64_t i = ((int64_t)b * 256 + threadIdx.x) * 4; i < count; i += (int64_t)blocks * 1024)
+            *(u32x4*)(w + (i < lo * words ? i : i + skip)) = u32x4{what, what, what, what};
+        return;
+    }
+    for (int64_t i = (int64_t)b * 256 + threadIdx.x; i < count; i += (int64_t)blocks * 256)
+        w[i < lo * words ? i : i + skip] = what;
+}
+
+// Outputs of the forward there: out 0, lse the log of an empty sum.
+template <typename T>
+__device__ __forceinline__ void clear_block(const AttnArgs& a, int b) {
+    fill_outside(a.cu, a.S, a.N, a.out, (int64_t)a.H * a.D * sizeof(T), 0, b, a.clear);
+    if (a.lse) fill_outside(a.cu, a.S, a.N, a.lse, (int64_t)a.H * 4, 0xff800000u, b, a.clear);
+}
+
 // Tokens a sequence has in the cache, clamped to what its page table holds.
 __device__ __forceinline__ int kept_tokens(const PagedKV& pg, int seq, int n) {
     const int64_t room = ((int64_t)pg.wide << pg.shift) - n;

@@ -121,7 +121,9 @@ __global__ __launch_bounds__(256, 1) void attn_decode_kernel(AttnArgs a, int gro
     static_assert(4 * BM * OLD * 4 <= (int)sizeof(lds), "the merge area fits in the stages");
 
     if ((int)blockIdx.x >= groups) {
-        append_block<__bf16>(a, blockIdx.x - groups);
+        const int past = blockIdx.x - groups;
+        if (past < a.clear) clear_block<__bf16>(a, past);
+        else append_block<__bf16>(a, past - a.clear);
         return;
     }
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -370,7 +372,7 @@ template <int DP>
 hipError_t launch(const AttnArgs& a, hipStream_t s) {
     const int64_t items = (int64_t)a.ntiles * a.K;
     const int64_t groups = a.nsplit > 1 ? kDecodeGroups : items;
-    const int64_t grid = groups + append_blocks(a, 8);
+    const int64_t grid = groups + a.clear + append_blocks(a, 8);
     if (grid > 0x7fffffff) return hipErrorInvalidValue;
     if (a.nsplit > 1)
         attn_decode_kernel<DP, true><<<dim3((unsigned)grid), dim3(256), 0, s>>>(a, (int)groups);

@@ -241,12 +241,10 @@ __global__ __launch_bounds__(256, DP == 64 ? 4 : 2) void attn_f32_fwd_kernel(Att
     __shared__ __attribute__((aligned(16))) float area[kWaves][BM * LD];
     __shared__ float stat[2][kWaves][BM];
     int b = blockIdx.x;
-    if constexpr (PAGED) {
-        const int tiles = a.ntiles * a.nsplit * a.K;
-        if (b >= tiles) {
-            append_block<float>(a, b - tiles);
-            return;
-        }
+    if (const int past = b - a.ntiles * a.nsplit * a.K; past >= 0) {  // as in attn_fwd.hip
+        if (past < a.clear) clear_block<float>(a, past);
+        else if constexpr (PAGED) append_block<float>(a, past - a.clear);
+        return;
     }
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int u = lane >> 4, col = lane & 15, G = a.G;
@@ -435,6 +433,10 @@ __global__ __launch_bounds__(256, 2) void attn_f32_dq_kernel(AttnBwdArgs a) {
     __shared__ __attribute__((aligned(16))) float area[kWaves][BM * LD];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int u = lane >> 4, col = lane & 15, G = a.G;
+    if (const int past = (int)(blockIdx.x + a.clear) - (int)gridDim.x; past >= 0) {  // as in attn_bwd.hip
+        fill_outside(a.cu, a.S, a.N, a.dq, (int64_t)a.H * a.D * 4, 0, past, a.clear);
+        return;
+    }
     const int kvh = blockIdx.x % a.K, part = blockIdx.x / a.K % a.dq_parts, t = blockIdx.x / a.K / a.dq_parts;
     Item it;
     if (!find_item(a.cu, a.S, (int)a.N, t, row_cap(a.window, G, BM), [&](int n) { return (n * G + BM - 1) / BM; }, it)) return;
@@ -575,6 +577,11 @@ __global__ __launch_bounds__(256, DP == 64 ? 2 : 1) void attn_f32_dkdv_kernel(At
     __shared__ __attribute__((aligned(16))) float area[2][kWaves][BK * LD];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int u = lane >> 4, col = lane & 15, G = a.G;
+    if (const int past = (int)(blockIdx.x + a.clear) - (int)gridDim.x; past >= 0) {
+        fill_outside(a.cu, a.S, a.N, a.dk, (int64_t)a.K * a.D * 4, 0, past, a.clear);
+        fill_outside(a.cu, a.S, a.N, a.dv, (int64_t)a.K * a.D * 4, 0, past, a.clear);
+        return;
+    }
     const int kvh = blockIdx.x % a.K, part = blockIdx.x / a.K % a.dkv_parts, t = blockIdx.x / a.K / a.dkv_parts;
     Item it;
     if (!find_item(a.cu, a.S, (int)a.N, t, row_cap(a.window, 1, BK), [&](int n) { return (n + BK - 1) / BK; }, it)) return;
@@ -758,7 +765,7 @@ __global__ __launch_bounds__(256, DP == 64 ? 2 : 1) void attn_f32_dkdv_kernel(At
 }
 
 // The gradients from the parts' sums, in order: dq, then dk, then dv.  (Tokens
-// outside every sequence have none.)
+// outside every sequence have none, and their zeros already.)
 __global__ __launch_bounds__(256) void attn_f32_parts_kernel(AttnBwdArgs a) {
     const int64_t nq = a.dq_parts > 1 ? a.N * a.H * a.D : 0, nk = a.dkv_parts > 1 ? a.N * a.K * a.D : 0;
     int64_t o = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
@@ -797,7 +804,7 @@ constexpr int bwd_tiles(int64_t D) { return D <= 64 ? 2 : 1; }
 template <int DP>
 hipError_t launch_fwd(const AttnArgs& a, hipStream_t s) {
     const bool paged = a.pg.kc != nullptr;
-    const int64_t grid = (int64_t)a.ntiles * a.K * a.nsplit + (paged ? append_blocks(a, 4) : 0);
+    const int64_t grid = (int64_t)a.ntiles * a.K * a.nsplit + a.clear + (paged ? append_blocks(a, 4) : 0);
     if (grid == 0) return hipSuccess;
     if (grid > 0x7fffffff) return hipErrorInvalidValue;
     if (paged)
@@ -810,7 +817,8 @@ hipError_t launch_fwd(const AttnArgs& a, hipStream_t s) {
 template <int DP>
 hipError_t launch_bwd(const AttnBwdArgs& a, hipStream_t s) {
     constexpr int RT = bwd_tiles(DP), B = 16 * RT;
-    const int64_t dq_grid = (a.N * a.G / B + a.S) * a.K * a.dq_parts, dkv_grid = (a.N / B + a.S) * a.K * a.dkv_parts;
+    const int64_t dq_grid = (a.N * a.G / B + a.S) * a.K * a.dq_parts + a.clear;
+    const int64_t dkv_grid = (a.N / B + a.S) * a.K * a.dkv_parts + a.clear;
     const int64_t sums = a.N * a.D * ((a.dq_parts > 1 ? a.H : 0) + (a.dkv_parts > 1 ? 2 * a.K : 0));
     const int64_t sum_grid = (sums / 4 + 255) / 256;
     if (dq_grid > 0x7fffffff || dkv_grid > 0x7fffffff || sum_grid > 0x7fffffff) return hipErrorInvalidValue;

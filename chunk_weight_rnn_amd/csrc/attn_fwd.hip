@@ -55,12 +55,12 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(AttnArgs a) {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int g = lane >> 5, col = lane & 31;
     int b = blockIdx.x;
-    if constexpr (PAGED) {  // blocks past the tiles write the new tokens into their slots
-        const int tiles = a.ntiles * a.nsplit * a.K;
-        if (b >= tiles) {
-            append_block<__bf16>(a, b - tiles);
-            return;
-        }
+    // blocks past the tiles write the rows outside every sequence, and the new
+    // tokens into their slots
+    if (const int past = b - a.ntiles * a.nsplit * a.K; past >= 0) {
+        if (past < a.clear) clear_block<__bf16>(a, past);
+        else if constexpr (PAGED) append_block<__bf16>(a, past - a.clear);
+        return;
     }
     const int kvh = b % a.K;
     b /= a.K;
@@ -297,7 +297,7 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
     const int64_t r = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
     const int64_t NH = a.N * a.H;
     const int lane = threadIdx.x & 63, g = lane >> 5, i = lane & 31, d = 4 * i;
-    // a token outside every sequence has no partial results
+    // a token outside every sequence has no partial results (and its output already)
     const int tok = (int)(r / a.H);
     const bool live = r < NH && tok >= clamped(a.cu[0], (int)a.N) && tok < clamped(a.cu[a.S], (int)a.N);
     const bool in = live && d < a.D;
@@ -340,7 +340,7 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
 template <int DP>
 hipError_t launch(const AttnArgs& a, hipStream_t s) {
     const bool paged = a.pg.kc != nullptr;
-    const int64_t grid = (int64_t)a.ntiles * a.K * a.nsplit + (paged ? append_blocks(a, 8) : 0);
+    const int64_t grid = (int64_t)a.ntiles * a.K * a.nsplit + a.clear + (paged ? append_blocks(a, 8) : 0);
     if (grid == 0) return hipSuccess;
     if (grid > 0x7fffffff) return hipErrorInvalidValue;
     const dim3 gr((unsigned)grid), bl(256);

@@ -90,6 +90,10 @@ AttnArgs make_args(const e2ttt_attention_desc& d) {
     a.gmagic = (unsigned)(((uint64_t)1 << 32) / a.G + 1);
     a.window = d.window;
     a.sl2 = d.scale * 1.4426950408889634f;
+    // Such tokens are rare, and their number is only known on the device: enough
+    // workgroups to write rows at some TB/s, and too few to notice where there are none.
+    const int64_t units = (d.tokens * d.heads * d.D * elem(d.io_dtype) / 16 + 255) / 256;
+    a.clear = (int)(units < 64 ? units : 64);
     a.q_tok = d.q_tok;
     a.q_head = d.q_head;
     a.k_tok = d.k_tok;
@@ -289,6 +293,7 @@ int e2ttt_attention_backward(const e2ttt_attention_desc* d, const void* q, const
     a.window = f.window;
     a.sl2 = f.sl2;
     a.scale = d->scale;
+    a.clear = f.clear;
     a.stats = (float*)ws;
     attn_f32_parts(N, f.G, K, D, &a.dq_parts, &a.dkv_parts);
     a.part = (float*)((char*)ws + stats_bytes(*d));

@@ -36,6 +36,7 @@ struct AttnArgs {
     int ntiles;   // row tiles at most, over all sequences
     int nsplit;   // key ranges per row tile; > 1: partial results, joined after
     int decode;   // paged: the kernel for few rows per sequence
+    int clear;    // workgroups that write the rows of tokens outside every sequence
     float* po;    // [nsplit][N][H][D] partial outputs
     float* pl;    // [nsplit][N][H] their base-2 log sums
     PagedKV pg;
@@ -70,6 +71,7 @@ struct AttnBwdArgs {
     // > 1: their sums [dq_parts][N][H][D] and [dkv_parts][2][N][K][D], joined after
     int dq_parts, dkv_parts;
     float* part;
+    int clear;  // as in AttnArgs
 };
 void attn_f32_parts(int64_t N, int64_t G, int64_t K, int64_t D, int* dq, int* dkv);
 hipError_t launch_attn_bwd_bf16(const AttnBwdArgs& a, hipStream_t s);

@@ -176,7 +176,9 @@ def attention_forward(q, k, v, cu_seqlens, *, window: int = 0, scale: float | No
     q: [N, H, D], k, v: [N, K, D], float32 or bfloat16, last dimension
     contiguous (views of one projection's output are fine); H a multiple of K,
     D a multiple of 8 up to 128.  cu_seqlens: [S + 1] int32 on the GPU, the
-    sequences' offsets into the N tokens.  ``window`` > 0: a query sees that
+    sequences' offsets into the N tokens; tokens before the first or from the
+    last on belong to no sequence: out and their gradients are 0, lse
+    -infinity.  ``window`` > 0: a query sees that
     many positions, its own the last.  ``scale``: of the scores, D ** -0.5 by
     default.  out: [N, H, D]; lse: [N, H] float32, the log of each row's
     softmax sum, which the backward needs.
@@ -194,6 +196,8 @@ def attention_forward(q, k, v, cu_seqlens, *, window: int = 0, scale: float | No
         lse = torch.empty(N, H, dtype=torch.float32, device=q.device)
     else:
         _full("lse", lse, (N, H), torch.float32)
+    if cu_seqlens.shape[0] == 1:  # no sequences, no launch
+        return out.zero_(), lse.fill_(float("-inf"))
     ws, n = _workspace(workspace, need, q)
     _call("e2ttt_attention_forward", dev, desc, q.data_ptr(), k.data_ptr(), v.data_ptr(),
           cu_seqlens.data_ptr(), out.data_ptr(), lse.data_ptr(), ws, n)
@@ -214,6 +218,8 @@ def attention_backward(q, k, v, out, lse, dout, cu_seqlens, *, window: int = 0, 
     _full("dout", dout, (N, H, D), q.dtype)
     _full("lse", lse, (N, H), torch.float32)
     g = {n: torch.empty(t.shape, dtype=q.dtype, device=q.device) for n, t in (("q", q), ("k", k), ("v", v))}
+    if cu_seqlens.shape[0] == 1:  # as in the forward
+        return {n: t.zero_() for n, t in g.items()}
     ws, n = _workspace(workspace, need, q)
     _call("e2ttt_attention_backward", dev, desc, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
           lse.data_ptr(), dout.data_ptr(), cu_seqlens.data_ptr(), g["q"].data_ptr(), g["k"].data_ptr(),
@@ -255,6 +261,8 @@ def paged_attention(q, k, v, k_cache, v_cache, table, cu_seqlens, cached, *, win
     two (any strides with a contiguous last dimension).  table: [S, W] int32,
     the pages of each sequence; cached: [S] int32, its tokens in the cache
     before the call.  New token i of sequence s is at position cached[s] + i.
+    Tokens before the first offset or from the last on belong to no sequence:
+    their out is 0, their k and v go nowhere.
     With k = v = None the cache holds the new tokens already.
     """
     if stream is not None:
@@ -274,6 +282,8 @@ def paged_attention(q, k, v, k_cache, v_cache, table, cu_seqlens, cached, *, win
         out = torch.empty(N, H, D, dtype=q.dtype, device=q.device)
     else:
         _full("out", out, (N, H, D), q.dtype)
+    if S == 0:  # no sequences, no launch
+        return out.zero_()
     ws, n = _workspace(workspace, need, q)
     _call("e2ttt_paged_attention", dev, desc, q.data_ptr(), _p(k), _p(v), k_cache.data_ptr(),
           v_cache.data_ptr(), table.data_ptr(), cu_seqlens.data_ptr(), cached.data_ptr(), out.data_ptr(), ws, n)

@@ -53,10 +53,12 @@ typedef struct {
 
 /*
  *   q, k, v     as above, 16-byte aligned
- *   cu_seqlens  [S + 1] int32, non-decreasing, cu_seqlens[0] = 0, [S] = N
- *   out         [N][heads][D] contiguous; rows of tokens outside every
- *               sequence are not written
- *   lse         [N][heads] fp32 (natural log), or NULL
+ *   cu_seqlens  [S + 1] int32, non-decreasing, from 0 to N; tokens before
+ *               the first or from the last on (room to spare in a packed
+ *               buffer) belong to no sequence and see nothing.  (A call of
+ *               no sequences, S = 0, returns without writing anything.)
+ *   out         [N][heads][D] contiguous; 0 for tokens of no sequence
+ *   lse         [N][heads] fp32 (natural log), or NULL; -infinity there
  *   workspace   >= e2ttt_attention_workspace_size(desc) bytes, 256-byte
  *               aligned; clobbered (NULL when that is 0)
  * bf16: bf16 MFMA with fp32 accumulation; scores, softmax and output sums are
@@ -72,7 +74,7 @@ E2TTT_API int e2ttt_attention_forward(const e2ttt_attention_desc* desc, const vo
  * Gradients of <dout, out> with respect to q, k, v, from the forward's
  * inputs, out and lse.  dout, dq [N][heads][D] and dk, dv [N][kv_heads][D]
  * contiguous, 16-byte aligned; a key head's gradient is the sum over the
- * query heads that share it.  Outputs must not overlap any other buffer.
+ * query heads that share it.  Those of tokens of no sequence are 0.  Outputs must not overlap any other buffer.
  */
 E2TTT_API size_t e2ttt_attention_backward_workspace_size(const e2ttt_attention_desc* desc);
 E2TTT_API int e2ttt_attention_backward(const e2ttt_attention_desc* desc, const void* q, const void* k, const void* v,
@@ -89,7 +91,8 @@ E2TTT_API int e2ttt_attention_backward(const e2ttt_attention_desc* desc, const v
  * tokens' keys and values into their slots and attends over cached and new
  * ones; with k = v = NULL the slots hold them already.  Scores, mask and
  * window as above, over positions.  A new token always sees itself; rows that
- * see nothing (k = v = NULL and a negative length) give 0.
+ * see nothing (of tokens outside every sequence; k = v = NULL and a negative
+ * length) give 0.
  * Slots that no query sees may hold anything.  A page index outside the pool
  * is read as zeros and not written.
  */
