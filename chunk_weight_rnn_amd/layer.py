@@ -4,9 +4,10 @@ include/e2ttt_layer.h.
 Argument marshalling only, as in the package's ``__init__``: the work runs in
 the HIP kernels behind the C ABI on the current stream, with tensors that the
 caller owns; outputs and workspaces that are not given are allocated through
-torch.  With ``stream`` the call runs as under ``torch.cuda.stream(stream)``:
-what it allocates belongs to that stream, so that no other work reuses a
-workspace before the kernels are done with it.  CPU tensors raise.
+torch.  With ``stream``, one of the tensors' device, the call runs as under
+``torch.cuda.stream(stream)``: what it allocates belongs to that stream, so that
+no other work reuses a workspace before the kernels are done with it.  CPU
+tensors raise.
 """
 from __future__ import annotations
 
@@ -34,6 +35,13 @@ def _device(first, **others) -> int:
         if t is not None and t.get_device() != dev:
             raise ValueError(f"{name} must be a GPU tensor on the same device as the others")
     return dev
+
+
+def _on(stream, first):
+    """The context of a stream of the tensors' device."""
+    if stream.device.index != _device(first):
+        raise ValueError(f"stream must be on the tensors' device {first.device}, not {stream.device}")
+    return torch.cuda.stream(stream)
 
 
 def _call(fn: str, dev: int, *args):
@@ -184,7 +192,7 @@ def attention_forward(q, k, v, cu_seqlens, *, window: int = 0, scale: float | No
     softmax sum, which the backward needs.
     """
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on(stream, q):
             return attention_forward(q, k, v, cu_seqlens, window=window, scale=scale, out=out, lse=lse, workspace=workspace)
     dev = _device(q, k=k, v=v, cu_seqlens=cu_seqlens, out=out, lse=lse)
     (N, H, D), desc, need, _, _ = _attention_plan(_layout(q), _layout(k), _layout(v), _layout(cu_seqlens), window, scale)
@@ -209,7 +217,7 @@ def attention_backward(q, k, v, out, lse, dout, cu_seqlens, *, window: int = 0, 
     """Gradients of <dout, out> through ``attention_forward``, from its inputs
     and outputs; returns a dict with keys q, k, v (the I/O dtype, contiguous)."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on(stream, q):
             return attention_backward(q, k, v, out, lse, dout, cu_seqlens, window=window, scale=scale,
                                       workspace=workspace)
     dev = _device(q, k=k, v=v, out=out, lse=lse, dout=dout, cu_seqlens=cu_seqlens)
@@ -266,7 +274,7 @@ def paged_attention(q, k, v, k_cache, v_cache, table, cu_seqlens, cached, *, win
     With k = v = None the cache holds the new tokens already.
     """
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on(stream, q):
             return paged_attention(q, k, v, k_cache, v_cache, table, cu_seqlens, cached, window=window, scale=scale,
                                    out=out, workspace=workspace)
     if (k is None) != (v is None):
@@ -302,7 +310,7 @@ def norm_forward(x, weight, *, residual=None, eps: float = 1e-6, bits8: bool = F
     max|y| / 448 of its row; else None).
     """
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on(stream, x):
             return norm_forward(x, weight, residual=residual, eps=eps, bits8=bits8, h=h)
     dev = _device(x, weight=weight, residual=residual, h=h)
     lead, desc, _, _ = _norm_plan(x.shape, x.dtype, eps, bits8)
@@ -334,7 +342,7 @@ def norm_backward(dy, h, weight, rstd, *, dh=None, workspace=None, stream=None):
     (dx, dweight).  dx is the gradient of both x and residual; ``dh`` is what
     arrives at h along the residual stream, added to it."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on(stream, dy):
             return norm_backward(dy, h, weight, rstd, dh=dh, workspace=workspace)
     dev = _device(h, dy=dy, weight=weight, rstd=rstd, dh=dh)
     lead, desc, need, _ = _norm_plan(h.shape, h.dtype, 0.0, False)
