@@ -174,6 +174,8 @@ def _workspace(workspace, n, like):
         workspace = torch.empty(n, dtype=torch.uint8, device=like.device)
     elif workspace.get_device() != like.get_device():
         raise ValueError("workspace must be a GPU tensor on the same device as the others")
+    elif not workspace.is_contiguous():  # an expanded one has fewer bytes than elements
+        raise ValueError("workspace must be contiguous")
     return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 

@@ -41,3 +41,10 @@ def test_cpu_tensors_are_refused_with_a_stream_too():
     x = torch.zeros(2, 4)
     with pytest.raises(ValueError, match="GPU"):
         e2.norm_forward(x, x[0], stream=s)
+
+
+def test_a_workspace_with_gaps_or_repeats_is_refused(t):
+    for ws in (t.z(1, d=torch.uint8).expand(1 << 24), t.z(1 << 24, 2, d=torch.uint8)[:, 0]):
+        for i in (0, 1, 2, 4):
+            with pytest.raises(ValueError, match="workspace must be contiguous"):
+                calls(t)[i](workspace=ws)
