@@ -36,17 +36,18 @@ __device__ __forceinline__ float wave_sum(float x) {
     for (int d = 32; d; d >>= 1) x += __shfl_xor(x, d);
     return x;
 }
-__device__ __forceinline__ float wave_max(float x) {
+__device__ __forceinline__ unsigned max_bits(unsigned x, unsigned y) { return x > y ? x : y; }
+__device__ __forceinline__ unsigned wave_max(unsigned x) {
 #pragma unroll
-    for (int d = 32; d; d >>= 1) x = fmaxf(x, __shfl_xor(x, d));
+    for (int d = 32; d; d >>= 1) x = max_bits(x, __shfl_xor(x, d));
     return x;
 }
 
 // Over the WPR waves of a row (one workgroup per row for WPR > 1); the same
 // order in every wave.
-template <int WPR, bool MAX>
-__device__ __forceinline__ float row_reduce(float x, float* sh) {
-    x = MAX ? wave_max(x) : wave_sum(x);
+template <int WPR>
+__device__ __forceinline__ float row_sum(float x, float* sh) {
+    x = wave_sum(x);
     if constexpr (WPR > 1) {
         const int wave = threadIdx.x >> 6;
         __syncthreads();
@@ -54,10 +55,29 @@ __device__ __forceinline__ float row_reduce(float x, float* sh) {
         __syncthreads();
         x = sh[0];
 #pragma unroll
-        for (int w = 1; w < WPR; ++w) x = MAX ? fmaxf(x, sh[w]) : x + sh[w];
+        for (int w = 1; w < WPR; ++w) x += sh[w];
     }
     return x;
 }
+template <int WPR>
+__device__ __forceinline__ unsigned row_max(unsigned x, float* sh) {
+    x = wave_max(x);
+    if constexpr (WPR > 1) {
+        unsigned* const us = (unsigned*)sh;
+        const int wave = threadIdx.x >> 6;
+        __syncthreads();
+        if ((threadIdx.x & 63) == 0) us[wave] = x;
+        __syncthreads();
+        x = us[0];
+#pragma unroll
+        for (int w = 1; w < WPR; ++w) x = max_bits(x, us[w]);
+    }
+    return x;
+}
+
+// A magnitude as a whole number: ordered as the values are, and NaN above all of
+// them, so that a maximum keeps it.
+__device__ __forceinline__ unsigned magnitude(float x) { return __builtin_bit_cast(unsigned, x) & 0x7fffffffu; }
 
 // One fp32 pair to e4m3, low two bytes.
 __device__ __forceinline__ unsigned pk8(float a, float b) {
@@ -65,6 +85,9 @@ __device__ __forceinline__ unsigned pk8(float a, float b) {
 }
 
 constexpr float kF8Max = 448.f;
+
+// A row's scale, from its largest magnitude: NaN if that is, 1 for zeros.
+__device__ __forceinline__ float scale_of(unsigned top) { return top ? __builtin_bit_cast(float, top) / kF8Max : 1.f; }
 
 // y / scale inside the format's range: a subnormal scale can round the
 // quotient of the row's largest value past it, which the conversion would turn
@@ -108,7 +131,7 @@ __global__ __launch_bounds__(256) void norm_fwd_kernel(NormArgs a) {
             for (int e = 0; e < V; ++e) ss = __builtin_fmaf((float)u[i].v[e], (float)u[i].v[e], ss);
         }
     }
-    ss = row_reduce<WPR, false>(ss, sh);
+    ss = row_sum<WPR>(ss, sh);
     const float rstd = rsqrtf(ss / (float)W + a.eps);
     if (a.rstd && t == 0) a.rstd[row] = rstd;
     if (!a.bits8) {
@@ -124,7 +147,8 @@ __global__ __launch_bounds__(256) void norm_fwd_kernel(NormArgs a) {
         }
         return;
     }
-    float y[NV][V], top = 0.f;
+    float y[NV][V];
+    unsigned top = 0;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int c = (i * TPR + t) * V;
@@ -133,12 +157,11 @@ __global__ __launch_bounds__(256) void norm_fwd_kernel(NormArgs a) {
 #pragma unroll
             for (int e = 0; e < V; ++e) {
                 y[i][e] = (float)u[i].v[e] * rstd * w.v[e];
-                top = fmaxf(top, fabsf(y[i][e]));
+                top = max_bits(top, magnitude(y[i][e]));
             }
         }
     }
-    top = row_reduce<WPR, true>(top, sh);
-    const float scale = top > 0.f ? top / kF8Max : 1.f;
+    const float scale = scale_of(row_max<WPR>(top, sh));
     if (t == 0) a.scale[row] = scale;
     unsigned char* y8 = (unsigned char*)a.y + row * W;
 #pragma unroll
@@ -178,17 +201,16 @@ __global__ __launch_bounds__(1024) void norm_fwd_wide_kernel(NormArgs a) {
         ss = __builtin_fmaf((float)u, (float)u, ss);
     }
     const T* u = res ? h : x;
-    ss = row_reduce<16, false>(ss, sh);
+    ss = row_sum<16>(ss, sh);
     const float rstd = rsqrtf(ss / (float)W + a.eps);
     if (a.rstd && threadIdx.x == 0) a.rstd[row] = rstd;
     if (!a.bits8) {
         for (int c = threadIdx.x; c < W; c += 1024) ((T*)a.y)[row * W + c] = (T)((float)u[c] * rstd * a.weight[c]);
         return;
     }
-    float top = 0.f;
-    for (int c = threadIdx.x; c < W; c += 1024) top = fmaxf(top, fabsf((float)u[c] * rstd * a.weight[c]));
-    top = row_reduce<16, true>(top, sh);
-    const float scale = top > 0.f ? top / kF8Max : 1.f;
+    unsigned top = 0;
+    for (int c = threadIdx.x; c < W; c += 1024) top = max_bits(top, magnitude((float)u[c] * rstd * a.weight[c]));
+    const float scale = scale_of(row_max<16>(top, sh));
     if (threadIdx.x == 0) a.scale[row] = scale;
     for (int c = threadIdx.x; c < W; c += 1024)
         ((unsigned char*)a.y)[row * W + c] = (unsigned char)pk8(quotient(((float)u[c] * rstd) * a.weight[c], scale), 0.f);
@@ -241,7 +263,7 @@ __global__ __launch_bounds__(256) void norm_bwd_kernel(NormBwdArgs a) {
                 }
             }
         }
-        s = row_reduce<WPR, false>(s, sh) / (float)W;
+        s = row_sum<WPR>(s, sh) / (float)W;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = (i * TPR + t) * V;
@@ -297,7 +319,7 @@ __global__ __launch_bounds__(1024) void norm_bwd_wide_dx_kernel(NormBwdArgs a) {
     float s = 0.f;
     for (int c = threadIdx.x; c < W; c += 1024)
         s = __builtin_fmaf((float)dy[c] * a.weight[c], (float)h[c] * rstd, s);
-    s = row_reduce<16, false>(s, sh) / (float)W;
+    s = row_sum<16>(s, sh) / (float)W;
     for (int c = threadIdx.x; c < W; c += 1024) {
         float d = rstd * ((float)dy[c] * a.weight[c] - (float)h[c] * rstd * s);
         if (a.dh) d += (float)((const T*)a.dh)[row * W + c];
