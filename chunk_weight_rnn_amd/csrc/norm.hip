@@ -86,8 +86,12 @@ __device__ __forceinline__ unsigned pk8(float a, float b) {
 
 constexpr float kF8Max = 448.f;
 
-// A row's scale, from its largest magnitude: NaN if that is, 1 for zeros.
-__device__ __forceinline__ float scale_of(unsigned top) { return top ? __builtin_bit_cast(float, top) / kF8Max : 1.f; }
+// A row's scale, from its largest magnitude: NaN if that is, 1 for zeros.  Not less
+// than the smallest value there is: a scale of 0 would make NaN of the row's zeros.
+__device__ __forceinline__ float scale_of(unsigned top) {
+    const float s = __builtin_bit_cast(float, top) / kF8Max;
+    return top == 0 ? 1.f : (s == 0.f ? __builtin_bit_cast(float, 1u) : s);
+}
 
 // y / scale inside the format's range: a subnormal scale can round the
 // quotient of the row's largest value past it, which the conversion would turn

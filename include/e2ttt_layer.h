@@ -118,7 +118,7 @@ E2TTT_API int e2ttt_paged_attention(const e2ttt_paged_desc* desc, const void* q,
  *   rstd = 1 / sqrt(mean(h^2) + eps),  y = h rstd weight,
  * y in the stream's type, or with bits8 in OCP e4m3 with an fp32 scale per
  * row: scale = max|y| / 448 (1 for a row of zeros, NaN for one that holds a
- * NaN), y8 = round(y / scale).
+ * NaN, and at least 2^-149), y8 = round(y / scale).
  *   x, residual, h  [rows][width] io_dtype contiguous; weight [width] fp32
  *   y               [rows][width] io_dtype, or uint8 with bits8
  *   scale           [rows] fp32, with bits8 only; rstd [rows] fp32 or NULL

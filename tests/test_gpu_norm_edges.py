@@ -25,3 +25,25 @@ def test_a_nan_in_the_weight_reaches_the_scale(W, dtype):
     assert bool(torch.isnan(scale).all()) and bool(torch.isnan(y.float()).all())
     y, _, _, _ = e2.norm_forward(x, w)  # in the stream's type it stays where it is
     assert torch.isnan(y).sum(dim=1).tolist() == [1, 1, 1]
+
+
+@pytest.mark.parametrize("W", [64, 999, 4095, 9001])
+@pytest.mark.parametrize("units", [1, 3, 100, 223, 225, 448, 5000])
+def test_rows_whose_scale_is_the_smallest_value(units, W):
+    """Rows of zeros and of values of a few times 2^-149: the zeros stay zeros and
+    the products with the scale stay within half a step of e4m3, a sixteenth of a
+    value, and of 2^-149."""
+    import chunk_weight_rnn_amd as e2
+    note(f"scale near 2^-149: {units} W={W}")
+    tiny = 2.0 ** -149
+    x = torch.zeros(2, W, device="cuda", dtype=torch.float64)
+    x[:, ::3] = 2.0 ** -126
+    w = torch.full((W,), units * 2.0 ** -23, device="cuda")  # x w = units 2^-149, exactly, and rstd is 1
+    y, scale, _, _ = e2.norm_forward(x.float(), w, eps=1.0, bits8=True)
+    y, scale = y.double(), scale.double()
+    assert bool((scale > 0).all())
+    assert bool((y[x == 0] == 0).all())
+    off = (y * scale[:, None] - torch.where(x > 0, units * tiny, 0.0)).abs()
+    # the scale is rounded to whole 2^-149, and a quotient past 448 is 448
+    bound = units * tiny / 16 + 0.5 * tiny + (448 * 0.5 * tiny if units >= 224 else 0.0)
+    assert float(off.max()) <= bound
