@@ -84,6 +84,14 @@ __device__ __forceinline__ unsigned pk8(float a, float b) {
     return __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false) & 0xFFFFu;
 }
 
+// HIP takes fewer than 2^32 threads along a dimension of a grid, which 2^31 rows
+// of a workgroup each exceed: the workgroups stand in two dimensions.
+constexpr int64_t kGridX = 1 << 21;
+dim3 grid_of(int64_t groups) {
+    return groups <= kGridX ? dim3((unsigned)groups) : dim3((unsigned)kGridX, (unsigned)((groups + kGridX - 1) / kGridX));
+}
+__device__ __forceinline__ int64_t group_index() { return (int64_t)blockIdx.y * gridDim.x + blockIdx.x; }
+
 constexpr float kF8Max = 448.f;
 
 // A row's scale, from its largest magnitude: NaN if that is, 1 for zeros.  Not less
@@ -105,7 +113,7 @@ template <typename T, int V, int WPR, int NV>
 __global__ __launch_bounds__(256) void norm_fwd_kernel(NormArgs a) {
     constexpr int TPR = 64 * WPR;  // threads per row
     __shared__ float sh[16];
-    const int64_t row = WPR == 1 ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6) : blockIdx.x;
+    const int64_t row = WPR == 1 ? group_index() * 4 + (threadIdx.x >> 6) : group_index();
     if (row >= a.rows) return;
     const int t = WPR == 1 ? (threadIdx.x & 63) : threadIdx.x;
     const int W = (int)a.width;
@@ -190,7 +198,8 @@ __global__ __launch_bounds__(256) void norm_fwd_kernel(NormArgs a) {
 template <typename T>
 __global__ __launch_bounds__(1024) void norm_fwd_wide_kernel(NormArgs a) {
     __shared__ float sh[16];
-    const int64_t row = blockIdx.x;
+    const int64_t row = group_index();
+    if (row >= a.rows) return;
     const int W = (int)a.width;
     const T* x = (const T*)a.x + row * W;
     const T* res = a.residual ? (const T*)a.residual + row * W : nullptr;
@@ -316,7 +325,8 @@ __global__ __launch_bounds__(256) void norm_bwd_kernel(NormBwdArgs a) {
 template <typename T>
 __global__ __launch_bounds__(1024) void norm_bwd_wide_dx_kernel(NormBwdArgs a) {
     __shared__ float sh[16];
-    const int64_t row = blockIdx.x;
+    const int64_t row = group_index();
+    if (row >= a.rows) return;
     const int W = (int)a.width;
     const T *dy = (const T*)a.dy + row * W, *h = (const T*)a.h + row * W;
     const float rstd = a.rstd[row];
@@ -374,15 +384,15 @@ template <typename T>
 hipError_t norm_forward(const NormArgs& a, hipStream_t s) {
     constexpr int V = kVec<T>;
     const int64_t W = a.width;
-    const unsigned per_row = (unsigned)a.rows, four = (unsigned)((a.rows + 3) / 4);
+    const dim3 per_row = grid_of(a.rows), four = grid_of((a.rows + 3) / 4);
     if (vector_rows<T>(W)) {
-        if (W <= 64 * V * 4) norm_fwd_kernel<T, V, 1, 4><<<dim3(four), dim3(256), 0, s>>>(a);
-        else if (W <= 256 * V * 4) norm_fwd_kernel<T, V, 4, 4><<<dim3(per_row), dim3(256), 0, s>>>(a);
-        else norm_fwd_wide_kernel<T><<<dim3(per_row), dim3(1024), 0, s>>>(a);
+        if (W <= 64 * V * 4) norm_fwd_kernel<T, V, 1, 4><<<four, dim3(256), 0, s>>>(a);
+        else if (W <= 256 * V * 4) norm_fwd_kernel<T, V, 4, 4><<<per_row, dim3(256), 0, s>>>(a);
+        else norm_fwd_wide_kernel<T><<<per_row, dim3(1024), 0, s>>>(a);
     } else {
-        if (W <= 64 * 16) norm_fwd_kernel<T, 1, 1, 16><<<dim3(four), dim3(256), 0, s>>>(a);
-        else if (W <= 256 * 16) norm_fwd_kernel<T, 1, 4, 16><<<dim3(per_row), dim3(256), 0, s>>>(a);
-        else norm_fwd_wide_kernel<T><<<dim3(per_row), dim3(1024), 0, s>>>(a);
+        if (W <= 64 * 16) norm_fwd_kernel<T, 1, 1, 16><<<four, dim3(256), 0, s>>>(a);
+        else if (W <= 256 * 16) norm_fwd_kernel<T, 1, 4, 16><<<per_row, dim3(256), 0, s>>>(a);
+        else norm_fwd_wide_kernel<T><<<per_row, dim3(1024), 0, s>>>(a);
     }
     return hipGetLastError();
 }
@@ -409,7 +419,7 @@ hipError_t norm_backward(const NormBwdArgs& a, hipStream_t s) {
         norm_bwd_wide_dw_kernel<T><<<dim3((unsigned)((W + 255) / 256), groups), bl, 0, s>>>(a);
         hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
-        norm_bwd_wide_dx_kernel<T><<<dim3((unsigned)a.rows), dim3(1024), 0, s>>>(a);
+        norm_bwd_wide_dx_kernel<T><<<grid_of(a.rows), dim3(1024), 0, s>>>(a);
     } else if (vector_rows<T>(W)) {
         if (waves == 1) norm_bwd_kernel<T, V, 1, 4><<<gr, bl, 0, s>>>(a);
         else norm_bwd_kernel<T, V, 4, 4><<<gr, bl, 0, s>>>(a);

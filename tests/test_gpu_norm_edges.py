@@ -47,3 +47,37 @@ def test_rows_whose_scale_is_the_smallest_value(units, W):
     # the scale is rounded to whole 2^-149, and a quotient past 448 is 448
     bound = units * tiny / 16 + 0.5 * tiny + (448 * 0.5 * tiny if units >= 224 else 0.0)
     assert float(off.max()) <= bound
+
+
+def repeated(block, rows):
+    """The rows of `block` again and again, `rows` in all."""
+    big = torch.empty(rows, block.shape[1], dtype=block.dtype, device="cuda")
+    for a in range(0, rows, block.shape[0]):
+        n = min(block.shape[0], rows - a)
+        big[a:a + n] = block[:n]
+    return big
+
+
+def same_rows(big, block):
+    return all(torch.equal(big[a:a + block.shape[0]], block[:big.shape[0] - a])
+               for a in range(0, big.shape[0], block.shape[0]))
+
+
+# more rows than workgroups that one dimension of a grid may have: four rows to a
+# workgroup of 256 threads, one to 256, one to 1024
+@pytest.mark.parametrize("W,rows", [(8, (1 << 26) + 5), (1025, (1 << 24) + 3), (4097, (1 << 22) + 3)])
+def test_more_rows_than_a_dimension_of_a_grid(W, rows):
+    import chunk_weight_rnn_amd as e2
+    note(f"norm of {rows} rows of {W}")
+    block = torch.randn(1 << 19, W, dtype=torch.bfloat16, device="cuda")
+    w = torch.rand(W, device="cuda")
+    x = repeated(block, rows)
+    y, _, _, rstd = e2.norm_forward(x, w)
+    want, _, _, want_rstd = e2.norm_forward(block, w)
+    assert same_rows(y, want) and same_rows(rstd[:, None], want_rstd[:, None])
+    del y
+    dx, _ = e2.norm_backward(x, x, w, rstd)
+    want, _ = e2.norm_backward(block, block, w, want_rstd)
+    assert same_rows(dx, want)
+    del x, dx, rstd, block, want, want_rstd
+    torch.cuda.empty_cache()
