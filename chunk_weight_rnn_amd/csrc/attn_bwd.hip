@@ -479,7 +479,7 @@ __global__ __launch_bounds__(256, 2) void attn_dkdv_kernel(AttnBwdArgs a) {
 template <int DP>
 hipError_t launch(const AttnBwdArgs& a, hipStream_t s) {
     const int64_t dq_grid = (a.N * a.G / BM + a.S) * a.K + a.clear, dkv_grid = (a.N / BK + a.S) * a.K + a.clear;
-    if (dq_grid > 0x7fffffff) return hipErrorInvalidValue;
+    if (dq_grid > kMaxGroups || dkv_grid > kMaxGroups) return hipErrorInvalidConfiguration;
     attn_dq_kernel<DP><<<dim3((unsigned)dq_grid), dim3(256), 0, s>>>(a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;

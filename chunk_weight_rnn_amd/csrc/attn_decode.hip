@@ -373,7 +373,7 @@ hipError_t launch(const AttnArgs& a, hipStream_t s) {
     const int64_t items = (int64_t)a.ntiles * a.K;
     const int64_t groups = a.nsplit > 1 ? kDecodeGroups : items;
     const int64_t grid = groups + a.clear + append_blocks(a, 8);
-    if (grid > 0x7fffffff) return hipErrorInvalidValue;
+    if (grid > kMaxGroups || items > kMaxGroups) return hipErrorInvalidConfiguration;
     if (a.nsplit > 1)
         attn_decode_kernel<DP, true><<<dim3((unsigned)grid), dim3(256), 0, s>>>(a, (int)groups);
     else

@@ -806,7 +806,7 @@ hipError_t launch_fwd(const AttnArgs& a, hipStream_t s) {
     const bool paged = a.pg.kc != nullptr;
     const int64_t grid = (int64_t)a.ntiles * a.K * a.nsplit + a.clear + (paged ? append_blocks(a, 4) : 0);
     if (grid == 0) return hipSuccess;
-    if (grid > 0x7fffffff) return hipErrorInvalidValue;
+    if (grid > kMaxGroups) return hipErrorInvalidConfiguration;
     if (paged)
         attn_f32_fwd_kernel<DP, true><<<dim3((unsigned)grid), dim3(256), 0, s>>>(a);
     else
@@ -821,7 +821,7 @@ hipError_t launch_bwd(const AttnBwdArgs& a, hipStream_t s) {
     const int64_t dkv_grid = (a.N / B + a.S) * a.K * a.dkv_parts + a.clear;
     const int64_t sums = a.N * a.D * ((a.dq_parts > 1 ? a.H : 0) + (a.dkv_parts > 1 ? 2 * a.K : 0));
     const int64_t sum_grid = (sums / 4 + 255) / 256;
-    if (dq_grid > 0x7fffffff || dkv_grid > 0x7fffffff || sum_grid > 0x7fffffff) return hipErrorInvalidValue;
+    if (dq_grid > kMaxGroups || dkv_grid > kMaxGroups || sum_grid > kMaxGroups) return hipErrorInvalidConfiguration;
     attn_f32_dq_kernel<DP, RT><<<dim3((unsigned)dq_grid), dim3(256), 0, s>>>(a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;

@@ -342,7 +342,7 @@ hipError_t launch(const AttnArgs& a, hipStream_t s) {
     const bool paged = a.pg.kc != nullptr;
     const int64_t grid = (int64_t)a.ntiles * a.K * a.nsplit + a.clear + (paged ? append_blocks(a, 8) : 0);
     if (grid == 0) return hipSuccess;
-    if (grid > 0x7fffffff) return hipErrorInvalidValue;
+    if (grid > kMaxGroups) return hipErrorInvalidConfiguration;
     const dim3 gr((unsigned)grid), bl(256);
     if (paged && a.nsplit > 1)
         attn_fwd_kernel<DP, true, true><<<gr, bl, 0, s>>>(a);
@@ -365,7 +365,7 @@ hipError_t launch_attn_fwd_bf16(const AttnArgs& a, hipStream_t s) {
 hipError_t launch_attn_join(const AttnArgs& a, bool f32, hipStream_t s) {
     const int64_t grid = (a.N * a.H + 7) / 8;
     if (grid == 0) return hipSuccess;
-    if (grid > 0x7fffffff) return hipErrorInvalidValue;
+    if (grid > kMaxGroups) return hipErrorInvalidConfiguration;
     if (f32)
         attn::attn_join_kernel<float><<<dim3((unsigned)grid), dim3(256), 0, s>>>(a);
     else

@@ -176,11 +176,16 @@ int alias_status(const Span (&in)[NI], const Span (&out)[NO]) {
     return E2TTT_OK;
 }
 
-int run_forward(AttnArgs& a, bool f32, hipStream_t s) {
-    if (a.decode) return launch_attn_decode_bf16(a, s) == hipSuccess ? E2TTT_OK : E2TTT_ERR_HIP;
-    hipError_t e = f32 ? launch_attn_fwd_f32(a, s) : launch_attn_fwd_bf16(a, s);
-    if (e == hipSuccess && a.nsplit > 1) e = launch_attn_join(a, f32, s);
+int launch_status(hipError_t e) {
+    if (e == hipErrorInvalidConfiguration) return E2TTT_ERR_UNSUPPORTED;  // kMaxGroups
     return e == hipSuccess ? E2TTT_OK : E2TTT_ERR_HIP;
+}
+
+int run_forward(AttnArgs& a, bool f32, hipStream_t s) {
+    if (a.decode) return launch_status(launch_attn_decode_bf16(a, s));
+    hipError_t e = f32 ? launch_attn_fwd_f32(a, s) : launch_attn_fwd_bf16(a, s);
+    if (e == hipSuccess && a.nsplit > 1) e = launch_attn_join(a, f32, s);  // split calls have few rows
+    return launch_status(e);
 }
 
 bool norm_desc_ok(const e2ttt_norm_desc* d) {
@@ -302,7 +307,7 @@ int e2ttt_attention_backward(const e2ttt_attention_desc* d, const void* q, const
     a.dv = dv;
     const hipError_t e = d->io_dtype == E2TTT_F32 ? launch_attn_bwd_f32(a, (hipStream_t)stream)
                                                   : launch_attn_bwd_bf16(a, (hipStream_t)stream);
-    return e == hipSuccess ? E2TTT_OK : E2TTT_ERR_HIP;
+    return launch_status(e);
 }
 
 size_t e2ttt_paged_workspace_size(const e2ttt_paged_desc* d) {

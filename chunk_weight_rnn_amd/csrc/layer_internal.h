@@ -11,6 +11,11 @@ namespace e2ttt {
 
 hipError_t device_cu_count(int* ncu);
 
+// Workgroups of 256 threads in a grid, at most: HIP counts the threads along a
+// dimension in 32 bits, and a larger grid wraps around without an error.
+// Launchers return hipErrorInvalidConfiguration for it, before they launch.
+constexpr int64_t kMaxGroups = (1 << 24) - 1;
+
 // Key/value pages of a paged call; kc == nullptr: packed sequences, no cache.
 struct PagedKV {
     void *kc, *vc;                   // pool, written where new tokens are appended

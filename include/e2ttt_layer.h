@@ -15,6 +15,10 @@
  * call and the status is returned; no exception crosses the ABI; NaN and Inf
  * reach the results that depend on them and, masked, no other.  Statuses and types are those of e2ttt.h.  Every result is the
  * same bit for bit from call to call (no floating-point atomics).
+ * Attention calls whose launch would take 2^24 workgroups or more are
+ * E2TTT_ERR_UNSUPPORTED: each is a tile of one key head, of 128 (token, head)
+ * rows or 64 keys in bf16 and 16 in fp32, at least one for every sequence, or
+ * 4 KiB of new keys where a cache is extended.
  * What a device tensor holds (offsets, lengths, page indices) cannot be
  * checked on the host: the kernels clamp it, so that bad values give wrong
  * results but no access outside the tensors.
