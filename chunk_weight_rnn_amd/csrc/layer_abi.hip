@@ -3,6 +3,8 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <initializer_list>
+
 #include "layer_internal.h"
 
 namespace e2ttt {
@@ -191,6 +193,13 @@ int run_forward(AttnArgs& a, bool f32, hipStream_t s) {
 bool norm_desc_ok(const e2ttt_norm_desc* d) {
     return d && d->reserved == 0 && (d->io_dtype == E2TTT_F32 || d->io_dtype == E2TTT_BF16) &&
            (d->bits8 == 0 || d->bits8 == 1) && d->rows >= 0 && d->width >= 1 && d->eps >= 0.f && isfinite(d->eps);
+}
+
+// Whether every row starts on 16 bytes in all of these (null ones do not count).
+int norm_rows_aligned(const e2ttt_norm_desc* d, std::initializer_list<const void*> ps) {
+    bool ok = d->width * elem(d->io_dtype) % 16 == 0;
+    for (const void* p : ps) ok = ok && (uintptr_t)p % 16 == 0;
+    return ok;
 }
 
 bool norm_supported(const e2ttt_norm_desc* d) { return d->width <= 65536 && d->rows <= 0x7fffffff; }
@@ -384,17 +393,19 @@ int e2ttt_norm_forward(const e2ttt_norm_desc* d, const void* x, const void* resi
     if (!norm_supported(d)) return E2TTT_ERR_UNSUPPORTED;
     if (d->rows == 0) return E2TTT_OK;
     if ((residual == nullptr) != (h == nullptr)) return E2TTT_ERR_INVALID_ARG;
-    if (!aligned(x, 16) || !aligned(weight, 16) || !aligned(y, 16)) return E2TTT_ERR_INVALID_ARG;
-    if (residual && (!aligned(residual, 16) || !aligned(h, 16))) return E2TTT_ERR_INVALID_ARG;
+    const size_t es = elem(d->io_dtype);
+    if (!aligned(x, es) || !aligned(weight, 4) || !aligned(y, d->bits8 ? 1 : es)) return E2TTT_ERR_INVALID_ARG;
+    if (residual && (!aligned(residual, es) || !aligned(h, es))) return E2TTT_ERR_INVALID_ARG;
     if (d->bits8 ? !aligned(scale, 4) : scale != nullptr) return E2TTT_ERR_INVALID_ARG;
     if (rstd && !aligned(rstd, 4)) return E2TTT_ERR_INVALID_ARG;
-    const int64_t n = d->rows * d->width, b = n * elem(d->io_dtype);
+    const int64_t n = d->rows * d->width, b = n * es;
     const Span xs = span(x, b), rs = span(residual, b), hs = span(h, b);
     const Span in[3] = {h == x ? Span{} : xs, h == residual ? Span{} : rs, span(weight, 4 * d->width)};
     const Span outs[4] = {hs, span(y, d->bits8 ? n : b), span(scale, 4 * d->rows), span(rstd, 4 * d->rows)};
     const int ast = alias_status(in, outs);
     if (ast != E2TTT_OK) return ast;
-    NormArgs a{x, residual, weight, y, scale, h, rstd, d->rows, d->width, d->eps, d->io_dtype == E2TTT_F32, d->bits8};
+    NormArgs a{x, residual, weight, y, scale, h, rstd, d->rows, d->width, d->eps, d->io_dtype == E2TTT_F32, d->bits8,
+               norm_rows_aligned(d, {x, residual, weight, y, h})};
     return launch_norm_forward(a, (hipStream_t)stream) == hipSuccess ? E2TTT_OK : E2TTT_ERR_HIP;
 }
 
@@ -408,11 +419,12 @@ int e2ttt_norm_backward(const e2ttt_norm_desc* d, const void* dy, const void* h,
                         void* stream) {
     if (!norm_desc_ok(d) || d->bits8) return E2TTT_ERR_INVALID_ARG;
     if (!norm_supported(d)) return E2TTT_ERR_UNSUPPORTED;
-    if (!aligned(dweight, 16)) return E2TTT_ERR_INVALID_ARG;
-    const int64_t b = d->rows * d->width * elem(d->io_dtype);
+    if (!aligned(dweight, 4)) return E2TTT_ERR_INVALID_ARG;
+    const size_t es = elem(d->io_dtype);
+    const int64_t b = d->rows * d->width * es;
     if (d->rows > 0) {
-        if (!aligned(dy, 16) || !aligned(h, 16) || !aligned(weight, 16) || !aligned(rstd, 4) || !aligned(dx, 16) ||
-            (dh && !aligned(dh, 16)))
+        if (!aligned(dy, es) || !aligned(h, es) || !aligned(weight, 4) || !aligned(rstd, 4) || !aligned(dx, es) ||
+            (dh && !aligned(dh, es)))
             return E2TTT_ERR_INVALID_ARG;
         const size_t need = e2ttt_norm_backward_workspace_size(d);
         const int wst = workspace_status(ws, ws_bytes, need);
@@ -423,7 +435,8 @@ int e2ttt_norm_backward(const e2ttt_norm_desc* d, const void* dy, const void* h,
         const int ast = alias_status(in, outs);
         if (ast != E2TTT_OK) return ast;
     }
-    NormBwdArgs a{dy, h, dh, weight, rstd, dx, dweight, (float*)ws, d->rows, d->width, d->io_dtype == E2TTT_F32};
+    NormBwdArgs a{dy, h, dh, weight, rstd, dx, dweight, (float*)ws, d->rows, d->width, d->io_dtype == E2TTT_F32,
+                  norm_rows_aligned(d, {dy, h, dh, weight, dx})};
     return launch_norm_backward(a, (hipStream_t)stream) == hipSuccess ? E2TTT_OK : E2TTT_ERR_HIP;
 }
 

@@ -92,6 +92,7 @@ struct NormArgs {
     int64_t rows, width;
     float eps;
     int f32, bits8;
+    int vec;  // every row of every tensor starts on 16 bytes
 };
 hipError_t launch_norm_forward(const NormArgs& a, hipStream_t s);
 
@@ -102,6 +103,7 @@ struct NormBwdArgs {
     float *dweight, *part;  // part: [norm_bwd_groups][width]
     int64_t rows, width;
     int f32;
+    int vec;  // as in NormArgs
 };
 int norm_bwd_groups(int64_t rows);
 hipError_t launch_norm_backward(const NormBwdArgs& a, hipStream_t s);

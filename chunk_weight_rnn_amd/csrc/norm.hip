@@ -9,8 +9,8 @@
 //
 // HBM bound.  A row is held in registers, so every tensor passes once: WPR
 // waves per row (one up to 64 threads' worth, four up to 256), NV units of V
-// consecutive values per thread (V = 16 bytes' worth where rows keep 16-byte
-// alignment, else 1).  The weight's gradient is summed in registers over the rows
+// consecutive values per thread (V = 16 bytes' worth where every row starts on
+// 16 bytes, else 1).  The weight's gradient is summed in registers over the rows
 // a workgroup walks, written once per workgroup and summed by a second launch in a
 // fixed order.
 //
@@ -375,17 +375,12 @@ __global__ __launch_bounds__(256) void norm_dw_sum_kernel(const float* part, flo
 template <typename T>
 constexpr int kVec = 16 / sizeof(T);
 
-// 16-byte units: every row starts on a 16-byte boundary (the tensors do, and
-// the width keeps it).
-template <typename T>
-bool vector_rows(int64_t width) { return width % kVec<T> == 0; }
-
 template <typename T>
 hipError_t norm_forward(const NormArgs& a, hipStream_t s) {
     constexpr int V = kVec<T>;
     const int64_t W = a.width;
     const dim3 per_row = grid_of(a.rows), four = grid_of((a.rows + 3) / 4);
-    if (vector_rows<T>(W)) {
+    if (a.vec) {
         if (W <= 64 * V * 4) norm_fwd_kernel<T, V, 1, 4><<<four, dim3(256), 0, s>>>(a);
         else if (W <= 256 * V * 4) norm_fwd_kernel<T, V, 4, 4><<<per_row, dim3(256), 0, s>>>(a);
         else norm_fwd_wide_kernel<T><<<per_row, dim3(1024), 0, s>>>(a);
@@ -399,8 +394,8 @@ hipError_t norm_forward(const NormArgs& a, hipStream_t s) {
 
 // Rows that the register form of the backward holds: 0 none, 1 a wave's, 4 a workgroup's.
 template <typename T>
-int bwd_waves(int64_t W) {
-    const int64_t one = vector_rows<T>(W) ? 64 * kVec<T> * 4 : 64 * 16;
+int bwd_waves(int64_t W, bool vec) {
+    const int64_t one = vec ? 64 * kVec<T> * 4 : 64 * 16;
     return W <= one ? 1 : (W <= 4 * one ? 4 : 0);
 }
 
@@ -409,7 +404,7 @@ hipError_t norm_backward(const NormBwdArgs& a, hipStream_t s) {
     constexpr int V = kVec<T>;
     const int64_t W = a.width;
     const int groups = norm_bwd_groups(a.rows);
-    const int waves = bwd_waves<T>(W);
+    const int waves = bwd_waves<T>(W, a.vec);
     const dim3 gr(groups), bl(256);
     if (a.rows == 0) {  // an empty sum
         norm_dw_sum_kernel<<<dim3((unsigned)((W + 15) / 16)), bl, 0, s>>>(nullptr, a.dweight, 0, (int)W);
@@ -420,7 +415,7 @@ hipError_t norm_backward(const NormBwdArgs& a, hipStream_t s) {
         hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
         norm_bwd_wide_dx_kernel<T><<<grid_of(a.rows), dim3(1024), 0, s>>>(a);
-    } else if (vector_rows<T>(W)) {
+    } else if (a.vec) {
         if (waves == 1) norm_bwd_kernel<T, V, 1, 4><<<gr, bl, 0, s>>>(a);
         else norm_bwd_kernel<T, V, 4, 4><<<gr, bl, 0, s>>>(a);
     } else {

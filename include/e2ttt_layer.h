@@ -126,6 +126,8 @@ E2TTT_API int e2ttt_paged_attention(const e2ttt_paged_desc* desc, const void* q,
  *   x, residual, h  [rows][width] io_dtype contiguous; weight [width] fp32
  *   y               [rows][width] io_dtype, or uint8 with bits8
  *   scale           [rows] fp32, with bits8 only; rstd [rows] fp32 or NULL
+ * Tensors are aligned to their elements; rows that all start on 16 bytes (the
+ * tensors, and width times the element's size) are read in wider loads.
  * residual = h = NULL for the norm alone.  h may be residual or x (in place);
  * any other overlap of an output is E2TTT_ERR_ALIAS.
  */

@@ -2,8 +2,10 @@
 import pytest
 import torch
 
+from tests import layer_ref as ref
 from tests.gpu_util import note
-from tests.test_gpu_attention import TYPES
+from tests.test_gpu_attention import TYPES, f64, within
+from tests.test_gpu_norm import make, rounder
 
 pytestmark = pytest.mark.gpu
 
@@ -81,3 +83,41 @@ def test_more_rows_than_a_dimension_of_a_grid(W, rows):
     assert same_rows(dx, want)
     del x, dx, rstd, block, want, want_rstd
     torch.cuda.empty_cache()
+
+
+def shifted(t):
+    """The same values one element past an allocation's start."""
+    flat = torch.empty(t.numel() + 1, dtype=t.dtype, device="cuda")
+    flat[1:] = t.flatten()
+    return flat[1:].view(t.shape)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("W", [1, 64, 777, 2048, 4104, 9001])
+def test_tensors_aligned_to_their_elements_alone(W, dtype):
+    import chunk_weight_rnn_amd as e2
+    note(f"norm of shifted tensors W={W} {dtype}")
+    x, r, w, dy, dh = (shifted(t) for t in make(5, W, dtype, True, seed=W))
+    y, _, h, rstd = e2.norm_forward(x, w, residual=r, h=shifted(r))
+    dx, dw = e2.norm_backward(dy, h, w, rstd, dh=dh)
+    want = ref.norm(f64(x), f64(r), f64(w), 1e-6, dtype, rounder(dtype), f64(dy), f64(dh))
+    for n, t in (("h", h), ("rstd", rstd), ("y", y), ("dx", dx), ("dweight", dw)):
+        within(n, t, *want[n], f"W={W} {dtype}")
+    y8, scale, _, _ = e2.norm_forward(h, w, bits8=True)
+    assert bool(torch.isfinite(y8.float()).all())
+    # half a step of e4m3, 2^-4 of a value or half of 2^-9, and what y itself is off
+    val, bnd = want["y32"]
+    within("y8", y8.double() * scale.double()[:, None], val, 1.01 * abs(val) / 16 + f64(scale)[:, None] * 2.0 ** -9 + bnd)
+
+
+def test_gradients_of_rows_put_together():
+    """What arrives from a concatenation are slices of one gradient, which start anywhere."""
+    import chunk_weight_rnn_amd as e2
+    g = torch.Generator(device="cuda").manual_seed(4)
+    a, b, dy = (torch.randn(n, 777, generator=g, device="cuda").bfloat16() for n in (3, 5, 8))
+    w = torch.ones(777, device="cuda")
+    leaves = [t.clone().requires_grad_(True) for t in (a, b)]
+    torch.cat([e2.rms_norm(t, w)[0] for t in leaves]).backward(dy)
+    for t, leaf, d in ((a, leaves[0], dy[:3]), (b, leaves[1], dy[3:])):
+        rstd = e2.norm_forward(t, w)[3]
+        assert torch.equal(leaf.grad, e2.norm_backward(d.clone(), t, w, rstd)[0])
