@@ -570,7 +570,7 @@ __global__ __launch_bounds__(256, 2) void attn_f32_dq_kernel(AttnBwdArgs a) {
 }
 
 // STEADY: the group's size divides 16, so that a tile starts on a token and a
-// lane's offsets are the same in every tile.
+// lane's offsets are the same in every tile, and the strides keep them in 31 bits.
 template <int DP, int RT, bool STEADY>
 __global__ __launch_bounds__(256, DP == 64 ? 2 : 1) void attn_f32_dkdv_kernel(AttnBwdArgs a) {
     constexpr int S4 = DP / 16, LD = DP + 4, BK = 16 * RT;
@@ -825,7 +825,7 @@ hipError_t launch_bwd(const AttnBwdArgs& a, hipStream_t s) {
     attn_f32_dq_kernel<DP, RT><<<dim3((unsigned)dq_grid), dim3(256), 0, s>>>(a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    if (16 % a.G == 0) attn_f32_dkdv_kernel<DP, RT, true><<<dim3((unsigned)dkv_grid), dim3(256), 0, s>>>(a);
+    if (16 % a.G == 0 && a.q_head < (1 << 25) / a.G) attn_f32_dkdv_kernel<DP, RT, true><<<dim3((unsigned)dkv_grid), dim3(256), 0, s>>>(a);
     else attn_f32_dkdv_kernel<DP, RT, false><<<dim3((unsigned)dkv_grid), dim3(256), 0, s>>>(a);
     e = hipGetLastError();
     if (e != hipSuccess || sums == 0) return e;

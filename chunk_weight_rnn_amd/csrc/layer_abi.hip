@@ -38,7 +38,8 @@ bool stride_ok(int64_t s, int64_t es) { return s >= 0 && s % (16 / es) == 0; }
 
 // Sizes, types and strides.  Limits keep every 32-bit index of the kernels in
 // range: row numbers, r G in the division by the group, and a tile's byte
-// offsets in the buffer copies.
+// offsets in the buffer copies, which hold token strides.  Head strides are only
+// kept where their products fit in 64 bits.
 int attention_desc_status(const e2ttt_attention_desc* d, bool packed_kv) {
     if (!d || d->reserved != 0) return E2TTT_ERR_INVALID_ARG;
     if (d->io_dtype != E2TTT_F32 && d->io_dtype != E2TTT_BF16) return E2TTT_ERR_INVALID_ARG;
@@ -46,7 +47,7 @@ int attention_desc_status(const e2ttt_attention_desc* d, bool packed_kv) {
     if (d->heads < 1 || d->kv_heads < 1 || d->heads % d->kv_heads || d->D < 1) return E2TTT_ERR_INVALID_ARG;
     if (!(d->scale > 0.f) || !isfinite(d->scale)) return E2TTT_ERR_INVALID_ARG;
     if (d->D % 8 || d->D > 128) return E2TTT_ERR_UNSUPPORTED;
-    const int64_t es = elem(d->io_dtype), lim = (int64_t)1 << 23;
+    const int64_t es = elem(d->io_dtype), lim[2] = {(int64_t)1 << 23, (int64_t)1 << 40};  // token, head
     if (d->heads > 65536 || d->seqs >= (1 << 28) || d->tokens > 0x7fffffff) return E2TTT_ERR_UNSUPPORTED;
     const int64_t st[6] = {d->q_tok, d->q_head, d->k_tok, d->k_head, d->v_tok, d->v_head};
     const int64_t sizes[6] = {d->tokens, d->heads, d->tokens, d->kv_heads, d->tokens, d->kv_heads};
@@ -55,7 +56,7 @@ int attention_desc_status(const e2ttt_attention_desc* d, bool packed_kv) {
     if (d->tokens > 1 && (d->q_tok < d->D || (packed_kv && (d->k_tok < d->D || d->v_tok < d->D))))
         return E2TTT_ERR_INVALID_ARG;
     for (int i = 0; i < (packed_kv ? 6 : 2); ++i)
-        if (sizes[i] > 1 && st[i] > lim) return E2TTT_ERR_UNSUPPORTED;
+        if (sizes[i] > 1 && st[i] > lim[i % 2]) return E2TTT_ERR_UNSUPPORTED;
     const int64_t G = d->heads / d->kv_heads;
     if ((d->tokens + 256) * d->heads > 0x7fffffff) return E2TTT_ERR_UNSUPPORTED;
     if ((d->tokens + 256) * G >= ((int64_t)1 << 32) / G) return E2TTT_ERR_UNSUPPORTED;

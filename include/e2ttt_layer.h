@@ -51,7 +51,8 @@ typedef struct {
     int32_t reserved;           /* 0 */
     /* strides in elements, multiples of 16 bytes, of q [N][heads][D],
      * k and v [N][kv_heads][D] over tokens and heads (the last dimension is
-     * contiguous); so views of one projection's output need no copy */
+     * contiguous), of tokens up to 2^23; so views of one projection's output,
+     * or of tensors that hold head after head, need no copy */
     int64_t q_tok, q_head, k_tok, k_head, v_tok, v_head;
 } e2ttt_attention_desc;
 

@@ -1,5 +1,5 @@
 """Edges of the layer's operators on the GPU: windows wider than every context, tokens
-outside every sequence."""
+outside every sequence, heads far apart."""
 import numpy as np
 import pytest
 import torch
@@ -112,3 +112,27 @@ def test_new_tokens_outside_every_sequence(new, cached, before, after, dtype):
     assert float((inside.float() - want.float()).abs().max()) <= 4 * u * float(torch.stack([v.abs().max(), vc.abs().max()]).max())
     assert bool((got[:before] == 0).all()) and bool((got[before + sum(new):] == 0).all())
     assert all(torch.equal(a, b) for a, b in zip(*caches))  # and their keys and values go nowhere
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("H,K", [(4, 2), (3, 1), (2, 2)])
+@pytest.mark.parametrize("far", [1 << 23, (1 << 25) + 8])
+def test_heads_far_apart(far, H, K, dtype):
+    """Head-major tensors of long sequences: heads 2^23 values apart and more, whose
+    offsets within a tile leave 31 bits."""
+    import chunk_weight_rnn_amd as e2
+    note(f"heads {far} apart H={H} K={K} {dtype}")
+
+    def spread(t):
+        n, h, d = t.shape
+        s = torch.empty((h - 1) * (far + 8) + n * d, dtype=t.dtype, device="cuda").as_strided(t.shape, (d, far + 8, 1))
+        return s.copy_(t)
+    q, k, v, dout = make([300, 41], H, K, 64, dtype, view=False)
+    cu = offsets([300, 41])
+    got = []
+    for x in ((q, k, v), tuple(spread(t) for t in (q, k, v))):
+        out, lse = e2.attention_forward(*x, cu)
+        got.append([out, lse, *e2.attention_backward(*x, out, lse, dout, cu).values()])
+    assert all(torch.equal(a, b) for a, b in zip(*got))
+    m = _paged(TYPES[dtype], [1, 100], H, K, 64, 16, [700, 90])
+    assert torch.equal(e2.paged_attention(*m), e2.paged_attention(*(spread(t) for t in m[:3]), *m[3:]))
