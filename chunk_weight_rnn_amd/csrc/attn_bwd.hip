@@ -16,8 +16,8 @@
 // the next product's operand (attn_common.h): S^T with a query per lane for
 // dq, S with a key per lane for dk and dv.
 //
-// 12 packed sequences of up to 2K, 16 heads of 128 over 4: dq 110 us (three
-// products, 350 Tflop/s), dk and dv 178 us (four, 290).  Bound by each wave's own
+// 12 packed sequences of up to 2K, 16 heads of 128 over 4: dq 103 us (three
+// products, 744 Tflop/s), dk and dv 177 us (four, 577).  Bound by each wave's own
 // chain: two waves per SIMD, the registers' limit, hide the exponentials, the
 // packing and the LDS reads of the next operands only in part.
 #include "attn_common.h"
@@ -299,7 +299,9 @@ __global__ __launch_bounds__(256, 2) void attn_dkdv_kernel(AttnBwdArgs a) {
     const char* dsrc = (const char*)a.dout + 2 * first_row * a.D;
     // A group whose size divides the tile starts every tile on a token: a
     // lane's offsets are the same in all of them, and only the base moves.
-    // Otherwise they come anew from the row number.
+    // Otherwise they come anew from the row number, and at 128 columns through
+    // spilled registers, each of whose loads waits for the copies before it: 12
+    // heads over 4 take 224 us for three quarters of the work of 16, which take 177.
     const bool steady = BR % G == 0 && a.q_head < (1 << 22) / G && a.q_tok < (1 << 30) / BR;
     // (They wait in the LDS: the accumulators leave no registers for them.)
 #pragma unroll
@@ -420,7 +422,7 @@ __global__ __launch_bounds__(256, 2) void attn_dkdv_kernel(AttnBwdArgs a) {
     // rows on the edge of the mask.  (Everything is computed and loaded anew
     // from an opaque lane number: what this path shared with the loop above
     // would cost that registers, and a spilled fragment there waits for every
-    // copy in flight.)
+    // copy in flight, as the copies of groups that do not divide a tile do.)
     if (wlive) {
         const float bad = not_finite(dk) + not_finite(dv);
         if (__any(bad != bad)) {

@@ -1,5 +1,5 @@
-// Shared by the attention kernels (attn_fwd.hip, attn_bwd.hip, attn_f32.hip):
-// argument structs, the work items of packed sequences, and the LDS tile
+// Shared by the attention kernels (attn_fwd.hip, attn_decode.hip,
+// attn_bwd.hip, attn_f32.hip): the work items of packed sequences, and the LDS tile
 // layout of the bf16 MFMA kernels.
 //
 // A row is one (token, query head) pair.  The G = heads / kv_heads query

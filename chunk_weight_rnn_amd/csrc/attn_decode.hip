@@ -20,8 +20,9 @@
 //
 // 64 tokens at contexts of 2K to 16K, 16 heads of 128 over 4: 189 us, 5.5 TB/s of
 // keys and values (a large copy moves 5.1, a read alone at most 6.3).  One token at
-// a context of 513: 13.9 us, of which the keys take 9, at the 28 bytes per ns that a
-// compute unit can take in; the rest is the launches and the way to the first key.
+// a context of 513 in one launch: 14.0 us, of which the keys take 9, at the 28 bytes
+// per ns that a compute unit can take in; the rest is the launch and the way to the
+// first key.
 #include "attn_common.h"
 
 namespace e2ttt {

@@ -22,8 +22,8 @@
 // in turn, and add their parts in the LDS; and in the backward the other axis of
 // an item is shared out over several workgroups where the items are few.
 //
-// Four heads of 64 over two key heads, rows of 2048 and 840 tokens: forward 43 us
-// (58 Tflop/s), dq 54 (68), dk and dv 70 (71), the join 5, of the 154 that a large
+// Four heads of 64 over two key heads, rows of 2048 and 840 tokens: forward 41 us
+// (61 Tflop/s), dq 53 (71), dk and dv 71 (71), the join 5, of the 154 that a large
 // library product reaches.  The products take half the time on their SIMDs; the
 // rest is each wave's way in and out (a wave has about ten tiles) and vector
 // instructions, which do not run beside the fp32 MFMA.  (Tiles staged in the LDS,

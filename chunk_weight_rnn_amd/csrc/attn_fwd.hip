@@ -14,9 +14,10 @@
 // stages deep; two workgroups share a compute unit, so that one's softmax
 // (VALU) runs beside the other's products.
 //
-// 16 heads of 128, a sequence of 16K under a window of 2K: 290 us, 890 Tflop/s of
-// the 1340 that a large library product reaches; 16 packed prompts of up to 2K over
-// 4 key heads, 101 us, 690.  The matrix pipe is busy 43 % of the time: what bounds
+// 16 heads of 128, a sequence of 16K under a window of 2K: 294 us a call, 877
+// Tflop/s of the 1340 that a large library product reaches; 16 packed prompts of up
+// to 2K over 4 key heads, 103 us, 673.  (Another card ran both a tenth slower.)  The
+// matrix pipe is busy 43 % of the time: what bounds
 // the kernel is the softmax's vector instructions (an exponential, a fused
 // multiply-add and half a pack per score), which run beside the products only in
 // part.  Tried and slower: products of one tile beside the softmax of the one

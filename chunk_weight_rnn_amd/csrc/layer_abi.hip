@@ -119,7 +119,7 @@ void plan(AttnArgs& a, bool f32, int64_t longest) {
     if (a.window > 0 && longest > seen) longest = seen;
     if (items > 0 && items < kCUs) {
         // 8 chunks of up to 256 tokens over a window of 2048, 208 tiles: 76 us
-        // whole, 56 in 2 ranges, 46 in 3, 52 in 4 (and 13 for the join); one
+        // whole, 56 in 2 ranges, 46 in 3, 52 in 4 (and 9 for the join); one
         // chunk at 16K, 32 tiles: 67 us in 8, 51 in 16, 65 in 20
         int64_t n = (2 * kCUs + items - 1) / items;
         const int64_t most = (longest + 255) / 256;
@@ -130,9 +130,11 @@ void plan(AttnArgs& a, bool f32, int64_t longest) {
 
 // A paged call of few rows per sequence on average goes to the decoding kernel
 // (bf16), which needs one launch where no context can be longer than
-// kOneLaunch keys, and two where the keys are shared out (one token, 16 heads of
-// 128 over 4: at a context of 500 keys 12.5 us in one and 13.4 in two, at 1000
-// 19.5 and 13.2; 16 sequences at 1000 19.8 and 16.1).
+// kOneLaunch keys, and two where the keys are shared out.  Where the two cross
+// depends on how many sequences there are (one token each, 16 heads of 128 over 4,
+// us in one launch and in two): one sequence at 512 keys 12.7 and 12.8, at 640 14.7
+// and 12.9, at 1000 19.6 and 12.3; 16 sequences at 640 14.7 and 18.5, at 700 16.5
+// and 15.1, at 1000 19.7 and 16.4; 64 at 640 19.0 and 23.0, at 1000 25.2 and 29.1.
 constexpr int64_t kOneLaunch = 640;
 void plan_paged(AttnArgs& a, bool f32, int64_t longest) {
     const int64_t units = (longest + a.N + 127) / 128, tiles = a.N * a.G / 32 + a.S;
