@@ -136,3 +136,15 @@ def test_heads_far_apart(far, H, K, dtype):
     assert all(torch.equal(a, b) for a, b in zip(*got))
     m = _paged(TYPES[dtype], [1, 100], H, K, 64, 16, [700, 90])
     assert torch.equal(e2.paged_attention(*m), e2.paged_attention(*(spread(t) for t in m[:3]), *m[3:]))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_paged_call_of_no_sequences(dtype):
+    import chunk_weight_rnn_amd as e2
+    note(f"paged, no sequences, {dtype}")
+    q, k, v, kc, vc, *_ = _paged(TYPES[dtype], [5], 4, 2, 64, 16, [3])
+    none = lambda *s: torch.zeros(*s, dtype=torch.int32, device="cuda")
+    before = kc.clone(), vc.clone()
+    out = torch.full_like(q, float("nan"))
+    assert e2.paged_attention(q, k, v, kc, vc, none(0, 4), none(1), none(0), out=out) is out
+    assert bool((out == 0).all()) and torch.equal(kc, before[0]) and torch.equal(vc, before[1])
