@@ -18,9 +18,14 @@ vector-Jacobian product of ``chunk_forward`` (SwiGLU MFMA path).
 The other operators of a hybrid layer (``layer.py``, include/e2ttt_layer.h):
 causal grouped-head attention over packed sequences with an optional window
 (``attention_forward``, ``attention_backward``, ``attention``), attention of
-new tokens over a paged cache (``paged_attention``) and the root-mean-square
-norm with the residual's addition (``norm_forward``, ``norm_backward``,
-``rms_norm``).
+new tokens over a paged cache in the queries' type or in 8 bits
+(``paged_attention``), the gated linear recurrence (``gated_scan_forward``,
+``gated_scan_backward``, ``gated_scan``) and the root-mean-square norm with the
+residual's addition (``norm_forward``, ``norm_backward``, ``rms_norm``).
+
+A model's two ends (``tokens.py``, include/e2ttt_tokens.h): the lookup of
+tokens' vectors (``embedding_forward``, ``embedding_backward``, ``embedding``)
+and the choice of the next token (``sample``).
 """
 from __future__ import annotations
 
@@ -32,11 +37,13 @@ from . import _lib
 from ._lib import (E2TTTError, FLAG_CHUNK_AVG, FLAG_FORCE_GENERIC, FLAG_NO_MOMENTUM, FLAG_PRECISE, FLAG_SAVE_STATES,
                    make_desc)
 
-from .layer import (attention, attention_backward, attention_forward, norm_backward, norm_forward, paged_attention,
-                    rms_norm)
+from .layer import (attention, attention_backward, attention_forward, gated_scan, gated_scan_backward,
+                    gated_scan_forward, norm_backward, norm_forward, paged_attention, rms_norm)
+from .tokens import embedding, embedding_backward, embedding_forward, sample
 
 __all__ = ["attention", "attention_forward", "attention_backward", "paged_attention", "rms_norm", "norm_forward",
-           "norm_backward", "chunk_forward", "chunk_forward_noalloc", "chunk_backward", "chunk_update",
+           "norm_backward", "gated_scan", "gated_scan_forward", "gated_scan_backward", "embedding", "embedding_forward",
+           "embedding_backward", "sample", "chunk_forward", "chunk_forward_noalloc", "chunk_backward", "chunk_update",
            "training_workspace", "logscan", "workspace_size", "param_count", "path", "validate", "E2TTTError",
            "library"]
 

@@ -29,7 +29,14 @@ EXPORTS = ("e2ttt_param_count", "e2ttt_workspace_size", "e2ttt_path", "e2ttt_val
 # include/e2ttt_layer.h
 LAYER_EXPORTS = ("e2ttt_attention_workspace_size", "e2ttt_attention_forward", "e2ttt_attention_backward_workspace_size",
                  "e2ttt_attention_backward", "e2ttt_paged_workspace_size", "e2ttt_paged_attention",
+                 "e2ttt_paged8_workspace_size", "e2ttt_paged8_attention", "e2ttt_scan_workspace_size", "e2ttt_scan_forward",
+                 "e2ttt_scan_backward_workspace_size", "e2ttt_scan_backward",
                  "e2ttt_norm_forward", "e2ttt_norm_backward_workspace_size", "e2ttt_norm_backward")
+
+# include/e2ttt_tokens.h
+TOKENS_EXPORTS = ("e2ttt_embedding_forward", "e2ttt_embedding_backward_workspace_size", "e2ttt_embedding_backward",
+                  "e2ttt_sample_workspace_size", "e2ttt_sample")
+SCAN_TILE = 128  # E2TTT_SCAN_TILE
 
 
 class Desc(ctypes.Structure):
@@ -57,6 +64,22 @@ class PagedDesc(ctypes.Structure):
 class NormDesc(ctypes.Structure):
     _fields_ = [("io_dtype", ctypes.c_int32), ("bits8", ctypes.c_int32), ("rows", ctypes.c_int64),
                 ("width", ctypes.c_int64), ("eps", ctypes.c_float), ("reserved", ctypes.c_int32)]
+
+
+class ScanDesc(ctypes.Structure):
+    _fields_ = [("io_dtype", ctypes.c_int32), ("gate_dtype", ctypes.c_int32), ("tokens", ctypes.c_int64),
+                ("seqs", ctypes.c_int64), ("width", ctypes.c_int64), ("x_tok", ctypes.c_int64), ("a_tok", ctypes.c_int64)]
+
+
+class EmbeddingDesc(ctypes.Structure):
+    _fields_ = [("table_dtype", ctypes.c_int32), ("io_dtype", ctypes.c_int32), ("token_bytes", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("tokens", ctypes.c_int64), ("vocab", ctypes.c_int64), ("width", ctypes.c_int64)]
+
+
+class SampleDesc(ctypes.Structure):
+    _fields_ = [("io_dtype", ctypes.c_int32), ("top_k", ctypes.c_int32), ("temperature", ctypes.c_float),
+                ("top_p", ctypes.c_float), ("min_p", ctypes.c_float), ("reserved", ctypes.c_int32),
+                ("rows", ctypes.c_int64), ("vocab", ctypes.c_int64), ("row_stride", ctypes.c_int64)]
 
 
 class E2TTTError(RuntimeError):
@@ -103,12 +126,24 @@ def load() -> ctypes.CDLL:
     lib.e2ttt_chunk_backward_events.argtypes = [pd] + [vp] * 19 + [vp, sz, vp, ctypes.POINTER(vp)]
     lib.e2ttt_chunk_backward_events.restype = ctypes.c_int
     pa, pp, pn = ctypes.POINTER(AttentionDesc), ctypes.POINTER(PagedDesc), ctypes.POINTER(NormDesc)
+    ps, pe, pt = ctypes.POINTER(ScanDesc), ctypes.POINTER(EmbeddingDesc), ctypes.POINTER(SampleDesc)
     for fn, args, res in (("e2ttt_attention_workspace_size", [pa], sz),
                           ("e2ttt_attention_forward", [pa] + [vp] * 6 + [vp, sz, vp], ctypes.c_int),
                           ("e2ttt_attention_backward_workspace_size", [pa], sz),
                           ("e2ttt_attention_backward", [pa] + [vp] * 10 + [vp, sz, vp], ctypes.c_int),
                           ("e2ttt_paged_workspace_size", [pp], sz),
                           ("e2ttt_paged_attention", [pp] + [vp] * 9 + [vp, sz, vp], ctypes.c_int),
+                          ("e2ttt_paged8_workspace_size", [pp], sz),
+                          ("e2ttt_paged8_attention", [pp] + [vp] * 11 + [vp, sz, vp], ctypes.c_int),
+                          ("e2ttt_scan_workspace_size", [ps], sz),
+                          ("e2ttt_scan_forward", [ps] + [vp] * 7 + [vp, sz, vp], ctypes.c_int),
+                          ("e2ttt_scan_backward_workspace_size", [ps], sz),
+                          ("e2ttt_scan_backward", [ps] + [vp] * 9 + [vp, sz, vp], ctypes.c_int),
+                          ("e2ttt_embedding_forward", [pe] + [vp] * 3 + [vp], ctypes.c_int),
+                          ("e2ttt_embedding_backward_workspace_size", [pe], sz),
+                          ("e2ttt_embedding_backward", [pe] + [vp] * 3 + [vp, sz, vp], ctypes.c_int),
+                          ("e2ttt_sample_workspace_size", [pt], sz),
+                          ("e2ttt_sample", [pt] + [vp] * 8 + [vp, sz, vp], ctypes.c_int),
                           ("e2ttt_norm_forward", [pn] + [vp] * 7 + [vp], ctypes.c_int),
                           ("e2ttt_norm_backward_workspace_size", [pn], sz),
                           ("e2ttt_norm_backward", [pn] + [vp] * 7 + [vp, sz, vp], ctypes.c_int)):

@@ -23,7 +23,9 @@ LIB = os.path.join(PKG, "libe2ttt.so")
 PROBE_LIB = os.path.join(PKG, "libe2ttt_probe.so")  # microbenchmarks of the chip's ceilings (bench.py --peaks)
 PROBE_SOURCES = ["probe.hip"]
 SOURCES = ["abi.hip", "logscan.hip", "generic.hip", "generic_bwd.hip", "f32_mfma.hip", "swiglu_loop.hip",
-           "swiglu_mfma.hip", "swiglu_bwd.hip", "layer_abi.hip", "attn_fwd.hip", "attn_decode.hip", "attn_bwd.hip", "attn_f32.hip", "norm.hip"]
+           "swiglu_mfma.hip", "swiglu_bwd.hip", "layer_abi.hip", "attn_fwd.hip", "attn_decode.hip", "attn_bwd.hip",
+           "attn_f32.hip", "attn8_append.hip", "attn8_decode.hip", "attn8_fwd.hip", "norm.hip", "scan.hip",
+           "tokens_abi.hip", "embedding.hip", "sample.hip"]
 ARCH = "gfx950"
 
 

@@ -5,29 +5,13 @@
 
 #include <initializer_list>
 
+#include "abi_util.h"
 #include "layer_internal.h"
 
 namespace e2ttt {
 namespace {
 
-constexpr size_t kWsAlign = 256;
 constexpr int64_t kCUs = 256;  // compute units of the MI355X
-constexpr size_t kBad = (size_t)-1;
-
-struct Span {  // the bytes a tensor reaches; empty for a null or empty one
-    uintptr_t lo = 0, hi = 0;
-    bool meets(const Span& o) const { return lo < hi && o.lo < o.hi && lo < o.hi && o.lo < hi; }
-};
-
-Span span(const void* p, int64_t bytes) {
-    Span s;
-    if (p && bytes > 0) s = {(uintptr_t)p, (uintptr_t)p + (uintptr_t)bytes};
-    return s;
-}
-
-bool aligned(const void* p, size_t n) { return p && (uintptr_t)p % n == 0; }
-
-int64_t elem(int dtype) { return dtype == E2TTT_BF16 ? 2 : 4; }
 
 // Elements from the first to past the last of [n][h][D] with these strides.
 int64_t reach(int64_t n, int64_t h, int64_t D, int64_t tok, int64_t head) {
@@ -63,13 +47,14 @@ int attention_desc_status(const e2ttt_attention_desc* d, bool packed_kv) {
     return E2TTT_OK;
 }
 
-int paged_desc_status(const e2ttt_paged_desc* d, bool append) {
+// `es`: bytes of the cache's elements.
+int paged_desc_status(const e2ttt_paged_desc* d, bool append, int64_t es) {
     if (!d) return E2TTT_ERR_INVALID_ARG;
     const int st = attention_desc_status(&d->a, append);
     if (st != E2TTT_OK) return st;
     if (d->pages < 0 || d->table_width < 0 || d->page_size < 1 || (d->page_size & (d->page_size - 1)))
         return E2TTT_ERR_INVALID_ARG;
-    const int64_t es = elem(d->a.io_dtype), D = d->a.D;
+    const int64_t D = d->a.D;
     const int64_t s[6] = {d->kc_page, d->kc_head, d->kc_slot, d->vc_page, d->vc_head, d->vc_slot};
     const int64_t n[3] = {d->pages, d->a.kv_heads, d->page_size}, lim[3] = {1 << 30, (int64_t)1 << 40, 1 << 23};
     for (int i = 0; i < 6; ++i)  // slots that the call writes must not overlap
@@ -80,6 +65,16 @@ int paged_desc_status(const e2ttt_paged_desc* d, bool append) {
     if (d->table_width > 0x7fffffff || d->table_width * d->page_size + d->a.tokens + 256 > 0x7fffffff)
         return E2TTT_ERR_UNSUPPORTED;
     return E2TTT_OK;
+}
+
+int paged_desc_status(const e2ttt_paged_desc* d, bool append) {
+    return paged_desc_status(d, append, d ? elem(d->a.io_dtype) : 1);
+}
+
+int paged8_desc_status(const e2ttt_paged_desc* d, bool append) {
+    const int st = paged_desc_status(d, append, 1);
+    if (st != E2TTT_OK) return st;
+    return d->a.io_dtype != E2TTT_BF16 || d->a.D % 16 ? E2TTT_ERR_UNSUPPORTED : E2TTT_OK;
 }
 
 AttnArgs make_args(const e2ttt_attention_desc& d) {
@@ -165,22 +160,6 @@ void set_split(AttnArgs& a, void* ws) {
     a.pl = (float*)((char*)ws + (rows * a.D * 4 + kWsAlign - 1) / kWsAlign * kWsAlign);
 }
 
-int workspace_status(const void* ws, size_t have, size_t need) {
-    if (need == 0) return E2TTT_OK;
-    return !ws || have < need || (uintptr_t)ws % kWsAlign ? E2TTT_ERR_WORKSPACE : E2TTT_OK;
-}
-
-template <int NI, int NO>
-int alias_status(const Span (&in)[NI], const Span (&out)[NO]) {
-    for (int o = 0; o < NO; ++o) {
-        for (int i = 0; i < NI; ++i)
-            if (out[o].meets(in[i])) return E2TTT_ERR_ALIAS;
-        for (int p = 0; p < o; ++p)
-            if (out[o].meets(out[p])) return E2TTT_ERR_ALIAS;
-    }
-    return E2TTT_OK;
-}
-
 int launch_status(hipError_t e) {
     if (e == hipErrorInvalidConfiguration) return E2TTT_ERR_UNSUPPORTED;  // kMaxGroups
     return e == hipSuccess ? E2TTT_OK : E2TTT_ERR_HIP;
@@ -190,6 +169,27 @@ int run_forward(AttnArgs& a, bool f32, hipStream_t s) {
     if (a.decode) return launch_status(launch_attn_decode_bf16(a, s));
     hipError_t e = f32 ? launch_attn_fwd_f32(a, s) : launch_attn_fwd_bf16(a, s);
     if (e == hipSuccess && a.nsplit > 1) e = launch_attn_join(a, f32, s);  // split calls have few rows
+    return launch_status(e);
+}
+
+// All launches of a call, before the first of them: the cache is not extended by a
+// call that is refused.
+bool grids8_ok(const AttnArgs& a) {
+    const int64_t items = (int64_t)a.ntiles * a.K, append = (2 * a.N * a.K + kAppend8Rows - 1) / kAppend8Rows;
+    const int64_t attend = (a.decode ? (a.nsplit > 1 ? kDecodeGroups : items) : items * a.nsplit) + a.clear;
+    return items <= kMaxGroups && attend <= kMaxGroups && append <= kMaxGroups && (a.N * a.H + 7) / 8 <= kMaxGroups;
+}
+
+int run_forward8(AttnArgs& a, hipStream_t s) {
+    if (!grids8_ok(a)) return E2TTT_ERR_UNSUPPORTED;
+    if (a.pg.append) {
+        const hipError_t e = launch_append8(a, s);
+        if (e != hipSuccess) return launch_status(e);
+        a.pg.append = 0;
+    }
+    if (a.decode) return launch_status(launch_attn_decode8(a, s));
+    hipError_t e = launch_attn_fwd8(a, s);
+    if (e == hipSuccess && a.nsplit > 1) e = launch_attn_join(a, false, s);
     return launch_status(e);
 }
 
@@ -206,6 +206,78 @@ int norm_rows_aligned(const e2ttt_norm_desc* d, std::initializer_list<const void
 }
 
 bool norm_supported(const e2ttt_norm_desc* d) { return d->width <= 65536 && d->rows <= 0x7fffffff; }
+
+int scan_desc_status(const e2ttt_scan_desc* d) {
+    if (!d) return E2TTT_ERR_INVALID_ARG;
+    if (d->io_dtype != E2TTT_F32 && d->io_dtype != E2TTT_BF16) return E2TTT_ERR_INVALID_ARG;
+    if (d->gate_dtype != E2TTT_F32 && d->gate_dtype != d->io_dtype) return E2TTT_ERR_INVALID_ARG;
+    if (d->tokens < 0 || d->seqs < 0 || d->width < 1) return E2TTT_ERR_INVALID_ARG;
+    if (d->tokens > 1 && (d->x_tok < d->width || d->a_tok < d->width)) return E2TTT_ERR_INVALID_ARG;
+    // offsets within a sequence are 32-bit, and so is a tile past its end
+    if (d->tokens > 0x7fffffff - 4096 || d->seqs >= (1 << 28) || d->width > (1 << 24)) return E2TTT_ERR_UNSUPPORTED;
+    const int64_t lim = (int64_t)1 << 31;
+    if (d->tokens > 1 && (d->x_tok > lim || d->a_tok > lim)) return E2TTT_ERR_UNSUPPORTED;
+    return E2TTT_OK;
+}
+
+// Whether two neighbouring channels can be read and written together.
+bool scan_pairs(const e2ttt_scan_desc& d, std::initializer_list<const void*> io, std::initializer_list<const void*> gates) {
+    if (d.io_dtype != E2TTT_BF16 || d.width % 2) return false;
+    if (d.tokens > 1 && (d.x_tok % 2 || d.a_tok % 2)) return false;
+    for (const void* p : io)
+        if ((uintptr_t)p % 4) return false;
+    for (const void* p : gates)
+        if ((uintptr_t)p % (2 * elem(d.gate_dtype))) return false;
+    return true;
+}
+
+// Slabs, parts and workgroups.  `slab` channels are the most that a workgroup
+// can take; a call whose tensors are only aligned to their elements takes half.
+ScanArgs scan_plan(const e2ttt_scan_desc& d, bool pairs, bool backward) {
+    ScanArgs a{};
+    a.N = d.tokens;
+    a.C = d.width;
+    a.S = (int)d.seqs;
+    a.x_f32 = d.io_dtype == E2TTT_F32;
+    a.gate_f32 = d.gate_dtype == E2TTT_F32;
+    a.pairs = pairs;
+    a.x_tok = d.tokens > 1 ? d.x_tok : d.width;
+    a.a_tok = d.tokens > 1 ? d.a_tok : d.width;
+    const int64_t slab = pairs ? 128 : 64;
+    const int64_t slabs = (d.width + slab - 1) / slab;
+    a.slabs = (int)slabs;
+    int64_t groups = d.seqs * slabs;
+    if (!backward && d.tokens <= 16 * d.seqs) {
+        a.shorts = 1;
+    } else if (groups < kCUs && d.tokens > 2 * E2TTT_SCAN_TILE) {
+        int64_t part = d.tokens * slabs / (2 * kCUs);
+        part = (part + E2TTT_SCAN_TILE - 1) / E2TTT_SCAN_TILE * E2TTT_SCAN_TILE;
+        if (part < 2 * E2TTT_SCAN_TILE) part = 2 * E2TTT_SCAN_TILE;
+        if (part < d.tokens) {
+            a.part = (int)part;
+            groups = (d.tokens / part + d.seqs) * slabs;
+        }
+    }
+    a.groups = (int)(groups < kMaxScanGroups ? groups : kMaxScanGroups + 1);
+    const int64_t units = (d.tokens * d.width + 2047) / 2048;
+    a.clear = (int)(units < 64 ? units : 64);
+    return a;
+}
+
+size_t scan_sums_bytes(const ScanArgs& a) {
+    if (!a.part) return 0;
+    return (((size_t)(a.N / a.part + a.S) * 2 * a.C) * 4 + kWsAlign - 1) / kWsAlign * kWsAlign;
+}
+// Of the call, whichever way its tensors are aligned.
+size_t scan_bytes(const e2ttt_scan_desc& d, bool backward) {
+    size_t most = 0;
+    for (int pairs = 0; pairs < 2; ++pairs) {
+        const ScanArgs a = scan_plan(d, pairs != 0, backward);
+        const size_t n = a.part ? scan_sums_bytes(a) + (backward ? 0 : (size_t)a.S * a.C * 4) : 0;
+        if (n > most) most = n;
+    }
+    return most;
+}
 
 }  // namespace
 }  // namespace e2ttt
@@ -322,18 +394,22 @@ int e2ttt_attention_backward(const e2ttt_attention_desc* d, const void* q, const
     return launch_status(e);
 }
 
-size_t e2ttt_paged_workspace_size(const e2ttt_paged_desc* d) {
-    if (paged_desc_status(d, false) != E2TTT_OK) return kBad;
+static size_t paged_bytes(const e2ttt_paged_desc* d) {
     AttnArgs a = make_args(d->a);
     plan_paged(a, d->a.io_dtype == E2TTT_F32, d->table_width * d->page_size);
     return split_bytes(a);
 }
 
-int e2ttt_paged_attention(const e2ttt_paged_desc* d, const void* q, const void* k, const void* v, void* k_cache,
-                          void* v_cache, const int32_t* table, const int32_t* cu, const int32_t* cached, void* out,
-                          void* ws, size_t ws_bytes, void* stream) {
+size_t e2ttt_paged_workspace_size(const e2ttt_paged_desc* d) {
+    return paged_desc_status(d, false) == E2TTT_OK ? paged_bytes(d) : kBad;
+}
+
+// bits8: a cache of one-byte elements, with a scale per slot and head.
+static int paged_attention(const e2ttt_paged_desc* d, bool bits8, const void* q, const void* k, const void* v, void* k_cache,
+                           void* v_cache, void* k_scale, void* v_scale, const int32_t* table, const int32_t* cu,
+                           const int32_t* cached, void* out, void* ws, size_t ws_bytes, void* stream) {
     const bool append = k || v;
-    const int st = paged_desc_status(d, append);
+    const int st = bits8 ? paged8_desc_status(d, append) : paged_desc_status(d, append);
     if (st != E2TTT_OK) return st;
     const int64_t N = d->a.tokens, S = d->a.seqs, H = d->a.heads, K = d->a.kv_heads, D = d->a.D;
     if (N == 0 || S == 0) return E2TTT_OK;
@@ -344,12 +420,13 @@ int e2ttt_paged_attention(const e2ttt_paged_desc* d, const void* q, const void* 
     const bool f32 = d->a.io_dtype == E2TTT_F32;
     AttnArgs a = make_args(d->a);
     plan_paged(a, f32, d->table_width * d->page_size);
+    if (bits8 && d->pages > 0 && (!k_scale || !v_scale)) return E2TTT_ERR_INVALID_ARG;
     const size_t need = split_bytes(a);
     const int wst = workspace_status(ws, ws_bytes, need);
     if (wst != E2TTT_OK) return wst;
-    const int64_t es = elem(d->a.io_dtype), P = d->pages, ps = d->page_size;
-    const Span kc = span(k_cache, P > 0 ? es * ((P - 1) * d->kc_page + (K - 1) * d->kc_head + (ps - 1) * d->kc_slot + D) : 0);
-    const Span vc = span(v_cache, P > 0 ? es * ((P - 1) * d->vc_page + (K - 1) * d->vc_head + (ps - 1) * d->vc_slot + D) : 0);
+    const int64_t es = elem(d->a.io_dtype), cs = bits8 ? 1 : es, P = d->pages, ps = d->page_size;
+    const Span kc = span(k_cache, P > 0 ? cs * ((P - 1) * d->kc_page + (K - 1) * d->kc_head + (ps - 1) * d->kc_slot + D) : 0);
+    const Span vc = span(v_cache, P > 0 ? cs * ((P - 1) * d->vc_page + (K - 1) * d->vc_head + (ps - 1) * d->vc_slot + D) : 0);
     const Span in[6] = {span(q, es * reach(N, H, D, d->a.q_tok, d->a.q_head)),
                         append ? span(k, es * reach(N, K, D, d->a.k_tok, d->a.k_head)) : Span{},
                         append ? span(v, es * reach(N, K, D, d->a.v_tok, d->a.v_head)) : Span{},
@@ -357,13 +434,17 @@ int e2ttt_paged_attention(const e2ttt_paged_desc* d, const void* q, const void* 
     const Span outs[2] = {span(out, es * N * H * D), span(ws, (int64_t)need)};
     const int ast = alias_status(in, outs);
     if (ast != E2TTT_OK) return ast;
-    const Span caches[2] = {kc, vc};  // one tensor may hold both, interleaved
+    const Span scales[2] = {span(k_scale, bits8 ? P * K * ps : 0), span(v_scale, bits8 ? P * K * ps : 0)};
+    const Span caches[4] = {kc, vc, scales[0], scales[1]};  // one tensor may hold both, interleaved
     for (const Span& c : caches) {
         for (const Span& o : outs)
             if (c.meets(o)) return E2TTT_ERR_ALIAS;
         for (const Span& i : in)
             if (c.meets(i)) return E2TTT_ERR_ALIAS;
     }
+    if (scales[0].meets(scales[1])) return E2TTT_ERR_ALIAS;
+    for (const Span& s : scales)
+        if (s.meets(kc) || s.meets(vc)) return E2TTT_ERR_ALIAS;
     a.q = q;
     a.k = k;
     a.v = v;
@@ -386,8 +467,26 @@ int e2ttt_paged_attention(const e2ttt_paged_desc* d, const void* q, const void* 
     a.pg.pages = (int)P;
     a.pg.append = append;
     while ((int64_t)1 << a.pg.shift < ps) ++a.pg.shift;
+    a.pg.ks = (unsigned char*)(P > 0 ? k_scale : nullptr);
+    a.pg.vs = (unsigned char*)(P > 0 ? v_scale : nullptr);
     set_split(a, ws);
-    return run_forward(a, f32, (hipStream_t)stream);
+    return bits8 ? run_forward8(a, (hipStream_t)stream) : run_forward(a, f32, (hipStream_t)stream);
+}
+
+int e2ttt_paged_attention(const e2ttt_paged_desc* d, const void* q, const void* k, const void* v, void* k_cache,
+                          void* v_cache, const int32_t* table, const int32_t* cu, const int32_t* cached, void* out,
+                          void* ws, size_t ws_bytes, void* stream) {
+    return paged_attention(d, false, q, k, v, k_cache, v_cache, nullptr, nullptr, table, cu, cached, out, ws, ws_bytes, stream);
+}
+
+size_t e2ttt_paged8_workspace_size(const e2ttt_paged_desc* d) {
+    return paged8_desc_status(d, false) == E2TTT_OK ? paged_bytes(d) : kBad;
+}
+
+int e2ttt_paged8_attention(const e2ttt_paged_desc* d, const void* q, const void* k, const void* v, void* k_cache,
+                           void* v_cache, void* k_scale, void* v_scale, const int32_t* table, const int32_t* cu,
+                           const int32_t* cached, void* out, void* ws, size_t ws_bytes, void* stream) {
+    return paged_attention(d, true, q, k, v, k_cache, v_cache, k_scale, v_scale, table, cu, cached, out, ws, ws_bytes, stream);
 }
 
 int e2ttt_norm_forward(const e2ttt_norm_desc* d, const void* x, const void* residual, const float* weight, void* y,
@@ -441,6 +540,83 @@ int e2ttt_norm_backward(const e2ttt_norm_desc* d, const void* dy, const void* h,
     NormBwdArgs a{dy, h, dh, weight, rstd, dx, dweight, (float*)ws, d->rows, d->width, d->io_dtype == E2TTT_F32,
                   norm_rows_aligned(d, {dy, h, dh, weight, dx})};
     return launch_norm_backward(a, (hipStream_t)stream) == hipSuccess ? E2TTT_OK : E2TTT_ERR_HIP;
+}
+
+size_t e2ttt_scan_workspace_size(const e2ttt_scan_desc* d) {
+    return scan_desc_status(d) == E2TTT_OK ? scan_bytes(*d, false) : kBad;
+}
+
+int e2ttt_scan_forward(const e2ttt_scan_desc* d, const void* x, const void* a, const float* h0, const int32_t* cu,
+                       void* out, float* state, float* starts, void* ws, size_t ws_bytes, void* stream) {
+    const int st = scan_desc_status(d);
+    if (st != E2TTT_OK) return st;
+    if (d->seqs == 0) return E2TTT_OK;
+    const size_t es = elem(d->io_dtype), gs = elem(d->gate_dtype);
+    const int64_t N = d->tokens, S = d->seqs, C = d->width;
+    if (!aligned(cu, 4) || (h0 && !aligned(h0, 4)) || (state && !aligned(state, 4)) || (starts && !aligned(starts, 4)))
+        return E2TTT_ERR_INVALID_ARG;
+    if (N > 0 && (!aligned(x, es) || !aligned(a, gs) || !aligned(out, es))) return E2TTT_ERR_INVALID_ARG;
+    ScanArgs r = scan_plan(*d, scan_pairs(*d, {x, out}, {a}), false);
+    if (r.groups > kMaxScanGroups) return E2TTT_ERR_UNSUPPORTED;
+    const size_t need = scan_bytes(*d, false);
+    const int wst = workspace_status(ws, ws_bytes, need);
+    if (wst != E2TTT_OK) return wst;
+    const Span in[4] = {span(x, es * reach(N, 1, C, r.x_tok, 0)), span(a, gs * reach(N, 1, C, r.a_tok, 0)),
+                        h0 == state ? Span{} : span(h0, 4 * S * C), span(cu, 4 * (S + 1))};
+    const Span outs[4] = {span(out, es * N * C), span(state, 4 * S * C),
+                          span(starts, 4 * (N / E2TTT_SCAN_TILE + S) * C), span(ws, (int64_t)need)};
+    const int ast = alias_status(in, outs);
+    if (ast != E2TTT_OK) return ast;
+    r.x = x;
+    r.a = a;
+    r.h0 = h0;
+    r.cu = cu;
+    r.out = out;
+    r.state = state;
+    r.starts = starts;
+    r.sums = (float*)ws;
+    r.first = r.part && h0 ? (float*)((char*)ws + scan_sums_bytes(r)) : nullptr;
+    return launch_status(launch_scan_forward(r, (hipStream_t)stream));
+}
+
+size_t e2ttt_scan_backward_workspace_size(const e2ttt_scan_desc* d) {
+    return scan_desc_status(d) == E2TTT_OK ? scan_bytes(*d, true) : kBad;
+}
+
+int e2ttt_scan_backward(const e2ttt_scan_desc* d, const void* dout, const void* x, const void* a, const float* starts,
+                        const float* dstate, const int32_t* cu, void* dx, void* da, float* dh0, void* ws,
+                        size_t ws_bytes, void* stream) {
+    const int st = scan_desc_status(d);
+    if (st != E2TTT_OK) return st;
+    if (d->seqs == 0) return E2TTT_OK;
+    const size_t es = elem(d->io_dtype), gs = elem(d->gate_dtype);
+    const int64_t N = d->tokens, S = d->seqs, C = d->width;
+    if (!aligned(cu, 4) || !aligned(starts, 4) || (dstate && !aligned(dstate, 4)) || (dh0 && !aligned(dh0, 4)))
+        return E2TTT_ERR_INVALID_ARG;
+    if (N > 0 && (!aligned(x, es) || !aligned(a, gs) || !aligned(dout, es) || !aligned(dx, es) || !aligned(da, gs)))
+        return E2TTT_ERR_INVALID_ARG;
+    ScanArgs r = scan_plan(*d, scan_pairs(*d, {x, dout, dx}, {a, da}), true);
+    if (r.groups > kMaxScanGroups) return E2TTT_ERR_UNSUPPORTED;
+    const size_t need = scan_bytes(*d, true);
+    const int wst = workspace_status(ws, ws_bytes, need);
+    if (wst != E2TTT_OK) return wst;
+    const Span in[6] = {span(x, es * reach(N, 1, C, r.x_tok, 0)), span(a, gs * reach(N, 1, C, r.a_tok, 0)),
+                        span(dout, es * N * C), span(starts, 4 * (N / E2TTT_SCAN_TILE + S) * C),
+                        span(dstate, 4 * S * C), span(cu, 4 * (S + 1))};
+    const Span outs[4] = {span(dx, es * N * C), span(da, gs * N * C), span(dh0, 4 * S * C), span(ws, (int64_t)need)};
+    const int ast = alias_status(in, outs);
+    if (ast != E2TTT_OK) return ast;
+    r.x = x;
+    r.a = a;
+    r.h0 = dstate;
+    r.cu = cu;
+    r.out = dx;
+    r.da = da;
+    r.dout = dout;
+    r.state = dh0;
+    r.starts = const_cast<float*>(starts);
+    r.sums = (float*)ws;
+    return launch_status(launch_scan_backward(r, (hipStream_t)stream));
 }
 
 }  // extern "C"

@@ -25,6 +25,7 @@ struct PagedKV {
     const int* cached;  // [S] tokens in the cache before the call
     int wide, pages, shift;
     int append;  // keys at positions >= cached come from k / v, and go into the cache
+    unsigned char *ks, *vs;  // 8-bit cache: biased exponents of the scales, [pages][K][page size]
 };
 
 struct AttnArgs {
@@ -58,7 +59,13 @@ hipError_t launch_attn_fwd_f32(const AttnArgs& a, hipStream_t s);
 // many half as long 27.5; 64 at 12000 the same).
 constexpr int kDecodeGroups = 256;
 hipError_t launch_attn_decode_bf16(const AttnArgs& a, hipStream_t s);
+hipError_t launch_attn_decode_join(const AttnArgs& a, hipStream_t s);  // of D up to 128 and kDecodeGroups
 hipError_t launch_attn_join(const AttnArgs& a, bool f32, hipStream_t s);
+// The same over a cache in 8 bits; the new tokens go into it in a launch before.
+constexpr int kAppend8Rows = 16;  // rows of keys and values per workgroup
+hipError_t launch_append8(const AttnArgs& a, hipStream_t s);
+hipError_t launch_attn_decode8(const AttnArgs& a, hipStream_t s);
+hipError_t launch_attn_fwd8(const AttnArgs& a, hipStream_t s);
 
 struct AttnBwdArgs {
     const void *q, *k, *v, *out, *dout;
@@ -107,5 +114,31 @@ struct NormBwdArgs {
 };
 int norm_bwd_groups(int64_t rows);
 hipError_t launch_norm_backward(const NormBwdArgs& a, hipStream_t s);
+
+struct ScanArgs {
+    const void *x, *a;
+    const float* h0;  // [S][C] state before a sequence (forward) or gradient after it (backward), may be null
+    const int* cu;    // [S + 1]
+    void* out;        // [N][C]; backward: dx
+    float* state;     // [S][C] state after a sequence, or the gradient before it; may be null
+    float* starts;    // states before every E2TTT_SCAN_TILE tokens; forward: may be null
+    const void* dout;  // backward
+    void* da;
+    int64_t x_tok, a_tok;  // strides in elements
+    int64_t N, C;
+    int S;
+    int x_f32, gate_f32;
+    int pairs;    // bf16: two channels per lane
+    int slabs;    // of 64 lanes, over the channels
+    int groups;   // (sequence or part, slab) pairs
+    int part;     // 0: whole sequences; else tokens of a part, a multiple of E2TTT_SCAN_TILE
+    int shorts;   // forward: sequences of a few tokens
+    int clear;    // workgroups that write the rows of tokens outside every sequence
+    float* sums;  // [N / part + S][2][C] what a part does to a state
+    float* first;  // forward in parts, with h0: its copy
+};
+constexpr int64_t kMaxScanGroups = 1 << 22;  // of 512 threads
+hipError_t launch_scan_forward(const ScanArgs& a, hipStream_t s);
+hipError_t launch_scan_backward(const ScanArgs& a, hipStream_t s);
 
 }  // namespace e2ttt

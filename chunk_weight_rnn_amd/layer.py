@@ -18,11 +18,12 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import _lib
-from ._lib import AttentionDesc, E2TTTError, NormDesc, PagedDesc
+from ._lib import SCAN_TILE, AttentionDesc, E2TTTError, NormDesc, PagedDesc, ScanDesc
 
 _IO = {torch.float32: 0, torch.bfloat16: 1}
 _BAD = ctypes.c_size_t(-1).value
 F8 = torch.float8_e4m3fn
+E8 = torch.float8_e8m0fnu
 _functions: dict = {}
 
 
@@ -132,12 +133,13 @@ def _attention_plan(q, k, v, cu, window, scale):
 
 
 @lru_cache(maxsize=512)
-def _paged_plan(q, k, v, kc, vc, table, cu, window, scale):
+def _paged_plan(q, k, v, kc, vc, table, cu, window, scale, bits8):
     if len(kc[0]) != 4 or kc[0] != vc[0]:
         raise ValueError("k_cache and v_cache must share one shape (pages, K, page_size, D)")
     P, K, ps, D = kc[0]
-    if kc[2] != q[2] or vc[2] != q[2]:
-        raise TypeError(f"k_cache and v_cache must be {q[2]}")
+    want = F8 if bits8 else q[2]
+    if kc[2] != want or vc[2] != want:
+        raise TypeError(f"k_cache and v_cache must be {want}")
     a = _attention_desc(q, k, v, cu, window, scale, K)
     if a.D != D or (D > 1 and (kc[1][3] != 1 or vc[1][3] != 1)):
         raise ValueError(f"k_cache and v_cache must have a contiguous last dimension of {a.D}")
@@ -145,7 +147,7 @@ def _paged_plan(q, k, v, kc, vc, table, cu, window, scale):
         raise ValueError("table must have shape (sequences, width)")
     s, t = kc[1], vc[1]
     d = PagedDesc(a, P, ps, table[0][1], s[0], s[1], s[2], t[0], t[1], t[2])
-    return tuple(q[0]), ctypes.byref(d), _size("e2ttt_paged_workspace_size", d), d
+    return tuple(q[0]), ctypes.byref(d), _size("e2ttt_paged8_workspace_size" if bits8 else "e2ttt_paged_workspace_size", d), d
 
 
 @lru_cache(maxsize=512)
@@ -159,6 +161,27 @@ def _norm_plan(shape, dtype, eps, bits8):
         rows *= n
     d = NormDesc(_IO[dtype], int(bits8), rows, shape[-1], eps, 0)
     return tuple(shape[:-1]), ctypes.byref(d), _size("e2ttt_norm_backward_workspace_size", d), d
+
+
+@lru_cache(maxsize=512)
+def _scan_plan(x, a, cu):
+    shape, stride, dtype = x
+    if len(shape) != 2:
+        raise ValueError(f"x must have shape (tokens, width), got {tuple(shape)}")
+    if dtype not in _IO:
+        raise TypeError(f"expected float32 or bfloat16, got {dtype}")
+    if a[0] != shape:
+        raise ValueError(f"a must have shape {tuple(shape)}")
+    if a[2] != torch.float32 and a[2] != dtype:
+        raise TypeError(f"a must be float32 or {dtype}")
+    if shape[1] > 1 and (stride[1] != 1 or a[1][1] != 1):
+        raise ValueError("x's and a's last dimension must be contiguous")
+    if len(cu[0]) != 1 or cu[0][0] < 1 or cu[2] != torch.int32 or (cu[0][0] > 1 and cu[1][0] != 1):
+        raise ValueError("cu_seqlens must be a contiguous int32 tensor of shape (sequences + 1,)")
+    N, C = shape
+    d = ScanDesc(_IO[dtype], _IO[a[2]], N, cu[0][0] - 1, C, stride[0], a[1][0])
+    return (N, C, cu[0][0] - 1, ctypes.byref(d), _size("e2ttt_scan_workspace_size", d),
+            _size("e2ttt_scan_backward_workspace_size", d), d)
 
 
 def _row_values(lead, x):
@@ -261,7 +284,7 @@ def attention(q, k, v, cu_seqlens, *, window: int = 0, scale: float | None = Non
 
 
 def paged_attention(q, k, v, k_cache, v_cache, table, cu_seqlens, cached, *, window: int = 0,
-                    scale: float | None = None, out=None, workspace=None, stream=None):
+                    scale: float | None = None, k_scale=None, v_scale=None, out=None, workspace=None, stream=None):
     """Attention of each sequence's new tokens over its cached ones and
     themselves; writes the new keys and values into the cache; returns out.
 
@@ -274,17 +297,30 @@ def paged_attention(q, k, v, k_cache, v_cache, table, cu_seqlens, cached, *, win
     Tokens before the first offset or from the last on belong to no sequence:
     their out is 0, their k and v go nowhere.
     With k = v = None the cache holds the new tokens already.
+
+    With k_scale and v_scale, [pages, K, page_size] float8_e8m0fnu, contiguous, the
+    cache is in 8 bits (float8_e4m3fn, D a multiple of 16; q, k, v bfloat16): a key
+    or value is its row of the cache times its scale, a power of two.  New ones are
+    rounded into it, with the smallest scale that brings their largest magnitude to
+    448, and queries see them as the cache holds them; one with a NaN or an Inf in
+    it becomes NaN as a whole.
     """
     if stream is not None:
         with _on(stream, q):
             return paged_attention(q, k, v, k_cache, v_cache, table, cu_seqlens, cached, window=window, scale=scale,
-                                   out=out, workspace=workspace)
+                                   k_scale=k_scale, v_scale=v_scale, out=out, workspace=workspace)
     if (k is None) != (v is None):
         raise ValueError("k and v must both be given, or neither")
+    bits8 = k_scale is not None
+    if bits8 != (v_scale is not None):
+        raise ValueError("k_scale and v_scale must both be given, or neither")
     dev = _device(q, k=k, v=v, k_cache=k_cache, v_cache=v_cache, table=table, cu_seqlens=cu_seqlens, cached=cached,
-                  out=out)
+                  out=out, k_scale=k_scale, v_scale=v_scale)
     (N, H, D), desc, need, _ = _paged_plan(_layout(q), _layout(k), _layout(v), _layout(k_cache), _layout(v_cache),
-                                           _layout(table), _layout(cu_seqlens), window, scale)
+                                           _layout(table), _layout(cu_seqlens), window, scale, bits8)
+    if bits8:
+        _full("k_scale", k_scale, k_cache.shape[:3], E8)
+        _full("v_scale", v_scale, k_cache.shape[:3], E8)
     S = cu_seqlens.shape[0] - 1
     _int32("table", table, (S, table.shape[1]))
     _int32("cached", cached, (S,))
@@ -295,9 +331,98 @@ def paged_attention(q, k, v, k_cache, v_cache, table, cu_seqlens, cached, *, win
     if S == 0:  # no sequences, no launch
         return out.zero_()
     ws, n = _workspace(workspace, need, q)
+    if bits8:
+        _call("e2ttt_paged8_attention", dev, desc, q.data_ptr(), _p(k), _p(v), k_cache.data_ptr(), v_cache.data_ptr(),
+              k_scale.data_ptr(), v_scale.data_ptr(), table.data_ptr(), cu_seqlens.data_ptr(), cached.data_ptr(),
+              out.data_ptr(), ws, n)
+        return out
     _call("e2ttt_paged_attention", dev, desc, q.data_ptr(), _p(k), _p(v), k_cache.data_ptr(),
           v_cache.data_ptr(), table.data_ptr(), cu_seqlens.data_ptr(), cached.data_ptr(), out.data_ptr(), ws, n)
     return out
+
+
+def gated_scan_forward(x, a, cu_seqlens, *, h0=None, out=None, state=None, save: bool = False, workspace=None, stream=None):
+    """Gated linear recurrence h_t = a_t h_{t-1} + x_t of every channel over
+    packed sequences; returns (out, state, starts).
+
+    x: [N, C] float32 or bfloat16, a: [N, C] in x's type or float32, gates of
+    magnitude up to 1; last dimension contiguous (views of a projection's output
+    are fine).  cu_seqlens: [S + 1] int32, as for ``attention_forward``; tokens of
+    no sequence give 0.  h0: [S, C] float32, the state before each sequence (None:
+    0).  out: [N, C], every h_t in x's type; state: [S, C] float32, the last one of
+    each sequence (h0 for an empty one; ``state=h0`` updates it in place).  With
+    sequences of one token each this is the step of a serving loop.  ``save``
+    also gives starts, the states that ``gated_scan_backward`` begins from
+    (else None).
+    """
+    if stream is not None:
+        with _on(stream, x):
+            return gated_scan_forward(x, a, cu_seqlens, h0=h0, out=out, state=state, save=save, workspace=workspace)
+    dev = _device(x, a=a, cu_seqlens=cu_seqlens, h0=h0, out=out, state=state)
+    N, C, S, desc, need, _, _ = _scan_plan(_layout(x), _layout(a), _layout(cu_seqlens))
+    if h0 is not None:
+        _full("h0", h0, (S, C), torch.float32)
+    if out is None:
+        out = torch.empty(N, C, dtype=x.dtype, device=x.device)
+    else:
+        _full("out", out, (N, C), x.dtype)
+    if state is None:
+        state = torch.empty(S, C, dtype=torch.float32, device=x.device)
+    else:
+        _full("state", state, (S, C), torch.float32)
+    starts = torch.empty(N // SCAN_TILE + S, C, dtype=torch.float32, device=x.device) if save else None
+    if S == 0:  # no sequences, no launch
+        return out.zero_(), state, starts
+    ws, n = _workspace(workspace, need, x)
+    _call("e2ttt_scan_forward", dev, desc, x.data_ptr(), a.data_ptr(), _p(h0), cu_seqlens.data_ptr(), out.data_ptr(),
+          state.data_ptr(), _p(starts), ws, n)
+    return out, state, starts
+
+
+def gated_scan_backward(dout, x, a, starts, cu_seqlens, *, dstate=None, workspace=None, stream=None):
+    """Gradients of <dout, out> + <dstate, state> through ``gated_scan_forward``,
+    from its inputs and starts; returns a dict with keys x and a (contiguous, in
+    their types) and h0 ([S, C] float32)."""
+    if stream is not None:
+        with _on(stream, x):
+            return gated_scan_backward(dout, x, a, starts, cu_seqlens, dstate=dstate, workspace=workspace)
+    dev = _device(x, a=a, dout=dout, starts=starts, cu_seqlens=cu_seqlens, dstate=dstate)
+    N, C, S, desc, _, need, _ = _scan_plan(_layout(x), _layout(a), _layout(cu_seqlens))
+    _full("dout", dout, (N, C), x.dtype)
+    _full("starts", starts, (N // SCAN_TILE + S, C), torch.float32)
+    if dstate is not None:
+        _full("dstate", dstate, (S, C), torch.float32)
+    g = {"x": torch.empty(N, C, dtype=x.dtype, device=x.device), "a": torch.empty(N, C, dtype=a.dtype, device=x.device),
+         "h0": torch.empty(S, C, dtype=torch.float32, device=x.device)}
+    if S == 0:  # as in the forward
+        return {n: t.zero_() for n, t in g.items()}
+    ws, n = _workspace(workspace, need, x)
+    _call("e2ttt_scan_backward", dev, desc, dout.data_ptr(), x.data_ptr(), a.data_ptr(), starts.data_ptr(), _p(dstate),
+          cu_seqlens.data_ptr(), g["x"].data_ptr(), g["a"].data_ptr(), g["h0"].data_ptr(), ws, n)
+    return g
+
+
+class _GatedScan(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, a, h0, cu_seqlens):
+        out, state, starts = gated_scan_forward(x, a, cu_seqlens, h0=h0, save=True)
+        ctx.save_for_backward(x, a, starts, cu_seqlens)
+        ctx.set_materialize_grads(False)
+        return out, state
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dout, dstate):
+        x, a, starts, cu_seqlens = ctx.saved_tensors
+        dout = torch.zeros(x.shape, dtype=x.dtype, device=x.device) if dout is None else dout.contiguous()
+        g = gated_scan_backward(dout, x, a, starts, cu_seqlens, dstate=None if dstate is None else dstate.contiguous())
+        return g["x"], g["a"], (g["h0"] if ctx.needs_input_grad[2] else None), None
+
+
+def gated_scan(x, a, cu_seqlens, h0=None):
+    """``gated_scan_forward`` as a differentiable op: returns (out, state), with
+    gradients for x, a and h0 from ``gated_scan_backward``."""
+    return _GatedScan.apply(x, a, h0, cu_seqlens)
 
 
 def norm_forward(x, weight, *, residual=None, eps: float = 1e-6, bits8: bool = False, h=None, stream=None):

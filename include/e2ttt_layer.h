@@ -6,8 +6,10 @@
  * branch side by side in a layer ("Rethinking Expressivity and Efficiency in
  * Test-Time Training", atlas summary "Approach").  Here are the attention for
  * prompts and training (forward and backward over packed sequences), the
- * attention of new tokens over a paged cache for serving, and the norm with
- * the residual's addition that stands before both branches.
+ * attention of new tokens over a paged cache for serving (in the queries' type or
+ * in 8 bits), the gated linear recurrence, whose state is a vector where the
+ * chunk update's is a matrix, and the norm with the residual's addition that
+ * stands before the branches.
  *
  * Conventions, as in e2ttt.h: every tensor pointer is a DEVICE pointer owned
  * by the caller; the library never allocates, frees or synchronises; work is
@@ -116,6 +118,73 @@ E2TTT_API int e2ttt_paged_attention(const e2ttt_paged_desc* desc, const void* q,
                         void* k_cache, void* v_cache, const int32_t* table, const int32_t* cu_seqlens,
                         const int32_t* cached, void* out,
                         void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * The same over a cache in 8 bits: k_cache and v_cache hold OCP e4m3 values,
+ * and k_scale and v_scale [pages][kv_heads][page_size] contiguous a scale for
+ * every slot and key head, a power of two 2^(b - 127) as its biased exponent b
+ * (OCP e8m0; 255 is NaN).  A key or value that the call writes gets the smallest
+ * such scale with max|x| <= 448 scale (1 for zeros), and x / scale rounded to
+ * nearest even; one that holds a NaN or an Inf becomes NaN as a whole.  Queries
+ * see keys and values as the cache holds them, the new ones among them.
+ * io_dtype is bf16, in which an 8-bit value times its scale is exact, and D a
+ * multiple of 16 (else E2TTT_ERR_UNSUPPORTED).  The cache's strides count
+ * elements of one byte, in multiples of 16.  Everything else as above.
+ */
+E2TTT_API size_t e2ttt_paged8_workspace_size(const e2ttt_paged_desc* desc);
+E2TTT_API int e2ttt_paged8_attention(const e2ttt_paged_desc* desc, const void* q, const void* k, const void* v,
+                        void* k_cache, void* v_cache, void* k_scale, void* v_scale, const int32_t* table,
+                        const int32_t* cu_seqlens, const int32_t* cached, void* out,
+                        void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Gated linear recurrence of every channel over packed sequences:
+ *   h_t = a_t h_{t-1} + x_t,  out_t = h_t,
+ * from h0 of each sequence (0 where h0 is NULL) to its state after its last
+ * token (h0 where it has none).  Held in 32 bits; out is rounded once.
+ *   x           [tokens][width] io_dtype, x_tok elements from token to token
+ *   a           [tokens][width] gate_dtype, a_tok elements from token to token;
+ *               gates, of magnitude up to 1: products of them over stretches of
+ *               a sequence are formed, which larger ones could take past the range
+ *   h0, state   [seqs][width] fp32, or NULL; state may be h0 (in place)
+ *   cu_seqlens  [seqs + 1] int32, as for the attention; out is 0 for tokens of
+ *               no sequence
+ *   out         [tokens][width] io_dtype contiguous
+ *   starts      NULL, or, for the backward, [tokens / E2TTT_SCAN_TILE + seqs][width]
+ *               fp32: the state before token E2TTT_SCAN_TILE j of sequence s, in
+ *               row cu_seqlens[s] / E2TTT_SCAN_TILE + s + j; other rows are left alone
+ *   workspace   >= e2ttt_scan_workspace_size(desc) bytes, 256-byte aligned;
+ *               clobbered (NULL when that is 0)
+ * Tensors are aligned to their elements; where width and strides are even and
+ * pairs of channels aligned to their size, they are read in pairs.  Outputs must
+ * not overlap any other buffer.
+ */
+#define E2TTT_SCAN_TILE 128
+typedef struct {
+    int32_t io_dtype;
+    int32_t gate_dtype; /* of a: fp32, or io_dtype */
+    int64_t tokens, seqs, width;
+    int64_t x_tok, a_tok; /* at least width, up to 2^31 */
+} e2ttt_scan_desc;
+
+E2TTT_API size_t e2ttt_scan_workspace_size(const e2ttt_scan_desc* desc);
+E2TTT_API int e2ttt_scan_forward(const e2ttt_scan_desc* desc, const void* x, const void* a, const float* h0,
+                        const int32_t* cu_seqlens, void* out, float* state, float* starts,
+                        void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Gradients of <dout, out> + <dstate, state>, from the forward's inputs and
+ * starts:
+ *   g_t = dout_t + a_{t+1} g_{t+1}  (+ dstate after the last token),
+ *   dx_t = g_t,  da_t = g_t h_{t-1},  dh0 = a_1 g_1  (dstate for no token).
+ * dout, dx [tokens][width] io_dtype and da [tokens][width] gate_dtype
+ * contiguous; dstate (or NULL: 0) and dh0 (or NULL) [seqs][width] fp32.  dx and
+ * da are 0 for tokens of no sequence.  Outputs must not overlap any other buffer.
+ */
+E2TTT_API size_t e2ttt_scan_backward_workspace_size(const e2ttt_scan_desc* desc);
+E2TTT_API int e2ttt_scan_backward(const e2ttt_scan_desc* desc, const void* dout, const void* x, const void* a,
+                        const float* starts, const float* dstate, const int32_t* cu_seqlens, void* dx, void* da,
+                        float* dh0, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * Root-mean-square norm with the residual's addition:
