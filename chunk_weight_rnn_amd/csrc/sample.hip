@@ -2,19 +2,36 @@
 // from a given random number of the row (the definition is in
 // include/e2ttt_tokens.h).
 //
-// A workgroup holds a row in the LDS (rows of more than 128 KiB are read again for
-// each pass, from the cache).  Nothing is sorted: a filter keeps a
-// stretch of the order by falling logit, so what it needs is the logit at which
-// the running count or weight reaches a target, found with a histogram in the
-// LDS over ever smaller ranges: first 2048 bins evenly over the logits that have
-// weight, then 2048 over the bit patterns of the bin's logits, until one value
-// is left.  Equal logits at the border are kept by index.
+// A workgroup per row.  Nothing is sorted: a filter keeps a stretch of the order by
+// falling logit, so what it needs is the logit at which the running count or
+// weight reaches a target.  Equal logits at that border are kept by index.
+//
+// The row is read once for the maximum of every tile (512 values of a wave) and,
+// as the settings ask for them, the tiles' weights relative to their own maxima and
+// the counts of the logits in bins of 1/kFine of a temperature, 16 of them deep, that
+// move along with the largest logit so far.  Then
+//  * without a filter the tile that holds the token follows from the tiles' weights,
+//    and it alone is read again;
+//  * else the bins' counts say within which bins the border lies: exactly for a
+//    count, and for a weight within the e^(1/kFine) that logits of a bin differ by.
+//    A second pass, over the tiles whose maximum is that large, sums the weights
+//    above those bins tile by tile and gathers the logits in them, some hundred at
+//    most times, in a list (or all logits down to them, if they are few).  The border
+//    is found in the list, the list's weights go to their tiles, and one tile is read
+//    again.
+// Rows whose border lies deeper than the bins reach, or where more than kList logits
+// share its bins (equal ones, say), go the slow way: histograms of the whole row.
 //
 // Weights are whole multiples of 2^-44 of the largest, so that sums of up to 2^18
 // of them are exact in 64 bits: any order of summation gives the same, and the
-// border cases of the definition (a target met exactly) come out as written.
-// The exponential is computed in 64 bits, to 2^-47 of its value: a table of 64
-// powers of two and a polynomial of degree 5.
+// border cases of the definition (a target met exactly) come out as written.  The
+// tiles' weights of the first pass, taken before the maximum is known, are 64-bit
+// floats added in one order: exact for equal logits, and else to 2^-45 of the largest
+// per logit, as the rounding is that they leave out.
+//
+// What bounds it: a compute unit reads its row once at its share of the bandwidth,
+// and the exponentials, where they are needed of every logit, are some 25
+// instructions in 64 bits each.
 #include "tokens_internal.h"
 
 namespace e2ttt {
@@ -25,127 +42,203 @@ typedef unsigned long long u64;
 
 constexpr int kThreads = 1024, kWaves = kThreads / 64;
 constexpr int kBins = 2 * kThreads;
-constexpr int kOne = 44;        // a weight of one is 2^44
-constexpr int kTiles = 1024;    // pieces of a row that a wave holds side by side, at most
+constexpr int kOne = 44;         // a weight of one is 2^44
+constexpr int E = 8;             // values of a thread in a step of the row
+constexpr int kTile = 64 * E;
+constexpr int kStep = kTile * kWaves;
+constexpr int kTiles = (E2TTT_SAMPLE_VOCAB + 8 + kStep - 1) / kStep * kWaves;
+constexpr int kList = 8192;      // logits that are gathered, at most
+constexpr int kFine = 128;       // bins of a temperature
+constexpr int kWhole = 15 * kFine - 2;  // bins below the newest that lack nothing
+constexpr int kTable = 1024;
+static_assert(kTiles <= kThreads && kTable == kThreads, "a thread per tile, and per entry");
 
 __device__ __forceinline__ float neg_inf() { return -__builtin_inff(); }
 
-// A logit as it is used: NaN is never chosen, and zeros are equal.
-__device__ __forceinline__ unsigned clean(unsigned u, __bf16) {  // two of them
-    unsigned r = 0;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        unsigned x = (u >> (16 * h)) & 0xffffu;
-        if ((x & 0x7fffu) > 0x7f80u) x = 0xff80u;
-        if (x == 0x8000u) x = 0;
-        r |= x << (16 * h);
+// --------------------------------------------------------- over a wave's lanes
+// x of the lane that `CTRL` names, `none` where there is none.
+template <int CTRL, int ROWS, typename X>
+__device__ __forceinline__ X from_lane(X x, X none) {
+    if constexpr (sizeof(X) == 4) {
+        const int r = __builtin_amdgcn_update_dpp(__builtin_bit_cast(int, none), __builtin_bit_cast(int, x), CTRL, ROWS, 0xf, false);
+        return __builtin_bit_cast(X, r);
+    } else {
+        const u64 n = __builtin_bit_cast(u64, none), v = __builtin_bit_cast(u64, x);
+        const unsigned lo = __builtin_amdgcn_update_dpp((int)n, (int)v, CTRL, ROWS, 0xf, false);
+        const unsigned hi = __builtin_amdgcn_update_dpp((int)(n >> 32), (int)(v >> 32), CTRL, ROWS, 0xf, false);
+        return __builtin_bit_cast(X, (u64)hi << 32 | lo);
     }
-    return r;
 }
-__device__ __forceinline__ unsigned clean(unsigned u, float) {
-    if ((u & 0x7fffffffu) > 0x7f800000u) u = 0xff800000u;
-    return u == 0x80000000u ? 0u : u;
+// op over the lanes up to this one.
+template <typename X, class F>
+__device__ __forceinline__ X wave_scan(X x, X none, F&& op) {
+    x = op(x, from_lane<0x111, 0xf>(x, none));  // row_shr:1, 2, 4, 8 within 16 lanes
+    x = op(x, from_lane<0x112, 0xf>(x, none));
+    x = op(x, from_lane<0x114, 0xf>(x, none));
+    x = op(x, from_lane<0x118, 0xf>(x, none));
+    x = op(x, from_lane<0x142, 0xa>(x, none));  // row_bcast:15, row_bcast:31
+    x = op(x, from_lane<0x143, 0xc>(x, none));
+    return x;
 }
-// Order of the values as whole numbers.
+template <typename X>
+__device__ __forceinline__ X wave_inclusive(X x) {
+    return wave_scan(x, X{}, [](X a, X b) { return a + b; });
+}
+template <typename X>
+__device__ __forceinline__ X last_lane(X x) {
+    if constexpr (sizeof(X) == 4) {
+        return __builtin_bit_cast(X, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), 63));
+    } else {
+        const u64 v = __builtin_bit_cast(u64, x);
+        const unsigned lo = __builtin_amdgcn_readlane((int)v, 63), hi = __builtin_amdgcn_readlane((int)(v >> 32), 63);
+        return __builtin_bit_cast(X, (u64)hi << 32 | lo);
+    }
+}
+__device__ __forceinline__ float wave_max(float x) {
+    return last_lane(wave_scan(x, neg_inf(), [](float a, float b) { return fmaxf(a, b); }));
+}
+__device__ __forceinline__ int lanes_below(u64 m) {
+    return __builtin_amdgcn_mbcnt_hi((unsigned)(m >> 32), __builtin_amdgcn_mbcnt_lo((unsigned)m, 0));
+}
+
+// Sum of x over the threads before this one, and over all of them, in one order.
+template <typename X>
+__device__ __forceinline__ X block_exclusive(X x, X* wave_sums, X* total) {
+    const int wave = threadIdx.x >> 6;
+    const X incl = wave_inclusive(x);
+    __syncthreads();
+    if ((threadIdx.x & 63) == 63) wave_sums[wave] = incl;
+    __syncthreads();
+    X before = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+        if (w == wave) before = all;
+        all += wave_sums[w];
+    }
+    *total = all;
+    return before + (incl - x);
+}
+
+// -------------------------------------------------------------------- logits
+// Order of the values as whole numbers (never of a NaN); zeros of either sign are equal.
 __device__ __forceinline__ unsigned key_of(float x) {
-    const unsigned u = __builtin_bit_cast(unsigned, x);
+    const float y = x + 0.f;
+    const unsigned u = __builtin_bit_cast(unsigned, y);
     return u ^ ((unsigned)((int)u >> 31) | 0x80000000u);
 }
-
-template <typename T>
-__device__ __forceinline__ void values(u32x4 u, float (&x)[16 / sizeof(T)]) {
-    if constexpr (sizeof(T) == 2) {
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-            x[2 * w] = __builtin_bit_cast(float, u[w] << 16);
-            x[2 * w + 1] = __builtin_bit_cast(float, u[w] & 0xffff0000u);
-        }
-    } else {
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-            const unsigned one = u[w];
-            x[w] = __builtin_bit_cast(float, one);
-        }
-    }
+__device__ __forceinline__ float value_of(unsigned key) {
+    return __builtin_bit_cast(float, key & 0x80000000u ? key ^ 0x80000000u : ~key);
 }
 
-// A row in units of 16 bytes, E values, from the last address on at or before its
-// first value that 16 divides: unit j kThreads + thread is this thread's j-th.
-// NU > 0: up to NU of them in the LDS, where each thread reads what it wrote
-// itself; 0: in memory.  Places before and past the row hold -infinity.
-template <typename T, int NU>
+// A row, from the last address on at or before its first value that 16 divides:
+// step j of thread t holds E values from place (j kThreads + t) E on.  Places before
+// and past the row hold -infinity.  A NaN stays one, and no comparison takes it.
+template <typename T>
 struct Row {
-    static constexpr int E = 16 / sizeof(T);
+    static constexpr int U = E * sizeof(T) / 16;
+    struct Raw {
+        u32x4 u[U];
+    };
     const T* p;  // aligned
     int off, V;  // places before the row, values in it
     int steps;
-    u32x4* lds;
-    __device__ __forceinline__ Row(const T* row, int V_, u32x4* lds_) : V(V_), lds(lds_) {
+    const float* tops;  // largest value of every tile
+    __device__ __forceinline__ Row(const T* row, int V_, const float* tops_) : V(V_), tops(tops_) {
         off = (int)((uintptr_t)row % 16 / sizeof(T));
         p = row - off;
-        steps = (V + off + E * kThreads - 1) / (E * kThreads);
+        steps = (V + off + kStep - 1) / kStep;
     }
-    // Index of value e of this thread's unit of step j.
+    // Index of value e of this thread's step j.
     __device__ __forceinline__ int index(int j, int e) const { return (j * kThreads + (int)threadIdx.x) * E + e - off; }
-    __device__ __forceinline__ u32x4 load(int j) const {
+    __device__ __forceinline__ Raw load(int j) const {
         const int first = index(j, 0);
-        u32x4 u;
+        Raw r;
         if (first >= 0 && first + E <= V) {
-            u = *(const u32x4*)(p + off + first);
+#pragma unroll
+            for (int k = 0; k < U; ++k) r.u[k] = *(const u32x4*)(p + off + first + k * (E / U));
         } else {
             T t[E];
 #pragma unroll
             for (int e = 0; e < E; ++e) t[e] = first + e >= 0 && first + e < V ? p[off + first + e] : (T)neg_inf();
-            __builtin_memcpy(&u, t, 16);
+            __builtin_memcpy(&r, t, sizeof r);
         }
-#pragma unroll
-        for (int w = 0; w < 4; ++w) u[w] = clean(u[w], T{});
-        return u;
+        return r;
     }
-    // f(j, values) for every step j, all threads together; `fresh`: from memory,
-    // into the LDS.
-    template <bool FRESH = false, class F>
-    __device__ __forceinline__ void each(F&& f) const {
-        float x[E];
-        if constexpr (NU > 0 && !FRESH) {
-#pragma unroll 1
-            for (int j = 0; j < steps; ++j) {
-                values<T>(lds[j * kThreads + threadIdx.x], x);
-                f(j, x);
+    static __device__ __forceinline__ void values(const Raw& r, float (&x)[E]) {
+#pragma unroll
+        for (int k = 0; k < U; ++k)
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                const unsigned u = r.u[k][w];
+                if constexpr (sizeof(T) == 2) {
+                    x[2 * w] = __builtin_bit_cast(float, u << 16);
+                    x[2 * w + 1] = __builtin_bit_cast(float, u & 0xffff0000u);
+                } else {
+                    x[4 * k + w] = __builtin_bit_cast(float, u);
+                }
             }
-        } else {
-            u32x4 next = load(0);
+    }
+    // f(j, values) for the steps of this wave whose tile's largest value is wanted, the
+    // next one's loads in flight.
+    template <class P, class F>
+    __device__ __forceinline__ void each(P&& wanted, F&& f) const {
+        const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        auto next = [&](int j) {
+            while (j < steps && !wanted(tops[j * kWaves + wave])) ++j;
+            return __builtin_amdgcn_readfirstlane(j);
+        };
+        int j = next(0);
+        if (j >= steps) return;
+        Raw raw = load(j);
 #pragma unroll 1
-            for (int j = 0; j < steps; ++j) {
-                const u32x4 u = next;
-                if (j + 1 < steps) next = load(j + 1);
-                if constexpr (NU > 0) lds[j * kThreads + threadIdx.x] = u;
-                values<T>(u, x);
-                f(j, x);
-            }
+        while (j < steps) {
+            const int jn = next(j + 1);
+            Raw more = raw;
+            if (jn < steps) more = load(jn);
+            float x[E];
+            values(raw, x);
+            f(j, x);
+            j = jn;
+            raw = more;
         }
     }
 };
 
-// Weights: scaled(x) = 2^44 exp((x - max) / T) in 64 bits, fixed(x) rounded to a
-// whole number.
+// A few logits and their indices in the LDS.
+struct List {
+    const unsigned* keys;
+    const int* at;
+    int n;
+    template <class P, class F>
+    __device__ __forceinline__ void each(P&&, F&& f) const {
+#pragma unroll 1
+        for (int i0 = 0; i0 < n; i0 += kThreads) {
+            const int i = i0 + (int)threadIdx.x;
+            const float x[1] = {i < n ? value_of(keys[i]) : __builtin_nanf("")};
+            f(i, x);
+        }
+    }
+};
+
+// Weights of finite logits and -infinity: scaled(x) = 2^44 exp((x - top) / T) in 64
+// bits, to 2^-47 of its value, and fixed(x) rounded to a whole number.  The exponent
+// in 1024ths of a power of two: its whole part picks a power from the table, and the
+// rest goes through a polynomial of degree 3.  Exactly 2^44 for x = top.
 struct Weight {
-    double c, max;  // c = 64 log2(e) / T
-    float top;
-    const double* table;  // 2^(i / 64)
+    double c, top;        // c = 1024 log2(e) / T
+    const double* table;  // 2^(i / 1024)
+    __device__ __forceinline__ Weight(float T, float top_, const double* table_)
+        : c(kTable * 1.4426950408889634074 / (double)T), top((double)top_), table(table_) {}
     __device__ __forceinline__ double scaled(float x) const {
-        double t = ((double)x - max) * c;
-        t = fmax(t, -64.0 * 47);  // -infinity, and NaN of infinities, to a weight that rounds to 0
-        const double k = rint(t), r = (t - k) * (0.69314718055994530942 / 64);
-        double q = 1.0 / 120;
-        q = fma(q, r, 1.0 / 24);
-        q = fma(q, r, 1.0 / 6);
-        q = fma(q, r, 0.5);
-        q = fma(q, r, 1.0);
-        q = fma(q, r, 1.0);
-        const int i = (int)k;
-        const double w = ldexp(table[i & 63] * q, (i >> 6) + kOne);
-        return x == top ? (double)((u64)1 << kOne) : w;
+        constexpr double magic = 6755399441055744.0;  // 1.5 2^52: what is added to it is rounded to a whole number
+        constexpr double a1 = 0.69314718055994530942 / kTable, a2 = a1 * a1 / 2, a3 = a1 * a1 * a1 / 6;
+        double t = ((double)x - top) * c;
+        t = fmax(t, -1000.0 * kTable);  // also of NaN: nothing
+        const double y = t + magic, r = t - (y - magic);
+        const int k = (int)(unsigned)__builtin_bit_cast(u64, y);
+        const double q = fma(fma(fma(a3, r, a2), r, a1), r, 1.0);
+        const u64 w = __builtin_bit_cast(u64, table[k & (kTable - 1)] * q);
+        return __builtin_bit_cast(double, w + ((u64)(unsigned)(((k >> 10) + kOne) << 20) << 32));
     }
     static __device__ __forceinline__ u64 round(double w) {  // to nearest even, below 2^52
         return __builtin_bit_cast(u64, w + 4503599627370496.0) & (((u64)1 << 52) - 1);
@@ -170,46 +263,53 @@ __device__ __forceinline__ u64 part_of(float x, u64 n, bool* whole) {
     *whole = m == 0 || n == 0;
     return 0;
 }
+__device__ __forceinline__ u64 part_up(float x, u64 n) {  // rounded up, at least 1
+    bool whole;
+    const u64 r = part_of(x, n, &whole);
+    return r + (!whole || r == 0);
+}
 
 struct Shared {
     u64 hist[kBins];
-    double table[64];
-    u64 sum[kTiles];     // weight of what is kept without question, of each tile
-    int ties[kTiles];    // logits at the border
+    double table[kTable];
+    unsigned keys[kList];
+    int at[kList];
+    float tops[kTiles];   // largest value of each tile
+    u64 sum[kTiles];      // its weight (a double), then that of what is kept of it
+    int ties[kTiles];     // slow way: its logits at the border
+    float wtop[2][kWaves];
+    float wave_f[kWaves];
+    double wave_d[kWaves];
     u64 wave[kWaves];
-    u64 picked[2];       // measure before the picked bin, and in it
+    u64 picked[2];        // measure before the picked bin, and in it
     unsigned bin, lo, hi;
-    int index;
+    int index, last;
 };
 
-template <typename X>
-__device__ __forceinline__ X wave_inclusive(X x) {
-    const int lane = threadIdx.x & 63;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const X y = __shfl_up(x, d);
-        if (lane >= d) x += y;
-    }
-    return x;
-}
+struct Settings {
+    float T, top_p, min_p, u;
+    int top_k;
+    bool by_k, by_p;
+};
 
-// Sum of x over the threads before this one, and over all of them.
-__device__ __forceinline__ u64 block_exclusive(u64 x, u64* wave_sums, u64* total) {
-    const int wave = threadIdx.x >> 6;
-    const u64 incl = wave_inclusive(x);
-    __syncthreads();
-    if ((threadIdx.x & 63) == 63) wave_sums[wave] = incl;
-    __syncthreads();
-    u64 before = 0, all = 0;
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w) {
-        if (w < wave) before += wave_sums[w];
-        all += wave_sums[w];
-    }
-    *total = all;
-    return before + incl - x;
-}
+// What top-k and top-p leave: logits above `key`, and the first `keep` of those at it.
+struct Kept {
+    unsigned key = 0;
+    u64 keep = ~(u64)0;
+};
 
+// The weight of a value that min-p keeps, else 0.
+struct Weigh {
+    const Weight& w;
+    double least;
+    __device__ __forceinline__ Weigh(const Weight& w_, float min_p) : w(w_), least((double)min_p * (double)((u64)1 << kOne)) {}
+    __device__ __forceinline__ u64 operator()(float x) const {
+        const double d = w.scaled(x);
+        return d >= least ? Weight::round(d) : 0;
+    }
+};
+
+// ---------------------------------------------------------------- histograms
 // hist[bin] += n for the active lanes.  A wave whose lanes all mean one bin adds
 // once: rows of few different logits would else wait for one address.
 __device__ __forceinline__ void add(u64* hist, int bin, u64 n, bool active) {
@@ -217,18 +317,23 @@ __device__ __forceinline__ void add(u64* hist, int bin, u64 n, bool active) {
     if (!m) return;
     const int first = __builtin_amdgcn_readlane(bin, __builtin_ctzll(m));
     if (__popcll(m) > 8 && __ballot(active && bin == first) == m) {
-        u64 x = active ? n : 0;
-#pragma unroll
-        for (int d = 32; d; d >>= 1) x += __shfl_xor(x, d);
+        const u64 x = last_lane(wave_inclusive(active ? n : 0));
         if ((threadIdx.x & 63) == 0) atomicAdd(&hist[first], x);
         return;
     }
     if (active) atomicAdd(&hist[bin], n);
 }
 
+__device__ __forceinline__ void clear_bins(Shared& s) {
+    s.hist[threadIdx.x] = 0;
+    s.hist[threadIdx.x + kThreads] = 0;
+    __syncthreads();
+}
+
 // The bin at which the running sum of the histogram reaches the target (>= 1).
 // False where the whole falls short of it.
 __device__ __forceinline__ bool pick(Shared& s, u64 target, int* bin, u64* before, u64* in) {
+    __syncthreads();
     const u64 h0 = s.hist[2 * threadIdx.x], h1 = s.hist[2 * threadIdx.x + 1];
     u64 all;
     const u64 ex = block_exclusive(h0 + h1, s.wave, &all);
@@ -243,14 +348,7 @@ __device__ __forceinline__ bool pick(Shared& s, u64 target, int* bin, u64* befor
     *bin = (int)s.bin;
     *before = s.picked[0];
     *in = s.picked[1];
-    __syncthreads();
     return true;
-}
-
-__device__ __forceinline__ void clear_bins(Shared& s) {
-    s.hist[threadIdx.x] = 0;
-    s.hist[threadIdx.x + kThreads] = 0;
-    __syncthreads();
 }
 
 // A border in the order by falling logit.
@@ -260,41 +358,37 @@ struct Border {
     u64 in;        // and of those at it
 };
 
-// Where the running measure (weights, or the count of logits) of the logits with
-// keys >= low reaches the target; false if that is not among those with weight.
-template <bool MASS, typename T, int NU>
-__device__ __forceinline__ bool find_border(Shared& s, const Row<T, NU>& row, const Weight& w, float per_bin, unsigned low, u64 target,
+// Where the running measure (weights, or the count of logits) of the logits >= low
+// reaches the target; false if that is not among those with weight.
+template <bool MASS, class Logits>
+__device__ __forceinline__ bool find_border(Shared& s, const Logits& logits, const Weight& w, float top, float T, float low, u64 target,
                                             Border& out) {
-    constexpr int E = Row<T, NU>::E;
     auto measure = [&](float x, bool active) { return MASS ? (__ballot(active) ? w.fixed(x) : 0) : (u64)1; };
     // bins of 1/64 of the temperature; the last takes all that has no weight
-    auto bin_of = [&](float x) {
-        const float d = w.top - x;  // NaN: both are infinite
-        return d > 0.f ? (int)fminf(d * per_bin, (float)(kBins - 1)) : 0;
-    };
+    const float per_bin = fminf(64.f / T, 1e30f);
+    auto bin_of = [&](float x) { return (int)fminf((top - x) * per_bin, (float)(kBins - 1)); };
+    auto wanted = [&](float tile_top) { return tile_top >= low; };
     clear_bins(s);
-    row.each([&](int, const float (&x)[E]) {
+    if (threadIdx.x == 0) s.lo = 0xffffffffu, s.hi = 0;
+    logits.each(wanted, [&](int, auto& x) {
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-            const bool active = key_of(x[e]) >= low;
-            add(s.hist, bin_of(x[e]), measure(x[e], active), active);
+        for (float v : x) {
+            const bool active = v >= low;
+            add(s.hist, bin_of(v), measure(v, active), active);
         }
     });
-    __syncthreads();
     int bin;
     u64 before, in;
     if (!pick(s, target, &bin, &before, &in) || bin == kBins - 1) return false;
     out.before = before;
     target -= before;
-    if (threadIdx.x == 0) s.lo = 0xffffffffu, s.hi = 0;
-    __syncthreads();
     {
         unsigned lo = 0xffffffffu, hi = 0;
-        row.each([&](int, const float (&x)[E]) {
+        logits.each(wanted, [&](int, auto& x) {
 #pragma unroll
-            for (int e = 0; e < E; ++e) {
-                const unsigned k = key_of(x[e]);
-                if (k >= low && bin_of(x[e]) == bin) {
+            for (float v : x) {
+                const unsigned k = key_of(v);
+                if (v >= low && bin_of(v) == bin) {
                     lo = lo < k ? lo : k;
                     hi = hi > k ? hi : k;
                 }
@@ -307,143 +401,334 @@ __device__ __forceinline__ bool find_border(Shared& s, const Row<T, NU>& row, co
     }
     __syncthreads();
     unsigned lo = s.lo, hi = s.hi;
+#pragma unroll 1
     while (lo != hi) {
         int shift = 0;
         while ((hi - lo) >> shift >= (unsigned)kBins) ++shift;
         clear_bins(s);
-        row.each([&](int, const float (&x)[E]) {
+        const float least = value_of(lo), most = value_of(hi);
+        logits.each([&](float tile_top) { return tile_top >= least; }, [&](int, auto& x) {
 #pragma unroll
-            for (int e = 0; e < E; ++e) {
-                const unsigned k = key_of(x[e]);
-                const bool active = k >= lo && k <= hi;
-                if (__ballot(active)) add(s.hist, active ? (int)((hi - k) >> shift) : 0, measure(x[e], active), active);
+            for (float v : x) {
+                const bool active = v >= least && v <= most;
+                if (__ballot(active)) add(s.hist, active ? (int)((hi - key_of(v)) >> shift) : 0, measure(v, active), active);
             }
         });
-        __syncthreads();
         if (!pick(s, target, &bin, &before, &in)) return false;  // not reached: the range's measure is at least the target
         out.before += before;
         target -= before;
-        const unsigned top = hi - ((unsigned)bin << shift);
-        const unsigned room = ((1u << shift) - 1) < top - lo ? (1u << shift) - 1 : top - lo;
-        lo = top - room;
-        hi = top;
+        const unsigned above = hi - ((unsigned)bin << shift);
+        const unsigned room = ((1u << shift) - 1) < above - lo ? (1u << shift) - 1 : above - lo;
+        lo = above - room;
+        hi = above;
     }
     out.key = lo;
     out.in = in;
     return true;
 }
 
-template <typename T, int NU>
-__global__ __launch_bounds__(kThreads) void sample_kernel(SampleArgs a) {
-    constexpr int E = 16 / sizeof(T);
-    __shared__ Shared s;
-    const int64_t r = blockIdx.x;
+__device__ __forceinline__ void answer(const SampleArgs& a, int64_t r, int token, double weight, double total) {
+    a.token[r] = token;
+    if (a.logprob) a.logprob[r] = (float)log(weight / total);
+}
+
+// ------------------------------------------------------- rows without a filter
+// The token from the tiles' weights, `mine` of this thread's.
+template <typename T>
+__device__ __forceinline__ void draw_from_tiles(Shared& s, const Row<T>& row, const Weight& w, double mine, const Settings& c,
+                                                const SampleArgs& a, int64_t r) {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    __shared__ u32x4 held[NU ? NU * kThreads : 1];
-    const Row<T, NU> row((const T*)a.logits + r * a.stride, a.V, held);
-    if (threadIdx.x < 64) s.table[threadIdx.x] = exp2((double)threadIdx.x / 64);
-
-    float T0 = a.temperature ? a.temperature[r] : a.T;
-    int top_k = a.top_k ? a.top_k[r] : a.k;
-    float top_p = a.top_p ? a.top_p[r] : a.p, min_p = a.min_p ? a.min_p[r] : a.mp, u = a.u[r];
-    if (!(top_p >= 0.f)) top_p = top_p != top_p ? 1.f : 0.f;
-    if (!(min_p <= 1.f)) min_p = min_p != min_p ? 0.f : 1.f;
-    u = u >= 0.f ? fminf(u, 0x1.fffffep-1f) : 0.f;
-
-    // the largest, and where it first stands
-    float top = neg_inf();
-    row.template each<true>([&](int, const float (&x)[E]) {
-#pragma unroll
-        for (int e = 0; e < E; ++e) top = fmaxf(top, x[e]);
-    });
-#pragma unroll
-    for (int d = 32; d; d >>= 1) top = fmaxf(top, __shfl_xor(top, d));
-    if (lane == 0) s.wave[wave] = key_of(top);
-    if (threadIdx.x == 0) s.index = 0x7fffffff;
+    if (threadIdx.x == 0) s.index = 0;
+    double total;
+    const double before = block_exclusive(mine, s.wave_d, &total), at = (double)c.u * total;
+    // the last tile that begins at or before the place: one with weight, since sums only grow there
+    if (mine > 0 && before <= at) atomicMax(&s.index, (int)threadIdx.x);
     __syncthreads();
-    unsigned best = 0;
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w) best = best > (unsigned)s.wave[w] ? best : (unsigned)s.wave[w];
-    top = __builtin_bit_cast(float, best & 0x80000000u ? best ^ 0x80000000u : ~best);
+    const int tile = s.index, j = tile / kWaves;
+    if ((int)threadIdx.x == tile) s.wave_d[0] = at - before;
     __syncthreads();
-    if (!(T0 > 0.f) || top == neg_inf()) {
-        int at = 0x7fffffff;
-        row.each([&](int j, const float (&x)[E]) {
+    if (wave != tile % kWaves) return;
+    const double left = s.wave_d[0];
+    float x[E];
+    row.values(row.load(j), x);
+    u64 v[E], sum = 0;
 #pragma unroll
-            for (int e = E - 1; e >= 0; --e)
-                if (x[e] == top) {
-                    const int i = row.index(j, e);
-                    at = i < at ? i : at;
-                }
-        });
-        if (at != 0x7fffffff) atomicMin(&s.index, at);
-        __syncthreads();
-        if (threadIdx.x == 0) {
-            const bool none = top == neg_inf();
-            a.token[r] = none ? -1 : s.index;
-            if (a.logprob) a.logprob[r] = none ? __builtin_nanf("") : 0.f;
-        }
-        return;
-    }
-    const Weight w{64 * 1.4426950408889634074 / (double)T0, (double)top, top, s.table};
-    const float per_bin = fminf(64.f / T0, 1e30f);
-
-    // the border: logits above `key` are kept, of those at it the first `keep`
-    unsigned key = 0;
-    u64 keep = ~(u64)0, spare = 0;  // spare: weight at the border that top-k has dropped
-    if (top_k > 0 && top_k < a.V) {
-        Border b;
-        if (find_border<false>(s, row, w, per_bin, 0u, (u64)top_k, b)) {
-            key = b.key;
-            keep = top_k - b.before;
-            const unsigned bits = key & 0x80000000u ? key ^ 0x80000000u : ~key;
-            spare = (b.in - keep) * w.fixed(__builtin_bit_cast(float, bits));
-        }
-    }
-    if (top_p < 1.f) {
-        u64 sum = 0, total;
-        row.each([&](int, const float (&x)[E]) {
+    for (int e = 0; e < E; ++e) sum += v[e] = w.fixed(x[e]);
+    u64 run = wave_inclusive(sum) - sum;
+    // the first value whose running weight exceeds it; where the tile's sum is less by
+    // what rounding the weights left out, the last value with weight
+    int found = -1, last = -1;
 #pragma unroll
-            for (int e = 0; e < E; ++e) {
-                const bool in = key_of(x[e]) >= key;
-                if (__ballot(in)) sum += in ? w.fixed(x[e]) : 0;
-            }
-        });
-        block_exclusive(sum, s.wave, &total);
-        bool whole;
-        u64 target = part_of(top_p, total - spare, &whole);
-        if (!whole || target == 0) ++target;
-        Border b;
-        if (find_border<true>(s, row, w, per_bin, key, target, b)) {
-            key = b.key;
-            const unsigned bits = key & 0x80000000u ? key ^ 0x80000000u : ~key;
-            const u64 each = w.fixed(__builtin_bit_cast(float, bits));
-            keep = (target - b.before + each - 1) / each;
-        }
+    for (int e = 0; e < E; ++e) {
+        if (v[e]) last = e;
+        if ((double)run <= left && left < (double)(run + v[e])) found = e;
+        run += v[e];
     }
+    const u64 some = __ballot(found >= 0), any = __ballot(last >= 0);
+    const int at_lane = some ? __builtin_ctzll(some) : 63 - __builtin_clzll(any);
+    if (lane != at_lane) return;
+    if (!some) found = last;
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+        if (e == found) answer(a, r, row.index(j, e), (double)v[e], total);
+}
 
-    // weights of what is kept, by tiles: step j of a wave
-    const double least = (double)min_p * (double)((u64)1 << kOne);
-    const unsigned bits = key & 0x80000000u ? key ^ 0x80000000u : ~key;
-    const float at_border = __builtin_bit_cast(float, bits);
-    auto weigh = [&](float x) {
-        const double d = w.scaled(x);
-        return d >= least ? Weight::round(d) : 0;
+// Rows whose largest logit is infinite: the tokens that have it, equal ones.
+template <typename T>
+__device__ __forceinline__ void draw_infinite(Shared& s, const Row<T>& row, float top, const Settings& c, const SampleArgs& a, int64_t r) {
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    if (threadIdx.x < kTiles) s.sum[threadIdx.x] = 0;
+    __syncthreads();
+    auto count = [&](const float (&x)[E]) {
+        int n = 0;
+#pragma unroll
+        for (int e = 0; e < E; ++e) n += x[e] == top;
+        return n;
     };
-    const u64 border = keep == ~(u64)0 ? 0 : weigh(at_border);
-    row.each([&](int j, const float (&x)[E]) {
+    row.each([&](float tile_top) { return tile_top == top; }, [&](int j, const float (&x)[E]) {
+        const int n = last_lane(wave_inclusive(count(x)));
+        if (lane == 0) s.sum[j * kWaves + wave] = (u64)n;
+    });
+    __syncthreads();
+    const u64 mine = threadIdx.x < kTiles ? s.sum[threadIdx.x] : 0;
+    u64 n;
+    const u64 before = block_exclusive(mine, s.wave, &n);
+    if (c.by_k && (u64)c.top_k < n) n = (u64)c.top_k;
+    if (c.by_p) n = part_up(c.top_p, n);
+    bool whole;
+    const u64 at = part_of(c.u, n, &whole);
+    if (before <= at && at < before + mine) {
+        s.bin = threadIdx.x;
+        s.picked[0] = at - before;
+    }
+    __syncthreads();
+    const int tile = (int)s.bin, j = tile / kWaves;
+    if (wave != tile % kWaves) return;
+    float x[E];
+    row.values(row.load(j), x);
+    const int here = count(x);
+    int run = wave_inclusive(here) - here;
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+        if (x[e] == top && run++ == (int)s.picked[0]) answer(a, r, row.index(j, e), 1.0, (double)n);
+}
+
+// ------------------------------------------------------------------ the list
+// Logits with `lo` <= bin <= `hi` go into the list, and the weights of those above
+// become their tiles' sums; false if there are too many.
+template <typename T, class B>
+__device__ __forceinline__ bool gather(Shared& s, const Row<T>& row, const Weight& w, B&& bin_of, int lo, int hi, float floor_x, List& list) {
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    if (threadIdx.x == 0) s.index = 0;
+    if (threadIdx.x < kTiles) s.sum[threadIdx.x] = 0;
+    __syncthreads();
+    row.each([&](float x) { return x >= floor_x && bin_of(x) >= lo; }, [&](int j, const float (&x)[E]) {
+        unsigned in = 0;
+        bool more = false;
+        u64 sum = 0;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const int b = bin_of(x[e]);
+            const bool ok = x[e] >= floor_x && x[e] != neg_inf();
+            in |= (unsigned)(ok && b >= lo && b <= hi) << e;
+            const bool above = ok && b > hi;
+            if (__ballot(above)) {
+                more = true;
+                const u64 v = w.fixed(x[e]);
+                sum += above ? v : 0;
+            }
+        }
+        if (more) {
+            sum = last_lane(wave_inclusive(sum));
+            if (lane == 0) s.sum[j * kWaves + wave] = sum;
+        }
+        const int mine = __popc(in), incl = wave_inclusive(mine), all = last_lane(incl);
+        if (all == 0) return;
+        int base = 0;
+        if (lane == 0) base = atomicAdd(&s.index, all);
+        int to = __builtin_amdgcn_readfirstlane(base) + incl - mine;
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            if (in >> e & 1) {
+                if (to < kList) {
+                    s.keys[to] = key_of(x[e]);
+                    s.at[to] = row.index(j, e);
+                }
+                ++to;
+            }
+    });
+    __syncthreads();
+    list = {s.keys, s.at, s.index};
+    return list.n <= kList;
+}
+
+// Where the running measure of a list in order of index reaches the target (which
+// it does).
+template <class F>
+__device__ __forceinline__ int find_index(Shared& s, const List& list, int V, u64 target, F&& measure) {
+    int lo = 0, shift = 0;
+    while ((V - 1) >> shift >= kBins) ++shift;
+#pragma unroll 1
+    for (;;) {
+        clear_bins(s);
+#pragma unroll 1
+        for (int i = threadIdx.x; i < list.n; i += kThreads) {
+            const int d = list.at[i] - lo;
+            if (d >= 0 && d >> shift < kBins)
+                if (const u64 m = measure(i)) atomicAdd(&s.hist[d >> shift], m);
+        }
+        int bin;
+        u64 before, in;
+        pick(s, target, &bin, &before, &in);
+        target -= before;
+        lo += bin << shift;
+        if (shift == 0) return lo;
+        shift = 0;  // the histogram takes that bin and what follows it, which the target does not reach
+    }
+}
+
+// top-k and top-p on a list, above which `n_above` logits are.  goal: the weight to
+// reach from the top of the row on, 0 where the list tells.  A list that ends where
+// min-p does may fall short of the targets, and is then kept as a whole.
+__device__ __forceinline__ bool filter_list(Shared& s, const List& list, const Weight& w, float top, const Settings& c, u64 n_above,
+                                            u64 goal, bool short_list, Kept& kept, bool* all_ties) {
+    *all_ties = true;
+    u64 spare = 0;  // weight at the border that top-k has dropped
+    if (c.by_k) {
+        Border b;
+        if (find_border<false>(s, list, w, top, c.T, neg_inf(), (u64)c.top_k - n_above, b)) {
+            kept.key = b.key;
+            kept.keep = c.top_k - n_above - b.before;
+            *all_ties = kept.keep == b.in;
+            spare = (b.in - kept.keep) * w.fixed(value_of(b.key));
+        } else if (n_above) {
+            return false;
+        }  // else the list is shorter, or what lies at the border has no weight
+    }
+    if (!c.by_p) return true;
+    const float low = kept.key == 0 ? neg_inf() : value_of(kept.key);
+    u64 sum = 0, all;
+    if (goal == 0) {  // the list holds all that top-k keeps, or the whole row
+        list.each(0, [&](int, auto& x) {
+#pragma unroll
+            for (float v : x) sum += v >= low ? w.fixed(v) : 0;
+        });
+        block_exclusive(sum, s.wave, &all);
+        goal = part_up(c.top_p, all - spare);
+    } else {
+        sum = threadIdx.x < kTiles ? s.sum[threadIdx.x] : 0;
+        block_exclusive(sum, s.wave, &all);
+        if (goal <= all) return false;
+        goal -= all;
+    }
+    Border b;
+    if (!find_border<true>(s, list, w, top, c.T, low, goal, b)) return short_list;
+    const u64 each = w.fixed(value_of(b.key));
+    kept.key = b.key;
+    kept.keep = (goal - b.before + each - 1) / each;
+    *all_ties = kept.keep * each == b.in;
+    return true;
+}
+
+// The token among the tiles' sums and what is kept of the list.
+template <typename T>
+__device__ __forceinline__ void draw_from_list(Shared& s, const Row<T>& row, const List& list, const Weight& w, const Settings& c,
+                                               const Kept& kept, bool all_ties, const SampleArgs& a, int64_t r) {
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const Weigh weigh(w, c.min_p);
+    int last = 0x7fffffff;  // the index of the last tie that is kept
+    if (!all_ties) last = find_index(s, list, a.V, kept.keep, [&](int i) { return (u64)(list.keys[i] == kept.key); });
+    auto measure = [&](unsigned k, int index, float x) { return k > kept.key || (k == kept.key && index <= last) ? weigh(x) : 0; };
+    __syncthreads();
+#pragma unroll 1
+    for (int i = threadIdx.x; i < list.n; i += kThreads) {
+        const u64 m = measure(list.keys[i], list.at[i], value_of(list.keys[i]));
+        if (m) atomicAdd(&s.sum[(list.at[i] + row.off) / kTile], m);
+    }
+    __syncthreads();
+    const u64 mine = threadIdx.x < kTiles ? s.sum[threadIdx.x] : 0;
+    u64 total;
+    const u64 before = block_exclusive(mine, s.wave, &total);
+    bool whole;
+    const u64 at = part_of(c.u, total, &whole);
+    if (before <= at && at < before + mine) {
+        s.bin = threadIdx.x;
+        s.picked[0] = at - before;
+    }
+    __syncthreads();
+    const int tile = (int)s.bin, j = tile / kWaves;
+    if (wave != tile % kWaves) return;
+    const u64 left = s.picked[0];
+    float x[E];
+    row.values(row.load(j), x);
+    u64 v[E], sum = 0;
+#pragma unroll
+    for (int e = 0; e < E; ++e) sum += v[e] = x[e] == x[e] ? measure(key_of(x[e]), row.index(j, e), x[e]) : 0;
+    u64 run = wave_inclusive(sum) - sum;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        if (run <= left && left < run + v[e]) answer(a, r, row.index(j, e), (double)v[e], (double)total);
+        run += v[e];
+    }
+}
+
+// -------------------------------------------------------------- the slow way
+// The same with passes over the whole row.
+template <typename T>
+__device__ __forceinline__ void draw_from_row(Shared& s, const Row<T>& row, const Weight& w, float top, const Settings& c, double weight,
+                                              const SampleArgs& a, int64_t r) {
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    float border = neg_inf();  // logits above it are kept, of those at it the first `keep`
+    u64 keep = ~(u64)0;
+    bool every = true;
+    Border b;
+    u64 spare = 0;
+    if (c.by_k && find_border<false>(s, row, w, top, c.T, neg_inf(), (u64)c.top_k, b)) {
+        border = value_of(b.key);
+        keep = c.top_k - b.before;
+        every = false;
+        spare = (b.in - keep) * w.fixed(border);
+    }
+    if (c.by_p) {
+        u64 goal;
+        if (weight > 0) {
+            goal = (u64)ceil((double)c.top_p * weight);
+            goal += goal == 0;
+        } else {
+            u64 sum = 0, all;
+            row.each([&](float tile_top) { return tile_top >= border; }, [&](int, const float (&x)[E]) {
+#pragma unroll
+                for (int e = 0; e < E; ++e)
+                    if (__ballot(x[e] >= border)) {
+                        const u64 v = w.fixed(x[e]);
+                        sum += x[e] >= border ? v : 0;
+                    }
+            });
+            block_exclusive(sum, s.wave, &all);
+            goal = part_up(c.top_p, all - spare);
+        }
+        if (find_border<true>(s, row, w, top, c.T, border, goal, b)) {
+            border = value_of(b.key);
+            const u64 each = w.fixed(border);
+            keep = (goal - b.before + each - 1) / each;
+            every = false;
+        }
+    }
+    const Weigh weigh(w, c.min_p);
+    const u64 at_border = every ? 0 : weigh(border);
+    if (threadIdx.x < kTiles) s.sum[threadIdx.x] = 0, s.ties[threadIdx.x] = 0;
+    __syncthreads();
+    auto is_tie = [&](float x) { return x == border && !every; };
+    row.each([&](float tile_top) { return tile_top >= border; }, [&](int j, const float (&x)[E]) {
         u64 sum = 0;
         int ties = 0;
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-            const unsigned k = key_of(x[e]);
-            if (__ballot(k >= key)) {
-                const bool tie = k == key && keep != ~(u64)0;
-                ties += tie;
+        for (int e = 0; e < E; ++e)
+            if (__ballot(x[e] >= border)) {
+                ties += is_tie(x[e]);
                 const u64 v = weigh(x[e]);
-                sum += k >= key && !tie ? v : 0;
+                sum += x[e] >= border && !is_tie(x[e]) ? v : 0;
             }
-        }
         sum = wave_inclusive(sum);
         ties = wave_inclusive(ties);
         if (lane == 63) {
@@ -453,69 +738,230 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(SampleArgs a) {
     });
     __syncthreads();
     // a thread per tile, in order of index: its ties that are kept, its weight
-    const int tiles = row.steps * kWaves, t = threadIdx.x;
-    const int n = t < tiles ? s.ties[t] : 0;
-    u64 all_ties;
+    const int t = threadIdx.x, n = t < kTiles ? s.ties[t] : 0;
+    u64 all_ties, total;
     const u64 ties_before = block_exclusive((u64)n, s.wave, &all_ties);
     const u64 room = keep > ties_before ? keep - ties_before : 0;
-    const u64 mine = (t < tiles ? s.sum[t] : 0) + border * (room < (u64)n ? room : (u64)n);
-    u64 total;
+    const u64 mine = (t < kTiles ? s.sum[t] : 0) + at_border * (room < (u64)n ? room : (u64)n);
     const u64 before = block_exclusive(mine, s.wave, &total);
     bool whole;
-    const u64 at = part_of(u, total, &whole);
+    const u64 at = part_of(c.u, total, &whole);
     if (before <= at && at < before + mine) {
         s.bin = t;
         s.picked[0] = at - before;
         s.picked[1] = ties_before;
     }
     __syncthreads();
-    const int tile = (int)s.bin;
+    const int tile = (int)s.bin, j = tile / kWaves;
     if (wave != tile % kWaves) return;
-    // in that tile: the first value whose running weight exceeds `left`
     const u64 left = s.picked[0];
-    u64 used = s.picked[1];
-    row.each([&](int j, const float (&x)[E]) {
-        if (j != tile / kWaves) return;
-        int ties = 0;
+    float x[E];
+    row.values(row.load(j), x);
+    int ties = 0;
 #pragma unroll
-        for (int e = 0; e < E; ++e) ties += key_of(x[e]) == key && keep != ~(u64)0;
-        used += wave_inclusive(ties) - ties;
-        u64 v[E], sum = 0;
+    for (int e = 0; e < E; ++e) ties += is_tie(x[e]);
+    u64 used = s.picked[1] + wave_inclusive(ties) - ties;
+    u64 v[E], sum = 0;
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-            const unsigned k = key_of(x[e]);
-            const bool tie = k == key && keep != ~(u64)0;
-            v[e] = k > key || (k == key && (!tie || used < keep)) ? weigh(x[e]) : 0;
-            used += tie;
-            sum += v[e];
-        }
-        u64 run = wave_inclusive(sum) - sum;
+    for (int e = 0; e < E; ++e) {
+        const bool tie = is_tie(x[e]);
+        v[e] = x[e] >= border && (!tie || used < keep) ? weigh(x[e]) : 0;
+        used += tie;
+        sum += v[e];
+    }
+    u64 run = wave_inclusive(sum) - sum;
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-            if (run <= left && left < run + v[e]) {
-                a.token[r] = row.index(j, e);
-                if (a.logprob) a.logprob[r] = (float)log((double)v[e] / (double)total);
-            }
-            run += v[e];
-        }
-    });
+    for (int e = 0; e < E; ++e) {
+        if (run <= left && left < run + v[e]) answer(a, r, row.index(j, e), (double)v[e], (double)total);
+        run += v[e];
+    }
 }
 
 template <typename T>
-hipError_t launch(const SampleArgs& a, hipStream_t s) {
-    const dim3 gr((unsigned)a.rows), bl(kThreads);
-    const int unit = 16 / (int)sizeof(T), units = (a.V + unit - 1 + kThreads * unit - 1) / (kThreads * unit);
-    if (units <= 1) sample_kernel<T, 1><<<gr, bl, 0, s>>>(a);
-    else if (units <= 4) sample_kernel<T, 4><<<gr, bl, 0, s>>>(a);
-    else if (units <= 8) sample_kernel<T, 8><<<gr, bl, 0, s>>>(a);
-    else sample_kernel<T, 0><<<gr, bl, 0, s>>>(a);
-    return hipGetLastError();
+__global__ __launch_bounds__(kThreads) void sample_kernel(SampleArgs a) {
+    __shared__ Shared s;
+    const int64_t r = blockIdx.x;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), t = threadIdx.x;
+    const Row<T> row((const T*)a.logits + r * a.stride, a.V, s.tops);
+    typename Row<T>::Raw raw = row.load(0);
+
+    Settings c;
+    c.T = a.temperature ? a.temperature[r] : a.T;
+    c.top_k = a.top_k ? a.top_k[r] : a.k;
+    c.top_p = a.top_p ? a.top_p[r] : a.p;
+    c.min_p = a.min_p ? a.min_p[r] : a.mp;
+    c.u = a.u[r];
+    if (!(c.top_p >= 0.f)) c.top_p = c.top_p != c.top_p ? 1.f : 0.f;
+    if (!(c.min_p <= 1.f)) c.min_p = c.min_p != c.min_p ? 0.f : 1.f;
+    c.u = c.u >= 0.f ? fminf(c.u, 0x1.fffffep-1f) : 0.f;
+    c.by_k = c.top_k > 0 && c.top_k < a.V;
+    c.by_p = c.top_p < 1.f;
+    const bool greedy = !(c.T > 0.f), small = a.V <= kList;  // a small row is a list
+    const bool counts = !greedy && !small && (c.by_k || c.by_p);
+    const bool weights = !greedy && !c.by_k && (c.by_p ? !small : !(c.min_p > 0.f));
+
+    if (!greedy) s.table[t] = exp2((double)t / kTable);
+    if (t < kTiles) s.tops[t] = neg_inf();
+    unsigned* const count = (unsigned*)s.hist;
+    clear_bins(s);
+    float top = neg_inf(), ref = 0.f;
+    const float per_bin = fminf((float)kFine / c.T, 1e30f);
+    auto place_of = [&](float x) { return fminf(fmaxf((x - ref) * per_bin, -1e9f), 1e9f); };
+    auto bin_of = [&](float x) { return (int)floorf(place_of(x)); };
+    int newest = 0;  // the bin of the largest value so far; bins count from the first such
+#pragma unroll 1
+    for (int j = 0; j < row.steps; ++j) {
+        typename Row<T>::Raw more = raw;
+        if (j + 1 < row.steps) more = row.load(j + 1);
+        float x[E];
+        row.values(raw, x);
+        raw = more;
+        float m = x[0];
+#pragma unroll
+        for (int e = 1; e < E; ++e) m = fmaxf(m, x[e]);
+        m = wave_max(m);
+        if (lane == 0) s.tops[j * kWaves + wave] = m;
+        if (weights) {
+            double sum = 0;
+            if (m != neg_inf()) {
+                const Weight w(c.T, m, s.table);
+#pragma unroll
+                for (int e = 0; e < E; ++e) sum += w.scaled(x[e]);
+            }
+            sum = wave_inclusive(sum);
+            if (lane == 63) s.sum[j * kWaves + wave] = __builtin_bit_cast(u64, sum);
+        }
+        if (!counts) continue;
+        const float old = top;
+        if (lane == 0) s.wtop[j & 1][wave] = m;
+        __syncthreads();
+        top = fmaxf(top, wave_max(s.wtop[j & 1][lane % kWaves]));
+        if (top == neg_inf()) continue;
+        if (old == neg_inf()) {
+            ref = top;
+            newest = bin_of(top);
+        } else if (top > old) {  // bins come in at the top, in the place of those that fall out at the bottom
+            const int now = bin_of(top), n = now - newest < kBins ? now - newest : kBins;
+            for (int i = t; i < n; i += kThreads) count[(now - i) & (kBins - 1)] = 0;
+            newest = now;
+            __syncthreads();
+        }
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const int b = bin_of(x[e]);
+            if (x[e] > neg_inf() && newest - b < kBins - 1) atomicAdd(&count[b & (kBins - 1)], 1u);
+        }
+    }
+    __syncthreads();
+    top = neg_inf();
+    for (int i = lane; i < kTiles; i += 64) top = fmaxf(top, s.tops[i]);
+    top = wave_max(top);
+    if (greedy || top == neg_inf()) {
+        if (t == 0) s.index = 0x7fffffff;
+        __syncthreads();
+        int at = 0x7fffffff;
+        row.each([&](float tile_top) { return tile_top == top; }, [&](int j, const float (&x)[E]) {
+#pragma unroll
+            for (int e = E - 1; e >= 0; --e)
+                if (x[e] == top) {
+                    const int i = row.index(j, e);
+                    at = i < at ? i : at;
+                }
+        });
+        if (at != 0x7fffffff) atomicMin(&s.index, at);
+        __syncthreads();
+        if (t == 0) {
+            const bool none = top == neg_inf();
+            a.token[r] = none ? -1 : s.index;
+            if (a.logprob) a.logprob[r] = none ? __builtin_nanf("") : 0.f;
+        }
+        return;
+    }
+    if (top == -neg_inf()) {
+        draw_infinite(s, row, top, c, a, r);
+        return;
+    }
+
+    const Weight w(c.T, top, s.table);
+    double weight = 0;  // of the row, in 2^-44
+    if (weights) {      // a tile's, relative to the row's maximum; 0 where no value of it has any
+        const float m = t < kTiles ? s.tops[t] : neg_inf();
+        const double mine = w.fixed(m) ? __builtin_bit_cast(double, s.sum[t]) * (w.scaled(m) * 0x1p-44) : 0.0;
+        if (!c.by_p) {
+            draw_from_tiles(s, row, w, mine, c, a, r);
+            return;
+        }
+        block_exclusive(mine, s.wave_d, &weight);
+    }
+
+    // the list need not reach below min-p, unless top-p takes a weight from it
+    const bool part = c.min_p > 0.f && !(c.by_p && (c.by_k || small));
+    const float floor_x = part ? top + c.T * (logf(c.min_p) - 0.001f) : neg_inf();
+    int lo = -0x7fffffff, hi = 0x7fffffff;
+    u64 n_above = 0, goal = 0;
+    bool fits = true, short_list = part;  // the list ends at min-p
+    if (counts) {
+        // the two bins of this thread, from the newest down, and what their counts weigh at least
+        const int i = 2 * t, end = (part && newest - bin_of(floor_x) < kWhole ? newest - bin_of(floor_x) + 1 : kWhole) / 2;
+        const unsigned n0 = i < kWhole ? count[(newest - i) & (kBins - 1)] : 0, n1 = i + 1 < kWhole ? count[(newest - i - 1) & (kBins - 1)] : 0;
+        u64 all;
+        const u64 before = block_exclusive((u64)(n0 + n1), s.wave, &all), upto = before + n0 + n1;
+        bool may = false, must = false;  // the border may lie in these bins, or above or in them
+        if (c.by_k) {
+            may = must = upto >= (u64)c.top_k;
+        } else {
+            const float step = exp2f(-1.44269504f / kFine), deep = place_of(top) - (float)(newest - i);
+            const float w0 = exp2f(-1.44269504f / kFine * deep), mine = (float)n0 * w0 + (float)n1 * (w0 * step);
+            float sum;
+            const float least = block_exclusive(mine, s.wave_f, &sum) + mine;
+            goal = (u64)ceil((double)c.top_p * weight);
+            goal += goal == 0;
+            const float want = (float)goal * 0x1p-44f;
+            must = least >= want * 1.004f;
+            may = least * 1.012f >= want;  // e^(1/kFine), and as much for rounding on either side
+        }
+        // the border's pairs of bins: from the first that may hold it to the first that it cannot lie below
+        if (t == 0) s.index = s.last = kThreads;
+        __syncthreads();
+        if (may) atomicMin(&s.index, t);
+        if (must) atomicMin(&s.last, t);
+        __syncthreads();
+        const int first = s.index < end ? s.index : end, last = s.last < end ? s.last : end;
+        fits = s.last < kWhole / 2 || (part && end < kWhole / 2);
+        short_list = part && last == end;
+        if (t == last) s.picked[0] = upto;
+        if (t == first) s.picked[1] = before;
+        __syncthreads();
+        lo = newest - 2 * last - 1;
+        const u64 most = s.picked[0], skipped = s.picked[1];
+        if (most > (u64)kList) {  // only the bins themselves
+            fits = fits && most - skipped <= (u64)kList && !(c.by_k && c.by_p);
+            hi = newest - 2 * first;
+            if (part && hi <= bin_of(floor_x)) hi = bin_of(floor_x) + 1;
+            n_above = skipped;
+            if (part && hi != newest - 2 * first) fits = false;
+        }
+        __syncthreads();
+    }
+    List list;
+    Kept kept;
+    bool all_ties;
+    if (fits && gather(s, row, w, bin_of, lo, hi, floor_x, list) &&
+        filter_list(s, list, w, top, c, n_above, goal, short_list, kept, &all_ties)) {
+        draw_from_list(s, row, list, w, c, kept, all_ties, a, r);
+        return;
+    }
+    __syncthreads();
+    draw_from_row(s, row, w, top, c, weight, a, r);
 }
 
 }  // namespace
 
 hipError_t launch_sample(const SampleArgs& a, hipStream_t s) {
-    return a.f32 ? launch<float>(a, s) : launch<__bf16>(a, s);
+    const dim3 gr((unsigned)a.rows), bl(kThreads);
+    if (a.f32) sample_kernel<float><<<gr, bl, 0, s>>>(a);
+    else sample_kernel<__bf16><<<gr, bl, 0, s>>>(a);
+    return hipGetLastError();
 }
 
 }  // namespace e2ttt
