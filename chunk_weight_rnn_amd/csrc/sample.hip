@@ -6,19 +6,21 @@
 // falling logit, so what it needs is the logit at which the running count or
 // weight reaches a target.  Equal logits at that border are kept by index.
 //
-// The row is read once for the maximum of every tile (512 values of a wave) and,
-// as the settings ask for them, the tiles' weights relative to their own maxima and
-// the counts of the logits in bins of 1/kFine of a temperature, 16 of them deep, that
-// move along with the largest logit so far.  Then
+// The row is read once for the maximum of every tile (512 values of a wave) and of
+// every thread and, as the settings ask for them, the tiles' weights and the counts
+// of the logits in bins of 1/64 of a power of two, 31 powers deep, that move along
+// with the largest logit so far.  Then
 //  * without a filter the tile that holds the token follows from the tiles' weights,
 //    and it alone is read again;
-//  * else the bins' counts say within which bins the border lies: exactly for a
-//    count, and for a weight within the e^(1/kFine) that logits of a bin differ by.
-//    A second pass, over the tiles whose maximum is that large, sums the weights
-//    above those bins tile by tile and gathers the logits in them, some hundred at
-//    most times, in a list (or all logits down to them, if they are few).  The border
-//    is found in the list, the list's weights go to their tiles, and one tile is read
-//    again.
+//  * the top_k largest lie at or above the top_k-th largest of the threads' maxima,
+//    and little more does (k of 1024: -1024 ln(1 - k/1024) logits);
+//  * for top_p the bins' counts say within which bins the border lies, up to the
+//    2^(1/64) that the weights in a bin differ by.
+// A second pass, over the tiles whose maximum is that large, gathers the logits from
+// there on in a list, some hundred at most times; or, where they are many, those of
+// the border's bins alone, and sums the weights above tile by tile.  The border is
+// found in the list, the list's weights go to their tiles, and one tile is read again.
+// A list of up to 128 is one wave's, which compares all with all.
 // Rows whose border lies deeper than the bins reach, or where more than kList logits
 // share its bins (equal ones, say), go the slow way: histograms of the whole row.
 //
@@ -29,9 +31,10 @@
 // floats added in one order: exact for equal logits, and else to 2^-45 of the largest
 // per logit, as the rounding is that they leave out.
 //
-// What bounds it: a compute unit reads its row once at its share of the bandwidth,
-// and the exponentials, where they are needed of every logit, are some 25
-// instructions in 64 bits each.
+// What bounds it: of long rows the exponentials, some 20 instructions in 64 bits for
+// every logit where its weight is needed, and the histogram (64 additions in the LDS
+// take some 25 cycles, and 6 each where they are to one address: so threads that agree
+// add once); of a few rows the chain of barriers.
 #include "tokens_internal.h"
 
 namespace e2ttt {
@@ -48,9 +51,12 @@ constexpr int kTile = 64 * E;
 constexpr int kStep = kTile * kWaves;
 constexpr int kTiles = (E2TTT_SAMPLE_VOCAB + 8 + kStep - 1) / kStep * kWaves;
 constexpr int kList = 8192;      // logits that are gathered, at most
-constexpr int kFine = 128;       // bins of a temperature
-constexpr int kWhole = 15 * kFine - 2;  // bins below the newest that lack nothing
-constexpr int kTable = 1024;
+constexpr int kTable = 1024;     // exponents are in 1024ths of a power of two
+constexpr int kBinShift = 4;     // and bins in 16 of those
+constexpr int kWhole = 31 * 64;  // bins from the newest on that lack nothing
+constexpr int kMostBin = 256 * 64;  // past it bins count anew, so that no weight overflows
+constexpr int kOneWave = 128;    // logits of a list that one wave deals with
+constexpr int kByMaxima = 1000;  // top_k up to which the threads' maxima tell
 static_assert(kTiles <= kThreads && kTable == kThreads, "a thread per tile, and per entry");
 
 __device__ __forceinline__ float neg_inf() { return -__builtin_inff(); }
@@ -85,15 +91,17 @@ __device__ __forceinline__ X wave_inclusive(X x) {
     return wave_scan(x, X{}, [](X a, X b) { return a + b; });
 }
 template <typename X>
-__device__ __forceinline__ X last_lane(X x) {
+__device__ __forceinline__ X lane_of(X x, int lane) {
     if constexpr (sizeof(X) == 4) {
-        return __builtin_bit_cast(X, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), 63));
+        return __builtin_bit_cast(X, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), lane));
     } else {
         const u64 v = __builtin_bit_cast(u64, x);
-        const unsigned lo = __builtin_amdgcn_readlane((int)v, 63), hi = __builtin_amdgcn_readlane((int)(v >> 32), 63);
+        const unsigned lo = __builtin_amdgcn_readlane((int)v, lane), hi = __builtin_amdgcn_readlane((int)(v >> 32), lane);
         return __builtin_bit_cast(X, (u64)hi << 32 | lo);
     }
 }
+template <typename X>
+__device__ __forceinline__ X last_lane(X x) { return lane_of(x, 63); }
 __device__ __forceinline__ float wave_max(float x) {
     return last_lane(wave_scan(x, neg_inf(), [](float a, float b) { return fmaxf(a, b); }));
 }
@@ -109,14 +117,15 @@ __device__ __forceinline__ X block_exclusive(X x, X* wave_sums, X* total) {
     __syncthreads();
     if ((threadIdx.x & 63) == 63) wave_sums[wave] = incl;
     __syncthreads();
-    X before = 0, all = 0;
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w) {
-        if (w == wave) before = all;
-        all += wave_sums[w];
-    }
-    *total = all;
-    return before + (incl - x);
+    // every 16 lanes add up the waves' sums
+    X v = wave_sums[threadIdx.x & (kWaves - 1)];
+    const X own = v;
+    v += from_lane<0x111, 0xf>(v, X{});
+    v += from_lane<0x112, 0xf>(v, X{});
+    v += from_lane<0x114, 0xf>(v, X{});
+    v += from_lane<0x118, 0xf>(v, X{});
+    *total = lane_of(v, kWaves - 1);
+    return lane_of(v - own, __builtin_amdgcn_readfirstlane(wave)) + (incl - x);
 }
 
 // -------------------------------------------------------------------- logits
@@ -229,13 +238,16 @@ struct Weight {
     const double* table;  // 2^(i / 1024)
     __device__ __forceinline__ Weight(float T, float top_, const double* table_)
         : c(kTable * 1.4426950408889634074 / (double)T), top((double)top_), table(table_) {}
-    __device__ __forceinline__ double scaled(float x) const {
-        constexpr double magic = 6755399441055744.0;  // 1.5 2^52: what is added to it is rounded to a whole number
+    __device__ __forceinline__ double exponent(float x) const {
+        return fmax(((double)x - top) * c, -1000.0 * kTable);  // also of NaN: nothing
+    }
+    static constexpr double magic = 6755399441055744.0;  // 1.5 2^52: what is added to it is rounded to a whole number
+    static __device__ __forceinline__ int whole(double t) { return (int)(unsigned)__builtin_bit_cast(u64, t + magic); }
+    __device__ __forceinline__ double scaled(float x) const { return power(exponent(x)); }
+    __device__ __forceinline__ double power(double t) const {
         constexpr double a1 = 0.69314718055994530942 / kTable, a2 = a1 * a1 / 2, a3 = a1 * a1 * a1 / 6;
-        double t = ((double)x - top) * c;
-        t = fmax(t, -1000.0 * kTable);  // also of NaN: nothing
-        const double y = t + magic, r = t - (y - magic);
-        const int k = (int)(unsigned)__builtin_bit_cast(u64, y);
+        const int k = whole(t);
+        const double r = t - ((t + magic) - magic);
         const double q = fma(fma(fma(a3, r, a2), r, a1), r, 1.0);
         const u64 w = __builtin_bit_cast(u64, table[k & (kTable - 1)] * q);
         return __builtin_bit_cast(double, w + ((u64)(unsigned)(((k >> 10) + kOne) << 20) << 32));
@@ -275,6 +287,7 @@ struct Shared {
     unsigned keys[kList];
     int at[kList];
     float tops[kTiles];   // largest value of each tile
+    float refs[kTiles];   // what its weight of the first pass is relative to
     u64 sum[kTiles];      // its weight (a double), then that of what is kept of it
     int ties[kTiles];     // slow way: its logits at the border
     float wtop[2][kWaves];
@@ -442,7 +455,7 @@ __device__ __forceinline__ void draw_from_tiles(Shared& s, const Row<T>& row, co
     double total;
     const double before = block_exclusive(mine, s.wave_d, &total), at = (double)c.u * total;
     // the last tile that begins at or before the place: one with weight, since sums only grow there
-    if (mine > 0 && before <= at) atomicMax(&s.index, (int)threadIdx.x);
+    if (const u64 m = __ballot(mine > 0 && before <= at); m && lane == 63 - __builtin_clzll(m)) atomicMax(&s.index, (int)threadIdx.x);
     __syncthreads();
     const int tile = s.index, j = tile / kWaves;
     if ((int)threadIdx.x == tile) s.wave_d[0] = at - before;
@@ -514,47 +527,58 @@ __device__ __forceinline__ void draw_infinite(Shared& s, const Row<T>& row, floa
 }
 
 // ------------------------------------------------------------------ the list
-// Logits with `lo` <= bin <= `hi` go into the list, and the weights of those above
-// become their tiles' sums; false if there are too many.
-template <typename T, class B>
-__device__ __forceinline__ bool gather(Shared& s, const Row<T>& row, const Weight& w, B&& bin_of, int lo, int hi, float floor_x, List& list) {
+// The least value for which `is` holds, as it does for `top` and all values from
+// the one asked for up to it: 64 keys at a time.
+template <class P>
+__device__ __forceinline__ float least_value(float top, P&& is) {
+    unsigned no = key_of(neg_inf()), yes = key_of(top);  // not a logit with weight, and one for which it holds
+    while (yes - no > 1) {
+        const unsigned step = (yes - no - 1) / 64 + 1, left = (yes - no - 1) / step;  // so many keys lie between
+        const unsigned lane = threadIdx.x & 63, key = no + (lane + 1) * step;
+        const u64 m = __ballot(lane < left && is(value_of(key)));
+        const int first = m ? __builtin_ctzll(m) : (int)left;
+        if (m) yes = no + (first + 1) * step;
+        no += first * step;
+    }
+    return value_of(yes);
+}
+
+// Logits from `lo` on and below `hi` go into the list, and the weights of those from
+// `hi` on become their tiles' sums; false if there are too many.
+template <typename T>
+__device__ __forceinline__ bool gather(Shared& s, const Row<T>& row, const Weight& w, float lo, float hi, List& list) {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     if (threadIdx.x == 0) s.index = 0;
     if (threadIdx.x < kTiles) s.sum[threadIdx.x] = 0;
     __syncthreads();
-    row.each([&](float x) { return x >= floor_x && bin_of(x) >= lo; }, [&](int j, const float (&x)[E]) {
-        unsigned in = 0;
-        bool more = false;
-        u64 sum = 0;
+    row.each([&](float x) { return x >= lo; }, [&](int j, const float (&x)[E]) {
+        bool any = false;
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-            const int b = bin_of(x[e]);
-            const bool ok = x[e] >= floor_x && x[e] != neg_inf();
-            in |= (unsigned)(ok && b >= lo && b <= hi) << e;
-            const bool above = ok && b > hi;
-            if (__ballot(above)) {
-                more = true;
+        for (int e = 0; e < E; ++e) any |= x[e] >= hi;
+        if (__ballot(any)) {
+            u64 sum = 0;
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
                 const u64 v = w.fixed(x[e]);
-                sum += above ? v : 0;
+                sum += x[e] >= hi ? v : 0;
             }
+            sum = wave_inclusive(sum);
+            if (lane == 63) s.sum[j * kWaves + wave] = sum;
         }
-        if (more) {
-            sum = last_lane(wave_inclusive(sum));
-            if (lane == 0) s.sum[j * kWaves + wave] = sum;
-        }
-        const int mine = __popc(in), incl = wave_inclusive(mine), all = last_lane(incl);
+        int mine = 0;
+#pragma unroll
+        for (int e = 0; e < E; ++e) mine += x[e] >= lo && x[e] < hi;
+        const int incl = wave_inclusive(mine), all = last_lane(incl);
         if (all == 0) return;
         int base = 0;
         if (lane == 0) base = atomicAdd(&s.index, all);
         int to = __builtin_amdgcn_readfirstlane(base) + incl - mine;
+        if (to + mine > kList) return;
 #pragma unroll
         for (int e = 0; e < E; ++e)
-            if (in >> e & 1) {
-                if (to < kList) {
-                    s.keys[to] = key_of(x[e]);
-                    s.at[to] = row.index(j, e);
-                }
-                ++to;
+            if (x[e] >= lo && x[e] < hi) {
+                s.keys[to] = key_of(x[e]);
+                s.at[to++] = row.index(j, e);
             }
     });
     __syncthreads();
@@ -672,6 +696,65 @@ __device__ __forceinline__ void draw_from_list(Shared& s, const Row<T>& row, con
     }
 }
 
+// The same for a list of up to 64 H that all that is kept is in, by one wave, H
+// logits per lane: each finds what stands before it, in the order of logits and then,
+// among what is kept, in the order of indices.  False as filter_list's.
+template <int H>
+__device__ __forceinline__ bool draw_from_few(const List& list, const Weight& w, const Settings& c, u64 goal, bool short_list,
+                                              const SampleArgs& a, int64_t r) {
+    const int lane = threadIdx.x & 63;
+    const Weigh weigh(w, c.min_p);
+    unsigned key[H];
+    int at[H], rank[H] = {};
+    u64 v[H], before[H] = {}, all = 0;
+#pragma unroll
+    for (int h = 0; h < H; ++h) {
+        const int i = 64 * h + lane;
+        key[h] = i < list.n ? list.keys[i] : 0;
+        at[h] = i < list.n ? list.at[i] : 0x7fffffff;
+        v[h] = i < list.n ? w.fixed(value_of(key[h])) : 0;
+    }
+    auto others = [&](auto&& f) {  // f(key, index, weight) of each
+#pragma unroll
+        for (int h = 0; h < H; ++h) {
+            const int n = list.n - 64 * h < 64 ? list.n - 64 * h : 64;
+            for (int i = 0; i < n; ++i) f(lane_of(key[h], i), lane_of(at[h], i), lane_of(v[h], i));
+        }
+    };
+    others([&](unsigned k, int p, u64 m) {
+#pragma unroll
+        for (int h = 0; h < H; ++h) {
+            const bool first = k > key[h] || (k == key[h] && p < at[h]);
+            rank[h] += first;
+            before[h] += first ? m : 0;
+        }
+    });
+#pragma unroll
+    for (int h = 0; h < H; ++h) all += !c.by_k || rank[h] < c.top_k ? v[h] : 0;
+    all = last_lane(wave_inclusive(all));
+    if (goal == 0) goal = part_up(c.top_p, all);  // the list holds all that top-k keeps, or the whole row
+    if (c.by_p && all < goal && !short_list) return false;
+    u64 total = 0;
+#pragma unroll
+    for (int h = 0; h < H; ++h) {
+        const bool kept = (!c.by_k || rank[h] < c.top_k) && (!c.by_p || before[h] < goal);
+        v[h] = 64 * h + lane < list.n && kept ? weigh(value_of(key[h])) : 0;
+        total += v[h];
+        before[h] = 0;
+    }
+    total = last_lane(wave_inclusive(total));
+    bool whole;
+    const u64 to = part_of(c.u, total, &whole);
+    others([&](unsigned, int p, u64 m) {
+#pragma unroll
+        for (int h = 0; h < H; ++h) before[h] += p < at[h] ? m : 0;
+    });
+#pragma unroll
+    for (int h = 0; h < H; ++h)
+        if (before[h] <= to && to < before[h] + v[h]) answer(a, r, at[h], (double)v[h], (double)total);
+    return true;
+}
+
 // -------------------------------------------------------------- the slow way
 // The same with passes over the whole row.
 template <typename T>
@@ -692,7 +775,7 @@ __device__ __forceinline__ void draw_from_row(Shared& s, const Row<T>& row, cons
     if (c.by_p) {
         u64 goal;
         if (weight > 0) {
-            goal = (u64)ceil((double)c.top_p * weight);
+            goal = (u64)ceil((double)c.top_p * weight * (1 - 0x1p-48));
             goal += goal == 0;
         } else {
             u64 sum = 0, all;
@@ -797,18 +880,18 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(SampleArgs a) {
     c.by_k = c.top_k > 0 && c.top_k < a.V;
     c.by_p = c.top_p < 1.f;
     const bool greedy = !(c.T > 0.f), small = a.V <= kList;  // a small row is a list
-    const bool counts = !greedy && !small && (c.by_k || c.by_p);
+    const bool maxima = !greedy && !small && c.by_k && c.top_k <= kByMaxima;
+    const bool counts = !greedy && !small && !maxima && (c.by_k || c.by_p);
     const bool weights = !greedy && !c.by_k && (c.by_p ? !small : !(c.min_p > 0.f));
 
     if (!greedy) s.table[t] = exp2((double)t / kTable);
     if (t < kTiles) s.tops[t] = neg_inf();
     unsigned* const count = (unsigned*)s.hist;
     clear_bins(s);
-    float top = neg_inf(), ref = 0.f;
-    const float per_bin = fminf((float)kFine / c.T, 1e30f);
-    auto place_of = [&](float x) { return fminf(fmaxf((x - ref) * per_bin, -1e9f), 1e9f); };
-    auto bin_of = [&](float x) { return (int)floorf(place_of(x)); };
-    int newest = 0;  // the bin of the largest value so far; bins count from the first such
+    float best = neg_inf();            // of this thread
+    float top = neg_inf(), ref = 0.f;  // bins count from ref, a value that was the largest
+    int newest = 0;                    // the bin of the largest so far
+    bool lost = false;                 // bins fell out that may matter
 #pragma unroll 1
     for (int j = 0; j < row.steps; ++j) {
         typename Row<T>::Raw more = raw;
@@ -819,37 +902,54 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(SampleArgs a) {
         float m = x[0];
 #pragma unroll
         for (int e = 1; e < E; ++e) m = fmaxf(m, x[e]);
+        best = fmaxf(best, m);
         m = wave_max(m);
-        if (lane == 0) s.tops[j * kWaves + wave] = m;
+        const int tile = j * kWaves + wave;
+        if (lane == 0) s.tops[tile] = m;
+        float by = m;  // what the tile's weight is relative to
+        if (counts) {
+            const float old = top;
+            if (lane == 0) s.wtop[j & 1][wave] = m;
+            __syncthreads();
+            top = fmaxf(top, wave_max(s.wtop[j & 1][lane % kWaves]));
+            if (top > old) {
+                const double exponent = Weight(c.T, ref, s.table).exponent(top);
+                int now = 0, n = kBins;
+                if (old != neg_inf() && exponent < (newest + kBins) * (double)(1 << kBinShift) && newest < kMostBin) {
+                    now = Weight::whole(exponent) >> kBinShift;
+                    n = now - newest;
+                } else {  // all bins fall out
+                    lost = lost || newest >= kMostBin;
+                    ref = top;
+                }
+                // bins come in at the top, in the place of those that fall out at the bottom
+                for (int i = t; i < n; i += kThreads) count[(now - i) & (kBins - 1)] = 0;
+                newest = now;
+                __syncthreads();
+            }
+            by = ref;
+        }
+        if (m == neg_inf() || !(counts || weights)) {
+            if (lane == 0) s.sum[tile] = 0, s.refs[tile] = m;
+            continue;
+        }
+        const Weight w(c.T, by, s.table);
+        double exponent[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) exponent[e] = w.exponent(x[e]);
         if (weights) {
             double sum = 0;
-            if (m != neg_inf()) {
-                const Weight w(c.T, m, s.table);
 #pragma unroll
-                for (int e = 0; e < E; ++e) sum += w.scaled(x[e]);
-            }
+            for (int e = 0; e < E; ++e) sum += w.power(exponent[e]);
             sum = wave_inclusive(sum);
-            if (lane == 63) s.sum[j * kWaves + wave] = __builtin_bit_cast(u64, sum);
+            if (lane == 63) s.sum[tile] = __builtin_bit_cast(u64, sum), s.refs[tile] = by;
         }
-        if (!counts) continue;
-        const float old = top;
-        if (lane == 0) s.wtop[j & 1][wave] = m;
-        __syncthreads();
-        top = fmaxf(top, wave_max(s.wtop[j & 1][lane % kWaves]));
-        if (top == neg_inf()) continue;
-        if (old == neg_inf()) {
-            ref = top;
-            newest = bin_of(top);
-        } else if (top > old) {  // bins come in at the top, in the place of those that fall out at the bottom
-            const int now = bin_of(top), n = now - newest < kBins ? now - newest : kBins;
-            for (int i = t; i < n; i += kThreads) count[(now - i) & (kBins - 1)] = 0;
-            newest = now;
-            __syncthreads();
-        }
+        if (counts) {
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-            const int b = bin_of(x[e]);
-            if (x[e] > neg_inf() && newest - b < kBins - 1) atomicAdd(&count[b & (kBins - 1)], 1u);
+            for (int e = 0; e < E; ++e) {
+                const int b = Weight::whole(exponent[e]) >> kBinShift;
+                if (x[e] > neg_inf() && newest - b < kBins - 1) atomicAdd(&count[b & (kBins - 1)], 1u);
+            }
         }
     }
     __syncthreads();
@@ -886,7 +986,7 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(SampleArgs a) {
     double weight = 0;  // of the row, in 2^-44
     if (weights) {      // a tile's, relative to the row's maximum; 0 where no value of it has any
         const float m = t < kTiles ? s.tops[t] : neg_inf();
-        const double mine = w.fixed(m) ? __builtin_bit_cast(double, s.sum[t]) * (w.scaled(m) * 0x1p-44) : 0.0;
+        const double mine = w.fixed(m) ? __builtin_bit_cast(double, s.sum[t]) * (w.scaled(s.refs[t]) * 0x1p-44) : 0.0;
         if (!c.by_p) {
             draw_from_tiles(s, row, w, mine, c, a, r);
             return;
@@ -896,13 +996,26 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(SampleArgs a) {
 
     // the list need not reach below min-p, unless top-p takes a weight from it
     const bool part = c.min_p > 0.f && !(c.by_p && (c.by_k || small));
-    const float floor_x = part ? top + c.T * (logf(c.min_p) - 0.001f) : neg_inf();
-    int lo = -0x7fffffff, hi = 0x7fffffff;
+    const float floor_x = part ? top + c.T * (0.69314718f * __builtin_amdgcn_logf(c.min_p) - 0.001f) : neg_inf();
+    float lo = floor_x, hi = -neg_inf();
     u64 n_above = 0, goal = 0;
     bool fits = true, short_list = part;  // the list ends at min-p
+    if (maxima) {
+        // bins of 1/64 of the temperature; the last takes all that has no weight
+        const float per_bin = fminf(64.f / c.T, 1e30f);
+        auto bin_of = [&](float x) { return (int)fminf((top - x) * per_bin, (float)(kBins - 1)); };
+        add(s.hist, bin_of(best), 1, true);
+        int bin;
+        u64 before, in;
+        pick(s, (u64)c.top_k, &bin, &before, &in);
+        bin = bin < kBins - 1 ? bin : kBins - 2;
+        lo = fmaxf(lo, least_value(top, [&](float x) { return bin_of(x) <= bin; }));
+    }
     if (counts) {
+        const Weight by(c.T, ref, s.table);
+        const int floor_bin = Weight::whole(by.exponent(floor_x)) >> kBinShift;
         // the two bins of this thread, from the newest down, and what their counts weigh at least
-        const int i = 2 * t, end = (part && newest - bin_of(floor_x) < kWhole ? newest - bin_of(floor_x) + 1 : kWhole) / 2;
+        const int i = 2 * t, end = (part && newest - floor_bin < kWhole ? newest - floor_bin + 1 : kWhole) / 2;
         const unsigned n0 = i < kWhole ? count[(newest - i) & (kBins - 1)] : 0, n1 = i + 1 < kWhole ? count[(newest - i - 1) & (kBins - 1)] : 0;
         u64 all;
         const u64 before = block_exclusive((u64)(n0 + n1), s.wave, &all), upto = before + n0 + n1;
@@ -910,46 +1023,61 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(SampleArgs a) {
         if (c.by_k) {
             may = must = upto >= (u64)c.top_k;
         } else {
-            const float step = exp2f(-1.44269504f / kFine), deep = place_of(top) - (float)(newest - i);
-            const float w0 = exp2f(-1.44269504f / kFine * deep), mine = (float)n0 * w0 + (float)n1 * (w0 * step);
+            // exponents are rounded: the least of a bin's is half a step below its first
+            const float deep = (float)((double)((newest - i) * 16) - 0.5 - by.exponent(top)) * (1.f / kTable);
+            const float w0 = __builtin_amdgcn_exp2f(deep), mine = (float)n0 * w0 + (float)n1 * (w0 * 0.98922819f);  // 2^(-1/64)
             float sum;
             const float least = block_exclusive(mine, s.wave_f, &sum) + mine;
-            goal = (u64)ceil((double)c.top_p * weight);
+            goal = (u64)ceil((double)c.top_p * weight * (1 - 0x1p-48));  // what rounding added to the weight takes no logit in
             goal += goal == 0;
             const float want = (float)goal * 0x1p-44f;
-            must = least >= want * 1.004f;
-            may = least * 1.012f >= want;  // e^(1/kFine), and as much for rounding on either side
+            must = least >= want * 1.0005f;
+            may = least * 1.0115f >= want;  // 2^(1/64), and as much for rounding on either side
         }
         // the border's pairs of bins: from the first that may hold it to the first that it cannot lie below
         if (t == 0) s.index = s.last = kThreads;
         __syncthreads();
-        if (may) atomicMin(&s.index, t);
-        if (must) atomicMin(&s.last, t);
+        if (const u64 m = __ballot(may); m && lane == __builtin_ctzll(m)) atomicMin(&s.index, t);
+        if (const u64 m = __ballot(must); m && lane == __builtin_ctzll(m)) atomicMin(&s.last, t);
         __syncthreads();
         const int first = s.index < end ? s.index : end, last = s.last < end ? s.last : end;
-        fits = s.last < kWhole / 2 || (part && end < kWhole / 2);
+        fits = !lost && (s.last < kWhole / 2 || (part && end < kWhole / 2));
         short_list = part && last == end;
         if (t == last) s.picked[0] = upto;
         if (t == first) s.picked[1] = before;
         __syncthreads();
-        lo = newest - 2 * last - 1;
+        auto from_bin = [&](int b) {
+            return least_value(top, [&](float x) { return Weight::whole(by.exponent(x)) >= b * (1 << kBinShift); });
+        };
+        lo = fmaxf(lo, from_bin(newest - 2 * last - 1));
         const u64 most = s.picked[0], skipped = s.picked[1];
         if (most > (u64)kList) {  // only the bins themselves
-            fits = fits && most - skipped <= (u64)kList && !(c.by_k && c.by_p);
-            hi = newest - 2 * first;
-            if (part && hi <= bin_of(floor_x)) hi = bin_of(floor_x) + 1;
+            const int first_bin = newest - 2 * first;
+            if (first > 0) hi = from_bin(first_bin + 1);
             n_above = skipped;
-            if (part && hi != newest - 2 * first) fits = false;
+            fits = fits && most - skipped <= (u64)kList && !(c.by_k && c.by_p) && !(part && first_bin <= floor_bin);
         }
         __syncthreads();
     }
+    lo = fmaxf(lo, -3.402823466e38f);  // not -infinity
     List list;
-    Kept kept;
-    bool all_ties;
-    if (fits && gather(s, row, w, bin_of, lo, hi, floor_x, list) &&
-        filter_list(s, list, w, top, c, n_above, goal, short_list, kept, &all_ties)) {
-        draw_from_list(s, row, list, w, c, kept, all_ties, a, r);
-        return;
+    if (fits && gather(s, row, w, lo, hi, list)) {
+        if (list.n <= kOneWave && hi == -neg_inf()) {
+            if (wave == 0) {
+                const bool ok = list.n <= 64 ? draw_from_few<1>(list, w, c, goal, short_list, a, r)
+                                             : draw_from_few<2>(list, w, c, goal, short_list, a, r);
+                if (t == 0) s.bin = ok;
+            }
+            __syncthreads();
+            if (s.bin) return;
+        } else {
+            Kept kept;
+            bool all_ties;
+            if (filter_list(s, list, w, top, c, n_above, goal, short_list, kept, &all_ties)) {
+                draw_from_list(s, row, list, w, c, kept, all_ties, a, r);
+                return;
+            }
+        }
     }
     __syncthreads();
     draw_from_row(s, row, w, top, c, weight, a, r);
