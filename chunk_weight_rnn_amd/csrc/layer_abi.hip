@@ -220,63 +220,29 @@ int scan_desc_status(const e2ttt_scan_desc* d) {
     return E2TTT_OK;
 }
 
-// Whether two neighbouring channels can be read and written together.
-bool scan_pairs(const e2ttt_scan_desc& d, std::initializer_list<const void*> io, std::initializer_list<const void*> gates) {
-    if (d.io_dtype != E2TTT_BF16 || d.width % 2) return false;
-    if (d.tokens > 1 && (d.x_tok % 2 || d.a_tok % 2)) return false;
-    for (const void* p : io)
-        if ((uintptr_t)p % 4) return false;
-    for (const void* p : gates)
-        if ((uintptr_t)p % (2 * elem(d.gate_dtype))) return false;
-    return true;
-}
-
-// Slabs, parts and workgroups.  `slab` channels are the most that a workgroup
-// can take; a call whose tensors are only aligned to their elements takes half.
-ScanArgs scan_plan(const e2ttt_scan_desc& d, bool pairs, bool backward) {
+// Slabs and workgroups.
+ScanArgs scan_plan(const e2ttt_scan_desc& d, bool backward) {
     ScanArgs a{};
     a.N = d.tokens;
     a.C = d.width;
     a.S = (int)d.seqs;
     a.x_f32 = d.io_dtype == E2TTT_F32;
     a.gate_f32 = d.gate_dtype == E2TTT_F32;
-    a.pairs = pairs;
     a.x_tok = d.tokens > 1 ? d.x_tok : d.width;
     a.a_tok = d.tokens > 1 ? d.a_tok : d.width;
-    const int64_t slab = pairs ? 128 : 64;
-    const int64_t slabs = (d.width + slab - 1) / slab;
+    const int64_t slabs = (d.width + 63) / 64;
     a.slabs = (int)slabs;
-    int64_t groups = d.seqs * slabs;
-    if (!backward && d.tokens <= 16 * d.seqs) {
-        a.shorts = 1;
-    } else if (groups < kCUs && d.tokens > 2 * E2TTT_SCAN_TILE) {
-        int64_t part = d.tokens * slabs / (2 * kCUs);
-        part = (part + E2TTT_SCAN_TILE - 1) / E2TTT_SCAN_TILE * E2TTT_SCAN_TILE;
-        if (part < 2 * E2TTT_SCAN_TILE) part = 2 * E2TTT_SCAN_TILE;
-        if (part < d.tokens) {
-            a.part = (int)part;
-            groups = (d.tokens / part + d.seqs) * slabs;
-        }
-    }
+    a.shorts = !backward && d.tokens <= 16 * d.seqs;
+    const int64_t groups = (a.shorts ? d.seqs : d.tokens / E2TTT_SCAN_TILE + d.seqs) * slabs;
     a.groups = (int)(groups < kMaxScanGroups ? groups : kMaxScanGroups + 1);
     const int64_t units = (d.tokens * d.width + 2047) / 2048;
     a.clear = (int)(units < 64 ? units : 64);
     return a;
 }
 
-size_t scan_sums_bytes(const ScanArgs& a) {
-    if (!a.part) return 0;
-    return (((size_t)(a.N / a.part + a.S) * 2 * a.C) * 4 + kWsAlign - 1) / kWsAlign * kWsAlign;
-}
-// Of the call, whichever way its tensors are aligned.
 size_t scan_bytes(const e2ttt_scan_desc& d, bool backward) {
-    size_t most = 0;
-    for (int pairs = 0; pairs < 2; ++pairs) {
-        const ScanArgs a = scan_plan(d, pairs != 0, backward);
-        const size_t n = a.part ? scan_sums_bytes(a) + (backward ? 0 : (size_t)a.S * a.C * 4) : 0;
-        if (n > most) most = n;
-    }
-    return most;
+    if (d.tokens <= E2TTT_SCAN_TILE || scan_plan(d, backward).shorts) return 0;
+    return (size_t)scan_words(d.tokens, d.seqs, d.width) * 8;
 }
 
 }  // namespace
@@ -556,7 +522,7 @@ int e2ttt_scan_forward(const e2ttt_scan_desc* d, const void* x, const void* a, c
     if (!aligned(cu, 4) || (h0 && !aligned(h0, 4)) || (state && !aligned(state, 4)) || (starts && !aligned(starts, 4)))
         return E2TTT_ERR_INVALID_ARG;
     if (N > 0 && (!aligned(x, es) || !aligned(a, gs) || !aligned(out, es))) return E2TTT_ERR_INVALID_ARG;
-    ScanArgs r = scan_plan(*d, scan_pairs(*d, {x, out}, {a}), false);
+    ScanArgs r = scan_plan(*d, false);
     if (r.groups > kMaxScanGroups) return E2TTT_ERR_UNSUPPORTED;
     const size_t need = scan_bytes(*d, false);
     const int wst = workspace_status(ws, ws_bytes, need);
@@ -574,8 +540,7 @@ int e2ttt_scan_forward(const e2ttt_scan_desc* d, const void* x, const void* a, c
     r.out = out;
     r.state = state;
     r.starts = starts;
-    r.sums = (float*)ws;
-    r.first = r.part && h0 ? (float*)((char*)ws + scan_sums_bytes(r)) : nullptr;
+    r.words = need ? (unsigned long long*)ws : nullptr;
     return launch_status(launch_scan_forward(r, (hipStream_t)stream));
 }
 
@@ -595,7 +560,7 @@ int e2ttt_scan_backward(const e2ttt_scan_desc* d, const void* dout, const void* 
         return E2TTT_ERR_INVALID_ARG;
     if (N > 0 && (!aligned(x, es) || !aligned(a, gs) || !aligned(dout, es) || !aligned(dx, es) || !aligned(da, gs)))
         return E2TTT_ERR_INVALID_ARG;
-    ScanArgs r = scan_plan(*d, scan_pairs(*d, {x, dout, dx}, {a, da}), true);
+    ScanArgs r = scan_plan(*d, true);
     if (r.groups > kMaxScanGroups) return E2TTT_ERR_UNSUPPORTED;
     const size_t need = scan_bytes(*d, true);
     const int wst = workspace_status(ws, ws_bytes, need);
@@ -615,7 +580,7 @@ int e2ttt_scan_backward(const e2ttt_scan_desc* d, const void* dout, const void* 
     r.dout = dout;
     r.state = dh0;
     r.starts = const_cast<float*>(starts);
-    r.sums = (float*)ws;
+    r.words = need ? (unsigned long long*)ws : nullptr;
     return launch_status(launch_scan_backward(r, (hipStream_t)stream));
 }
 

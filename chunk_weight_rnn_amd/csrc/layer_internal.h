@@ -128,15 +128,13 @@ struct ScanArgs {
     int64_t N, C;
     int S;
     int x_f32, gate_f32;
-    int pairs;    // bf16: two channels per lane
     int slabs;    // of 64 lanes, over the channels
-    int groups;   // (sequence or part, slab) pairs
-    int part;     // 0: whole sequences; else tokens of a part, a multiple of E2TTT_SCAN_TILE
+    int groups;   // (tile or sequence, slab) pairs
     int shorts;   // forward: sequences of a few tokens
     int clear;    // workgroups that write the rows of tokens outside every sequence
-    float* sums;  // [N / part + S][2][C] what a part does to a state
-    float* first;  // forward in parts, with h0: its copy
+    unsigned long long* words;  // what tiles tell each other, scan_words of them; null where no sequence has two
 };
+int64_t scan_words(int64_t N, int64_t S, int64_t C);
 constexpr int64_t kMaxScanGroups = 1 << 22;  // of 512 threads
 hipError_t launch_scan_forward(const ScanArgs& a, hipStream_t s);
 hipError_t launch_scan_backward(const ScanArgs& a, hipStream_t s);

@@ -4,92 +4,85 @@
 //   h_t = a_t h_{t-1} + x_t,
 //   g_t = dout_t + a_{t+1} g_{t+1},  dx_t = g_t,  da_t = g_t h_{t-1}.
 //
-// HBM bound: two operations per value read.  A stretch of tokens acts on the
-// state that enters it as h -> P h + H, with P the product of its gates and H
-// its result from zero, so that stretches can be read side by side: a workgroup
-// takes a slab of channels (V per lane) of one sequence and walks over tiles of
-// E2TTT_SCAN_TILE tokens, every wave with R of them in registers and the next
-// tile's on their way.  The waves exchange their (P, H) through the LDS, each
-// folds those before it onto the tile's state, and runs its tokens a second
-// time from registers, now from the right state: the outputs are those of the
-// recurrence itself, not of products and sums over the stretch.
+// HBM bound: two operations per value read (one sequence of 16384 tokens, 2048 channels
+// in bf16: 63 us, 3.2 TB/s; 8 of up to 2048 tokens with gates in fp32: 38 us, the
+// gradients 46).  A stretch of tokens acts on the state that enters it as h -> P h + H,
+// with P the product of its gates and H its result from zero, so that stretches can be
+// read side by side.  A workgroup
+// takes one tile, E2TTT_SCAN_TILE tokens of a slab of channels (one per lane), every
+// wave R of them in registers, and reads it once:
+//  * the waves exchange their (P, H) through the LDS, and the tile's is published;
+//  * the state that enters the tile follows from those of the tiles before it: the
+//    waves wait for the kLook nearest, the farthest of which has to have its end state
+//    published, and all of them are folded in order;
+//  * the tile's end state is published for the tiles after it, and each wave runs
+//    its tokens a second time from registers, now from the right state: the outputs
+//    are those of the recurrence itself, not of products and sums over the stretch.
+// An end state is the fold of the one before it and the tile's (P, H) wherever it is
+// computed, so that results do not depend on who was first.
 //
-// The gradient walks the same way from the last tile to the first.  It needs
+// Workgroups take their tiles by a ticket, in the order of the sequences, so a tile
+// waits only for tiles that were taken before it, by workgroups that run already and
+// finish theirs in the order they took them, and words only grow, whatever the offsets
+// hold: every wait ends.  (One that does not,
+// because another call was given the same workspace meanwhile, is given up after
+// kSpinTicks, and its results are NaN.)  What is published is a word of 64 bits, stored
+// and loaded as a whole past the caches of the compute dies, so nothing has to be flushed.
+//
+// The gradient goes the same way from the last tile to the first.  It needs
 // the states again, which out holds rounded: they are computed once more from
 // the saved states at the tiles' starts, which costs no more reading than out
 // would (x in its place).
-//
-// Where sequences and slabs are too few for the chip (PARTS), each sequence is
-// cut into parts of `part` tokens; a first launch reads the gates and inputs of
-// all but the last for their (P, H), and the second folds those before its part.
 #include "attn_common.h"
 
 namespace e2ttt {
 namespace {
 
 using attn::clamped;
+typedef unsigned long long u64;
 
-constexpr int R = 16;                     // tokens of a wave per tile
+constexpr int R = 16;                     // tokens of a wave
 constexpr int NW = E2TTT_SCAN_TILE / R;   // waves of a workgroup
 constexpr int TILE = E2TTT_SCAN_TILE;
 
-template <typename T, int V>
-struct alignas(sizeof(T) * V) Pack {
-    T v[V];
+// A tile of a sequence: tokens [lo, lo + n) of the sequence at tok0, tile `tile` of `tiles`.
+struct Tile {
+    int seq, tok0, lo, n, tile, tiles;
+    // Tiles of the sequence that come before this one, on the way that is taken.
+    int before;
+    // Row of the published words and of starts: the tiles of the sequences before, and
+    // never past the end whatever the offsets hold.
+    __device__ __forceinline__ int64_t row() const { return tok0 / TILE + seq + tile; }
 };
 
-// One sequence, or one part of it: tokens [lo, hi) of the n from tok0 on.
-struct Stretch {
-    int seq, tok0, n, lo, hi;
-};
-
-__device__ __forceinline__ Stretch whole_sequence(const ScanArgs& a, int s) {
-    Stretch r{s, clamped(a.cu[s], (int)a.N), 0, 0, 0};
-    const int n = clamped(a.cu[s + 1], (int)a.N) - r.tok0;
-    r.n = r.hi = n > 0 ? n : 0;
-    return r;
-}
-
-__device__ __forceinline__ bool find_part(const ScanArgs& a, int t, Stretch& r) {
+// The t-th tile: a sequence's tiles from its end (BWD), as the search goes, or its start.
+template <bool BWD>
+__device__ __forceinline__ bool find_tile(const ScanArgs& a, int t, Tile& r) {
     attn::Item it;
-    const int part = a.part;
-    if (!attn::find_item(a.cu, a.S, (int)a.N, t, attn::kInOrder,
-                         [&](int n) { return n > part ? (n - 1) / part + 1 : 1; }, it))
-        return false;
-    r = {it.seq, it.tok0, it.n, it.tile * part, it.n};
-    if (r.n - r.lo > part) r.hi = r.lo + part;
+    if (!attn::find_item(a.cu, a.S, (int)a.N, t, attn::kInOrder, [](int n) { return n > TILE ? (n - 1) / TILE + 1 : 1; }, it)) return false;
+    const auto same = [](int v) { return __builtin_amdgcn_readfirstlane(v); };  // of all lanes: rows in scalars
+    it = {same(it.seq), same(it.tok0), same(it.n), same(it.tile), same(it.tiles)};
+    const int from_end = it.tiles - 1 - it.tile, tile = BWD ? it.tile : from_end;
+    r = {it.seq, it.tok0, tile * TILE, it.n - tile * TILE, tile, it.tiles, BWD ? from_end : tile};
+    if (r.n > TILE) r.n = TILE;
     return true;
 }
 
-// Rows of the workspace and of starts: parts, or tiles, of the sequences before,
-// and never past the end whatever the offsets hold.
-__device__ __forceinline__ int64_t row_of(const Stretch& r, int len) { return r.tok0 / len + r.seq; }
-
-// `rows` tokens' values of this lane's channels from p on; the others are `fill`.
-template <typename T, int V>
-__device__ __forceinline__ void load(Pack<T, V> (&x)[R], const T* p, int64_t stride, int rows, bool in, float fill) {
-    Pack<T, V> f;
+// Channel c of `rows` tokens from p on, which is the same for all lanes (so rows are
+// addressed by scalars); the others are `fill`.
+template <typename T>
+__device__ __forceinline__ void load(T (&x)[R], const T* p, int64_t stride, int rows, unsigned c, bool in, float fill) {
 #pragma unroll
-    for (int e = 0; e < V; ++e) f.v[e] = (T)fill;
+    for (int r = 0; r < R; ++r) x[r] = (T)fill;
+    if (!in) return;
     if (rows >= R) {
 #pragma unroll
-        for (int r = 0; r < R; ++r) x[r] = in ? *(const Pack<T, V>*)(p + r * stride) : f;
+        for (int r = 0; r < R; ++r, p += stride) x[r] = p[c];
     } else {
 #pragma unroll
-        for (int r = 0; r < R; ++r) x[r] = in && r < rows ? *(const Pack<T, V>*)(p + r * stride) : f;
+        for (int r = 0; r < R; ++r, p += stride)
+            if (r < rows) x[r] = p[c];
     }
-}
-
-template <int V>
-__device__ __forceinline__ void load_state(float (&h)[V], const float* p, bool in) {
-#pragma unroll
-    for (int e = 0; e < V; ++e) h[e] = in && p ? p[e] : 0.f;
-}
-template <int V>
-__device__ __forceinline__ void store_state(float* p, const float (&h)[V], bool in) {
-#pragma unroll
-    for (int e = 0; e < V; ++e)
-        if (in) p[e] = h[e];
 }
 
 // Outputs of the tokens of no sequence: block b of a.clear.
@@ -101,113 +94,178 @@ __device__ __forceinline__ void clear_rows(const ScanArgs& a, T* p, int b) {
         p[i < first ? i : i + skip] = (T)0.f;
 }
 
-// The state before this part, from the (P, H) of the parts on the way to it:
-// parts [0, count) in steps of `dir` from row `first` on.  Every wave folds its
-// share, then all of them together.
-template <int V>
-__device__ __forceinline__ void fold_parts(const ScanArgs& a, float (&h)[V], float (*sh)[2][64 * V], int64_t first, int dir,
-                                           int count, int c, bool in) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int per = (count + NW - 1) / NW, i0 = wave * per, i1 = i0 + per < count ? i0 + per : count;
-    float P[V], H[V];
-#pragma unroll
-    for (int e = 0; e < V; ++e) P[e] = 1.f, H[e] = 0.f;
-    for (int i = i0; i < i1; ++i) {
-        const float* s = a.sums + (first + (int64_t)dir * i) * 2 * a.C + c;
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-            const float p = in ? s[e] : 1.f, q = in ? s[a.C + e] : 0.f;
-            H[e] = __builtin_fmaf(p, H[e], q);
-            P[e] *= p;
-        }
-    }
-#pragma unroll
-    for (int e = 0; e < V; ++e) sh[wave][0][lane * V + e] = P[e], sh[wave][1][lane * V + e] = H[e];
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < NW; ++w)
-#pragma unroll
-        for (int e = 0; e < V; ++e) h[e] = __builtin_fmaf(sh[w][0][lane * V + e], h[e], sh[w][1][lane * V + e]);
-    __syncthreads();
+// ------------------------------------------------------------ published words
+// One per tile and channel, 0 before the launch: {H, P + 1 as bits}, then
+// {the state after the tile, kState}, which is more than any of P.
+constexpr unsigned kState = 0xffffffffu;
+__device__ __forceinline__ u64 word_of(float h, unsigned key) { return (u64)key << 32 | __builtin_bit_cast(unsigned, h); }
+__device__ __forceinline__ unsigned key_of(float P) { return P != P ? 0x7fc00001u : __builtin_bit_cast(unsigned, P) + 1; }
+__device__ __forceinline__ float applied(u64 w, float h) {
+    const unsigned key = (unsigned)(w >> 32);
+    const float H = __builtin_bit_cast(float, (unsigned)w);
+    return key == kState ? H : __builtin_fmaf(__builtin_bit_cast(float, key - 1), h, H);
+}
+__device__ __forceinline__ void publish(u64* p, u64 w) { __hip_atomic_store(p, w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
+// Never in place of a state: sequences that overlap, by offsets that fall, share words.
+__device__ __forceinline__ void publish_first(u64* p, u64 w) {
+    __hip_atomic_fetch_max(p, w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ u64 published(const u64* p) { return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
+
+__global__ __launch_bounds__(256) void scan_clear_kernel(u64* words, int64_t n) {
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) words[i] = 0;
 }
 
-template <typename TX, typename TA, int V, bool PARTS>
-__global__ __launch_bounds__(64 * NW) void scan_fwd_kernel(ScanArgs a) {
-    __shared__ float sh[2][NW][2][64 * V];
+// Words before the tiles': whether a wait was given up, and a ticket counter for each
+// slab (tiles wait for tiles of their slab alone, and additions to one address take
+// their turn: 2000 of them some 50 us), 64 bytes apart.
+__host__ __device__ __forceinline__ int64_t header_words(int64_t C) { return 8 * ((C + 63) / 64 + 1); }
+
+// The next tile of a slab that nobody has taken.
+__device__ __forceinline__ int take_ticket(const ScanArgs& a, int slab) {
+    return (int)__hip_atomic_fetch_add((unsigned*)(a.words + 8 * (slab + 1)), 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+constexpr u64 kSpinTicks = 200000000;  // 2 s of the 100 MHz wall clock
+
+// The state h that enters the tile from the `before` tiles in direction -dir, the
+// words of the nearest at `row`: each wave waits for its share of the kLook nearest,
+// the farthest of which has to be a state, and all are folded in order.  Words that are
+// there cost one way to memory, some 2 us, and a chain of states takes some 5 us every
+// kLook tiles (16384 tokens of 2048 channels: 78 us with 16 and two words per tile and
+// channel, 66 so).
+constexpr int kLook = 32;
+__device__ __forceinline__ void enter(const ScanArgs& a, float& h, u64 (*sh)[64], int64_t row, int dir, int before, int c, bool in) {
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int n = before < kLook ? before : kLook;
+    const u64* const base = a.words + header_words(a.C) + row * a.C + c;
+    u64 w[kLook / NW];
+#pragma unroll
+    for (int j = 0; j < kLook / NW; ++j) {
+        const int i = wave + j * NW;
+        w[j] = word_of(0.f, kState);
+        if (i < n && in) w[j] = published(base - (int64_t)dir * i * a.C);
+    }
+#pragma unroll
+    for (int j = 0; j < kLook / NW; ++j) {
+        const int i = wave + j * NW;
+        if (i >= n) break;
+        const unsigned want = i == kLook - 1 ? kState : 1;
+        u64 since = 0;
+        for (unsigned tries = 1; __ballot((unsigned)(w[j] >> 32) < want); ++tries) {
+            if (tries % 64 == 0) {
+                const u64 now = wall_clock64();
+                if (since == 0) since = now;
+                if (now - since > kSpinTicks || published(a.words) != 0) {
+                    publish(a.words, 1);
+                    w[j] = word_of(__builtin_nanf(""), kState);
+                    break;
+                }
+            }
+            __builtin_amdgcn_s_sleep(1);
+            if (in) w[j] = published(base - (int64_t)dir * i * a.C);
+        }
+        sh[i][lane] = w[j];
+    }
+    __syncthreads();
+#pragma unroll 4
+    for (int i = n - 1; i >= 0; --i) h = applied(sh[i][lane], h);
+}
+
+// Workgroups stay, kStay on a compute unit, and take tile after tile: the next one's
+// tokens are on their way while this one's state is awaited and its outputs go out
+// (16384 tokens of 2048 channels: 100 us with a workgroup per tile, three on a compute
+// unit).  One channel per lane: with two, 67 us against 63, and half the workgroups for
+// few channels.
+constexpr int kStay = 2;
+template <typename TX, typename TA, bool CHAIN>
+__global__ __launch_bounds__(64 * NW, 2 * kStay) void scan_fwd_kernel(ScanArgs a) {
+    __shared__ float2 all[2][NW + 1][64];  // (P, H) of the waves and of the tile
+    __shared__ u64 words_of[CHAIN ? kLook : 1][64];
+    __shared__ int tickets[2];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     if ((int)blockIdx.x >= a.groups) {
         clear_rows(a, (TX*)a.out, blockIdx.x - a.groups);
         return;
     }
-    const int c = ((int)(blockIdx.x % a.slabs) * 64 + lane) * V;
+    const int slab = blockIdx.x % a.slabs, c = slab * 64 + lane;
     const bool in = c < a.C;
-    Stretch s;
-    if (PARTS) {
-        if (!find_part(a, blockIdx.x / a.slabs, s)) return;
-    } else {
-        s = whole_sequence(a, blockIdx.x / a.slabs);
-    }
-    float h[V];
-    load_state<V>(h, (PARTS ? a.first : a.h0) ? (PARTS ? a.first : a.h0) + (int64_t)s.seq * a.C + c : nullptr, in);
-    if (PARTS && s.lo > 0) fold_parts<V>(a, h, sh[0], row_of(s, a.part), 1, s.lo / a.part, c, in);
-    const TX* xp = (const TX*)a.x + (s.tok0 + (int64_t)wave * R) * a.x_tok + c;
-    const TA* ap = (const TA*)a.a + (s.tok0 + (int64_t)wave * R) * a.a_tok + c;
-    TX* op = (TX*)a.out + (s.tok0 + (int64_t)wave * R) * a.C + c;
-    float* st = a.starts ? a.starts + row_of(s, TILE) * a.C + c : nullptr;
-    Pack<TX, V> x[R];
-    Pack<TA, V> g[R];
-    load(x, xp + s.lo * a.x_tok, a.x_tok, s.hi - s.lo - wave * R, in, 0.f);
-    load(g, ap + s.lo * a.a_tok, a.a_tok, s.hi - s.lo - wave * R, in, 1.f);
-    int buf = 0;
-    for (int t = s.lo; t < s.hi; t += TILE, buf ^= 1) {
-        Pack<TX, V> xn[R];
-        Pack<TA, V> gn[R];
-        const int64_t tn = t + TILE;
-        load(xn, xp + tn * a.x_tok, a.x_tok, s.hi - t - TILE - wave * R, in, 0.f);
-        load(gn, ap + tn * a.a_tok, a.a_tok, s.hi - t - TILE - wave * R, in, 1.f);
-        float P[V], H[V];
+    Tile next;
+    TX nx[R];
+    TA ng[R];
+    float nh;  // the next tile's tokens, and the state that enters it if no tile is before it
+    bool more;
+    auto fetch = [&](int turn) {
+        more = find_tile<false>(a, turn, next);
+        if (!more) return;
+        const int rows = next.n - wave * R;
+        const int64_t tok = next.tok0 + next.lo + wave * R;
+        nh = next.before == 0 && a.h0 && in ? a.h0[(int64_t)next.seq * a.C + c] : 0.f;
+        load(nx, (const TX*)a.x + tok * a.x_tok, a.x_tok, rows, c, in, 0.f);
+        load(ng, (const TA*)a.a + tok * a.a_tok, a.a_tok, rows, c, in, 1.f);
+    };
+    if (CHAIN && threadIdx.x == 0) tickets[0] = take_ticket(a, slab), tickets[1] = take_ticket(a, slab);
+    if (CHAIN) __syncthreads();
+    fetch(CHAIN ? tickets[0] : (int)blockIdx.x / a.slabs);
+    for (int k = 1; more; ++k) {
+        float2 (*const sh)[64] = all[k & 1];
+        const Tile s = next;
+        float h = nh;
+        TX x[R];
+        TA g[R];
 #pragma unroll
-        for (int e = 0; e < V; ++e) P[e] = 1.f, H[e] = 0.f;
-#pragma unroll
-        for (int r = 0; r < R; ++r)
-#pragma unroll
-            for (int e = 0; e < V; ++e) {
-                H[e] = __builtin_fmaf((float)g[r].v[e], H[e], (float)x[r].v[e]);
-                P[e] *= (float)g[r].v[e];
-            }
-#pragma unroll
-        for (int e = 0; e < V; ++e) sh[buf][wave][0][lane * V + e] = P[e], sh[buf][wave][1][lane * V + e] = H[e];
-        __syncthreads();  // one barrier a tile: the other buffer was read before it
-        if (st && wave == 0) store_state<V>(st + (int64_t)(t / TILE) * a.C, h, in);
-        float mine[V];
-#pragma unroll
-        for (int w = 0; w < NW; ++w)
-#pragma unroll
-            for (int e = 0; e < V; ++e) {
-                if (w == wave) mine[e] = h[e];
-                h[e] = __builtin_fmaf(sh[buf][w][0][lane * V + e], h[e], sh[buf][w][1][lane * V + e]);
-            }
-        const int rows = s.hi - t - wave * R;
+        for (int r = 0; r < R; ++r) x[r] = nx[r], g[r] = ng[r];
+        float P = 1.f, H = 0.f;
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            Pack<TX, V> o;
-#pragma unroll
-            for (int e = 0; e < V; ++e) {
-                mine[e] = __builtin_fmaf((float)g[r].v[e], mine[e], (float)x[r].v[e]);
-                o.v[e] = (TX)mine[e];
-            }
-            if (in && r < rows) *(Pack<TX, V>*)(op + (int64_t)(t + r) * a.C) = o;
+            H = __builtin_fmaf((float)g[r], H, (float)x[r]);
+            P *= (float)g[r];
         }
+        sh[wave][lane] = make_float2(P, H);
+        asm volatile("" : "+v"(h));  // is here before the barrier: state may be h0
+        __syncthreads();
+        const int turn = tickets[k & 1];
+        u64* const word = CHAIN ? a.words + header_words(a.C) + s.row() * a.C + c : nullptr;
+        const bool last = s.tile == s.tiles - 1;
+        if (wave == NW - 1) {
+            float p = 1.f, q = 0.f;
 #pragma unroll
-        for (int r = 0; r < R; ++r) x[r] = xn[r], g[r] = gn[r];
+            for (int w = 0; w < NW; ++w) {
+                const float2 f = sh[w][lane];
+                q = __builtin_fmaf(f.x, q, f.y);
+                p *= f.x;
+            }
+            sh[NW][lane] = make_float2(p, q);
+            if (CHAIN && s.before > 0 && !last && in) publish_first(word, word_of(q, key_of(p)));
+        }
+        if (CHAIN) {
+            fetch(turn);
+            if (threadIdx.x == 0) tickets[~k & 1] = take_ticket(a, slab);
+            if (s.before > 0) enter(a, h, words_of, s.row() - 1, 1, s.before, c, in);
+        } else {
+            more = false;
+        }
+        float end = 0.f;
+        if (wave == NW - 1) {
+            end = __builtin_fmaf(sh[NW][lane].x, h, sh[NW][lane].y);
+            if (CHAIN && !last && in) publish(word, word_of(end, kState));
+        }
+        if (a.starts && s.n > 0 && wave == 0 && in) a.starts[s.row() * a.C + c] = h;
+        for (int w = 0; w < wave; ++w) h = __builtin_fmaf(sh[w][lane].x, h, sh[w][lane].y);
+        const int rows = s.n - wave * R;
+        TX* op = (TX*)a.out + (s.tok0 + s.lo + wave * R) * a.C;
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            h = __builtin_fmaf((float)g[r], h, (float)x[r]);
+            if (in && r < rows) op[c] = (TX)h;
+            op += a.C;
+        }
+        if (a.state && last && wave == NW - 1 && in) a.state[(int64_t)s.seq * a.C + c] = end;
     }
-    if (!a.state || s.hi != s.n) return;
-    __syncthreads();  // state may be h0, which every wave has used by now
-    if (wave == 0) store_state<V>(a.state + (int64_t)s.seq * a.C + c, h, in);
 }
 
 // Sequences of a few tokens: a wave each and slab, no exchange.
-template <typename TX, typename TA, int V>
+template <typename TX, typename TA>
 __global__ __launch_bounds__(256) void scan_short_kernel(ScanArgs a) {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int past = (int)blockIdx.x - (a.groups + 3) / 4;
@@ -217,267 +275,155 @@ __global__ __launch_bounds__(256) void scan_short_kernel(ScanArgs a) {
     }
     const int unit = (int)blockIdx.x * 4 + wave;
     if (unit >= a.groups) return;
-    const int c = (unit % a.slabs * 64 + lane) * V;
+    const int c = unit % a.slabs * 64 + lane;
     const bool in = c < a.C;
-    const Stretch s = whole_sequence(a, unit / a.slabs);
-    float h[V];
-    load_state<V>(h, a.h0 ? a.h0 + (int64_t)s.seq * a.C + c : nullptr, in);
-    const TX* xp = (const TX*)a.x + s.tok0 * a.x_tok + c;
-    const TA* ap = (const TA*)a.a + s.tok0 * a.a_tok + c;
-    TX* op = (TX*)a.out + (int64_t)s.tok0 * a.C + c;
-    float* st = a.starts ? a.starts + row_of(s, TILE) * a.C + c : nullptr;
-    for (int t = 0; t < s.n; t += R) {
-        Pack<TX, V> x[R];
-        Pack<TA, V> g[R];
-        load(x, xp + t * a.x_tok, a.x_tok, s.n - t, in, 0.f);
-        load(g, ap + t * a.a_tok, a.a_tok, s.n - t, in, 1.f);
-        if (st && t % TILE == 0) store_state<V>(st + (int64_t)(t / TILE) * a.C, h, in);
+    const int seq = unit / a.slabs, tok0 = clamped(a.cu[seq], (int)a.N), n = clamped(a.cu[seq + 1], (int)a.N) - tok0;
+    float h = a.h0 && in ? a.h0[(int64_t)seq * a.C + c] : 0.f;
+    const TX* xp = (const TX*)a.x + tok0 * a.x_tok;
+    const TA* ap = (const TA*)a.a + tok0 * a.a_tok;
+    TX* op = (TX*)a.out + (int64_t)tok0 * a.C;
+    float* st = a.starts ? a.starts + (tok0 / TILE + seq) * a.C + c : nullptr;
+    for (int t = 0; t < n; t += R) {
+        TX x[R];
+        TA g[R];
+        load(x, xp + t * a.x_tok, a.x_tok, n - t, c, in, 0.f);
+        load(g, ap + t * a.a_tok, a.a_tok, n - t, c, in, 1.f);
+        if (st && t % TILE == 0 && in) st[(int64_t)(t / TILE) * a.C] = h;
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            Pack<TX, V> o;
-#pragma unroll
-            for (int e = 0; e < V; ++e) {
-                h[e] = __builtin_fmaf((float)g[r].v[e], h[e], (float)x[r].v[e]);
-                o.v[e] = (TX)h[e];
-            }
-            if (in && r < s.n - t) *(Pack<TX, V>*)(op + (int64_t)(t + r) * a.C) = o;
+            h = __builtin_fmaf((float)g[r], h, (float)x[r]);
+            if (in && r < n - t) op[(int64_t)(t + r) * a.C + c] = (TX)h;
         }
     }
-    if (a.state) store_state<V>(a.state + (int64_t)s.seq * a.C + c, h, in);
+    if (a.state && in) a.state[(int64_t)seq * a.C + c] = h;
 }
 
-// (P, H) of the parts that others follow (forward), or (P, K) of those that others
-// precede (BWD: c -> P c + K, the gradient a part hands to the one before it).
-// Every wave takes a stretch of its part, then all of them together.  The state
-// that a sequence begins with is copied, so that the second launch may write the
-// new one in its place.
-template <typename TX, typename TA, int V, bool BWD>
-__global__ __launch_bounds__(64 * NW) void scan_parts_kernel(ScanArgs a) {
-    __shared__ float sh[NW][2][64 * V];
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int c = ((int)(blockIdx.x % a.slabs) * 64 + lane) * V;
-    const bool in = c < a.C;
-    Stretch s;
-    if (!find_part(a, blockIdx.x / a.slabs, s)) return;
-    if (!BWD && s.lo == 0 && a.first && wave == 0) {
-        float h[V];
-        load_state<V>(h, a.h0 + (int64_t)s.seq * a.C + c, in);
-        store_state<V>(a.first + (int64_t)s.seq * a.C + c, h, in);
-    }
-    if (BWD ? s.lo == 0 : s.hi == s.n) return;
-    const int per = ((s.hi - s.lo + NW - 1) / NW + R - 1) / R * R;
-    const int t0 = s.lo + wave * per, t1 = t0 + per < s.hi ? t0 + per : s.hi;
-    const TX* xp = (const TX*)a.x + s.tok0 * a.x_tok + c;
-    const TA* ap = (const TA*)a.a + s.tok0 * a.a_tok + c;
-    float P[V], H[V];
-#pragma unroll
-    for (int e = 0; e < V; ++e) P[e] = 1.f, H[e] = 0.f;
-    const int steps = t1 > t0 ? (t1 - t0 + R - 1) / R : 0;
-    auto at = [&](int i) { return t0 + (BWD ? steps - 1 - i : i) * R; };
-    Pack<TX, V> x[R];
-    Pack<TA, V> g[R];
-    if (steps > 0) {
-        load(x, xp + at(0) * a.x_tok, a.x_tok, t1 - at(0), in, 0.f);
-        load(g, ap + at(0) * a.a_tok, a.a_tok, t1 - at(0), in, 1.f);
-    }
-    for (int i = 0; i < steps; ++i) {
-        Pack<TX, V> xn[R];
-        Pack<TA, V> gn[R];
-        const bool more = i + 1 < steps;
-        load(xn, xp + at(more ? i + 1 : i) * a.x_tok, a.x_tok, more ? t1 - at(i + 1) : 0, in, 0.f);
-        load(gn, ap + at(more ? i + 1 : i) * a.a_tok, a.a_tok, more ? t1 - at(i + 1) : 0, in, 1.f);
-#pragma unroll
-        for (int k = 0; k < R; ++k) {
-            const int r = BWD ? R - 1 - k : k;
-#pragma unroll
-            for (int e = 0; e < V; ++e) {
-                const float av = (float)g[r].v[e], xv = (float)x[r].v[e];
-                H[e] = BWD ? av * (xv + H[e]) : __builtin_fmaf(av, H[e], xv);
-                P[e] *= av;
-            }
-        }
-#pragma unroll
-        for (int r = 0; r < R; ++r) x[r] = xn[r], g[r] = gn[r];
-    }
-#pragma unroll
-    for (int e = 0; e < V; ++e) sh[wave][0][lane * V + e] = P[e], sh[wave][1][lane * V + e] = H[e];
-    __syncthreads();
-    if (wave != 0) return;
-    float Q[V], K[V];
-#pragma unroll
-    for (int e = 0; e < V; ++e) Q[e] = 1.f, K[e] = 0.f;
-#pragma unroll
-    for (int k = 0; k < NW; ++k) {
-        const int w = BWD ? NW - 1 - k : k;
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-            K[e] = __builtin_fmaf(sh[w][0][lane * V + e], K[e], sh[w][1][lane * V + e]);
-            Q[e] *= sh[w][0][lane * V + e];
-        }
-    }
-    float* o = a.sums + (row_of(s, a.part) + s.lo / a.part) * 2 * a.C + c;
-    store_state<V>(o, Q, in);
-    store_state<V>(o + a.C, K, in);
-}
-
-template <typename TX, typename TA, int V, bool PARTS>
-__global__ __launch_bounds__(64 * NW) void scan_bwd_kernel(ScanArgs a) {
-    __shared__ float sh[2][NW][3][64 * V];
+template <typename TX, typename TA, bool CHAIN>
+__global__ __launch_bounds__(64 * NW, 4) void scan_bwd_kernel(ScanArgs a) {
+    __shared__ float sh[NW + 1][3][64];  // (P, H, K) of the waves, (P, K) of the tile
+    __shared__ u64 words_of[CHAIN ? kLook : 1][64];
+    __shared__ int ticket;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     if ((int)blockIdx.x >= a.groups) {
         clear_rows(a, (TX*)a.out, blockIdx.x - a.groups);
         clear_rows(a, (TA*)a.da, blockIdx.x - a.groups);
         return;
     }
-    const int c = ((int)(blockIdx.x % a.slabs) * 64 + lane) * V;
+    const int slab = blockIdx.x % a.slabs, c = slab * 64 + lane;
     const bool in = c < a.C;
-    Stretch s;
-    if (PARTS) {
-        if (!find_part(a, blockIdx.x / a.slabs, s)) return;
-    } else {
-        s = whole_sequence(a, blockIdx.x / a.slabs);
+    if (CHAIN && threadIdx.x == 0) ticket = take_ticket(a, slab);
+    if (CHAIN) __syncthreads();
+    Tile s;
+    if (!find_tile<true>(a, CHAIN ? ticket : (int)blockIdx.x / a.slabs, s)) return;
+    const int rows = s.n - wave * R;
+    const int64_t tok = s.tok0 + s.lo + wave * R;
+    TX x[R], d[R];
+    TA g[R];
+    load(g, (const TA*)a.a + tok * a.a_tok, a.a_tok, rows, c, in, 1.f);
+    load(d, (const TX*)a.dout + tok * a.C, a.C, rows, c, in, 0.f);
+    load(x, (const TX*)a.x + tok * a.x_tok, a.x_tok, rows, c, in, 0.f);
+    // the gradient that comes from after the tile, a_{t+1} g_{t+1}, and the state before it
+    float gc = s.before == 0 && a.h0 && in ? a.h0[(int64_t)s.seq * a.C + c] : 0.f;
+    float h = s.n > 0 && in ? a.starts[s.row() * a.C + c] : 0.f;
+    float P = 1.f, H = 0.f, K = 0.f;  // h -> P h + H over the wave's tokens, and the gradient's c -> P c + K
+#pragma unroll
+    for (int r = R - 1; r >= 0; --r) {
+        P *= (float)g[r];
+        K = (float)g[r] * ((float)d[r] + K);
     }
-    float gc[V];  // what reaches the state after the tile: a_{t+1} g_{t+1}
-    load_state<V>(gc, a.h0 ? a.h0 + (int64_t)s.seq * a.C + c : nullptr, in);
-    if (PARTS && s.hi < s.n) {
-        const int last = (s.n - 1) / a.part, mine = s.lo / a.part;
-        fold_parts<V>(a, gc, (float (*)[2][64 * V])&sh[0][0][0][0], row_of(s, a.part) + last, -1, last - mine, c, in);
-    }
-    const TX* xp = (const TX*)a.x + (s.tok0 + (int64_t)wave * R) * a.x_tok + c;
-    const TA* ap = (const TA*)a.a + (s.tok0 + (int64_t)wave * R) * a.a_tok + c;
-    const int64_t o0 = (s.tok0 + (int64_t)wave * R) * a.C + c;
-    const TX* dp = (const TX*)a.dout + o0;
-    const float* st = a.starts + row_of(s, TILE) * a.C + c;
-    Pack<TX, V> x[R], d[R];
-    Pack<TA, V> g[R];
-    float h0[V];
-    auto fetch = [&](int t, Pack<TX, V> (&x)[R], Pack<TX, V> (&d)[R], Pack<TA, V> (&g)[R], float (&h0)[V]) {
-        const int rows = t >= s.lo ? s.hi - t - wave * R : 0;
-        load(x, xp + t * a.x_tok, a.x_tok, rows, in, 0.f);
-        load(g, ap + t * a.a_tok, a.a_tok, rows, in, 1.f);
-        load(d, dp + (int64_t)t * a.C, a.C, rows, in, 0.f);
-        load_state<V>(h0, st + (int64_t)(t / TILE) * a.C, in && t >= s.lo);
-    };
-    int t = s.hi > s.lo ? s.lo + (s.hi - s.lo - 1) / TILE * TILE : s.lo - TILE;
-    fetch(t, x, d, g, h0);
-    int buf = 0;
-    for (; t >= s.lo; t -= TILE, buf ^= 1) {
-        Pack<TX, V> xn[R], dn[R];
-        Pack<TA, V> gn[R];
-        float hn[V];
-        fetch(t - TILE, xn, dn, gn, hn);
-        float P[V], H[V], K[V];
 #pragma unroll
-        for (int e = 0; e < V; ++e) P[e] = 1.f, H[e] = 0.f, K[e] = 0.f;
+    for (int r = 0; r < R; ++r) H = __builtin_fmaf((float)g[r], H, (float)x[r]);
+    sh[wave][0][lane] = P, sh[wave][1][lane] = H, sh[wave][2][lane] = K;
+    __syncthreads();
+    u64* const word = CHAIN ? a.words + header_words(a.C) + s.row() * a.C + c : nullptr;
+    if (wave == 0) {
+        float p = 1.f, q = 0.f;
 #pragma unroll
-        for (int r = 0; r < R; ++r)
-#pragma unroll
-            for (int e = 0; e < V; ++e) {
-                H[e] = __builtin_fmaf((float)g[r].v[e], H[e], (float)x[r].v[e]);
-                P[e] *= (float)g[r].v[e];
-                K[e] = (float)g[R - 1 - r].v[e] * ((float)d[R - 1 - r].v[e] + K[e]);
-            }
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-            sh[buf][wave][0][lane * V + e] = P[e];
-            sh[buf][wave][1][lane * V + e] = H[e];
-            sh[buf][wave][2][lane * V + e] = K[e];
+        for (int w = NW - 1; w >= 0; --w) {
+            q = __builtin_fmaf(sh[w][0][lane], q, sh[w][2][lane]);
+            p *= sh[w][0][lane];
         }
-        __syncthreads();
-        float mine[V];
-#pragma unroll
-        for (int w = 0; w < NW; ++w)
-#pragma unroll
-            for (int e = 0; e < V; ++e) {
-                if (w == wave) mine[e] = h0[e];
-                h0[e] = __builtin_fmaf(sh[buf][w][0][lane * V + e], h0[e], sh[buf][w][1][lane * V + e]);
-            }
-        float cin[V];
-#pragma unroll
-        for (int w = NW - 1; w >= 0; --w)
-#pragma unroll
-            for (int e = 0; e < V; ++e) {
-                if (w == wave) cin[e] = gc[e];
-                gc[e] = __builtin_fmaf(sh[buf][w][0][lane * V + e], gc[e], sh[buf][w][2][lane * V + e]);
-            }
-        float before[R][V];
-#pragma unroll
-        for (int r = 0; r < R; ++r)
-#pragma unroll
-            for (int e = 0; e < V; ++e) {
-                before[r][e] = mine[e];
-                mine[e] = __builtin_fmaf((float)g[r].v[e], mine[e], (float)x[r].v[e]);
-            }
-        const int rows = s.hi - t - wave * R;
-#pragma unroll
-        for (int r = R - 1; r >= 0; --r) {
-            Pack<TX, V> ox;
-            Pack<TA, V> oa;
-#pragma unroll
-            for (int e = 0; e < V; ++e) {
-                const float gt = (float)d[r].v[e] + cin[e];
-                ox.v[e] = (TX)gt;
-                oa.v[e] = (TA)(gt * before[r][e]);
-                cin[e] = (float)g[r].v[e] * gt;
-            }
-            if (in && r < rows) {
-                *(Pack<TX, V>*)((TX*)a.out + o0 + (int64_t)(t + r) * a.C) = ox;
-                *(Pack<TA, V>*)((TA*)a.da + o0 + (int64_t)(t + r) * a.C) = oa;
-            }
-        }
-#pragma unroll
-        for (int r = 0; r < R; ++r) x[r] = xn[r], d[r] = dn[r], g[r] = gn[r];
-#pragma unroll
-        for (int e = 0; e < V; ++e) h0[e] = hn[e];
+        sh[NW][0][lane] = p, sh[NW][2][lane] = q;
+        if (CHAIN && s.before > 0 && s.tile > 0 && in) publish_first(word, word_of(q, key_of(p)));
     }
-    if (a.state && wave == 0 && s.lo == 0) store_state<V>(a.state + (int64_t)s.seq * a.C + c, gc, in);
+    if (CHAIN && s.before > 0) enter(a, gc, words_of, s.row() + 1, -1, s.before, c, in);
+    if (wave == 0 && in) {
+        const float end = __builtin_fmaf(sh[NW][0][lane], gc, sh[NW][2][lane]);
+        if (CHAIN && s.tile > 0) publish(word, word_of(end, kState));
+        if (a.state && s.tile == 0) a.state[(int64_t)s.seq * a.C + c] = end;
+    }
+    for (int w = NW - 1; w > wave; --w) gc = __builtin_fmaf(sh[w][0][lane], gc, sh[w][2][lane]);
+    for (int w = 0; w < wave; ++w) h = __builtin_fmaf(sh[w][0][lane], h, sh[w][1][lane]);
+    float before[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        before[r] = h;
+        h = __builtin_fmaf((float)g[r], h, (float)x[r]);
+    }
+    const int64_t o0 = (tok + R - 1) * a.C;
+    TX* xp = (TX*)a.out + o0;
+    TA* ap = (TA*)a.da + o0;
+#pragma unroll
+    for (int r = R - 1; r >= 0; --r) {
+        const float gt = (float)d[r] + gc;
+        gc = (float)g[r] * gt;
+        if (in && r < rows) xp[c] = (TX)gt, ap[c] = (TA)(gt * before[r]);
+        xp -= a.C;
+        ap -= a.C;
+    }
 }
 
-template <typename TX, typename TA, int V>
-hipError_t forward(const ScanArgs& a, hipStream_t s) {
-    const dim3 bl(64 * NW), gr((unsigned)(a.groups + a.clear));
+// Clears the published words of a call whose tiles wait for each other.
+hipError_t clear_words(const ScanArgs& a, hipStream_t s) {
+    const int64_t n = scan_words(a.N, a.S, a.C), groups = (n + 1023) / 1024;
+    scan_clear_kernel<<<dim3((unsigned)(groups < 2048 ? groups : 2048)), dim3(256), 0, s>>>(a.words, n);
+    return hipGetLastError();
+}
+
+template <typename TX, typename TA>
+hipError_t forward(ScanArgs a, hipStream_t s) {
+    const dim3 bl(64 * NW);
     if (a.shorts) {
-        scan_short_kernel<TX, TA, V><<<dim3((unsigned)((a.groups + 3) / 4 + a.clear)), dim3(256), 0, s>>>(a);
-    } else if (a.part) {
-        scan_parts_kernel<TX, TA, V, false><<<dim3((unsigned)a.groups), bl, 0, s>>>(a);
-        const hipError_t e = hipGetLastError();
+        scan_short_kernel<TX, TA><<<dim3((unsigned)((a.groups + 3) / 4 + a.clear)), dim3(256), 0, s>>>(a);
+    } else if (a.words) {
+        int cus = 0;
+        hipError_t e = device_cu_count(&cus);
+        if (e == hipSuccess) e = clear_words(a, s);
         if (e != hipSuccess) return e;
-        scan_fwd_kernel<TX, TA, V, true><<<gr, bl, 0, s>>>(a);
+        const int stay = (kStay * cus + a.slabs - 1) / a.slabs * a.slabs;
+        if (a.groups > stay) a.groups = stay;
+        scan_fwd_kernel<TX, TA, true><<<dim3((unsigned)(a.groups + a.clear)), bl, 0, s>>>(a);
     } else {
-        scan_fwd_kernel<TX, TA, V, false><<<gr, bl, 0, s>>>(a);
+        scan_fwd_kernel<TX, TA, false><<<dim3((unsigned)(a.groups + a.clear)), bl, 0, s>>>(a);
     }
     return hipGetLastError();
 }
 
-template <typename TX, typename TA, int V>
+template <typename TX, typename TA>
 hipError_t backward(const ScanArgs& a, hipStream_t s) {
     const dim3 bl(64 * NW), gr((unsigned)(a.groups + a.clear));
-    if (a.part) {
-        ScanArgs b = a;  // the gradient of the parts goes through gates and dout
-        b.x = a.dout;
-        b.x_tok = a.C;
-        scan_parts_kernel<TX, TA, V, true><<<dim3((unsigned)a.groups), bl, 0, s>>>(b);
-        const hipError_t e = hipGetLastError();
+    if (a.words) {
+        const hipError_t e = clear_words(a, s);
         if (e != hipSuccess) return e;
-        scan_bwd_kernel<TX, TA, V, true><<<gr, bl, 0, s>>>(a);
+        scan_bwd_kernel<TX, TA, true><<<gr, bl, 0, s>>>(a);
     } else {
-        scan_bwd_kernel<TX, TA, V, false><<<gr, bl, 0, s>>>(a);
+        scan_bwd_kernel<TX, TA, false><<<gr, bl, 0, s>>>(a);
     }
     return hipGetLastError();
 }
 
 }  // namespace
 
+int64_t scan_words(int64_t N, int64_t S, int64_t C) { return header_words(C) + (N / TILE + S) * C; }
+
 hipError_t launch_scan_forward(const ScanArgs& a, hipStream_t s) {
-    if (a.x_f32) return forward<float, float, 1>(a, s);
-    if (a.gate_f32) return a.pairs ? forward<__bf16, float, 2>(a, s) : forward<__bf16, float, 1>(a, s);
-    return a.pairs ? forward<__bf16, __bf16, 2>(a, s) : forward<__bf16, __bf16, 1>(a, s);
+    if (a.x_f32) return forward<float, float>(a, s);
+    return a.gate_f32 ? forward<__bf16, float>(a, s) : forward<__bf16, __bf16>(a, s);
 }
 
 hipError_t launch_scan_backward(const ScanArgs& a, hipStream_t s) {
-    if (a.x_f32) return backward<float, float, 1>(a, s);
-    if (a.gate_f32) return a.pairs ? backward<__bf16, float, 2>(a, s) : backward<__bf16, float, 1>(a, s);
-    return a.pairs ? backward<__bf16, __bf16, 2>(a, s) : backward<__bf16, __bf16, 1>(a, s);
+    if (a.x_f32) return backward<float, float>(a, s);
+    return a.gate_f32 ? backward<__bf16, float>(a, s) : backward<__bf16, __bf16>(a, s);
 }
 
 }  // namespace e2ttt
