@@ -13,10 +13,17 @@
 //    to count those below its range and, wave by wave, each of its own; then to
 //    put every place where it belongs.  No workgroup waits for another, and the
 //    reads (the tokens alone, from the L2 cache) are little beside the rows.
-// 2. A wave per row of the table sums its places' rows from registers and writes
-//    the row.  Rows with more than kEmbedPiece places (a text's commonest words)
-//    are left to waves that own a piece of the sorted places each.
+// 2. A wave per row of the table and 1024 columns sums its places' rows from registers
+//    and writes the row.  Rows with more than kEmbedPiece places (a text's commonest
+//    words) are left to waves that own a piece of the sorted places each: a wave's
+//    places come in few ways to memory, so none is still at work when the others are
+//    done (16384 tokens of a text, a table of 32000 rows of 2048 in fp32, 262 MB of them:
+//    137 us with pieces of 32 and two rows on their way, 72 with 16 and eight; a fill of
+//    the table alone is 33).
 // 3. The pieces of such rows are summed in order.
+//
+// The whole gradient of that table takes 17 us for the order, 72 and 10; the lookup
+// before it 29 (200 MB at most), and a lookup of eight tokens is one launch, 7 us.
 #include "tokens_internal.h"
 
 namespace e2ttt {
@@ -24,38 +31,30 @@ namespace {
 
 typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
 
-// V values from p, aligned to 16 bytes where V is more than one.
+// V values from p, aligned to 16 bytes (or all of them) where V is more than one.
+template <typename T, int V>
+constexpr int kAtOnce = V * sizeof(T) < 16 ? V : 16 / sizeof(T);
 template <typename T, int V>
 __device__ __forceinline__ void read(float (&x)[V], const T* p) {
-    if constexpr (V == 1) {
-        x[0] = (float)p[0];
-    } else {
-        constexpr int E = 16 / sizeof(T);
+    constexpr int E = kAtOnce<T, V>;
+    typedef T Vec __attribute__((ext_vector_type(E)));
 #pragma unroll
-        for (int i = 0; i < V / E; ++i) {
-            const u32x4 u = *(const u32x4*)(p + i * E);
-            T t[E];
-            __builtin_memcpy(t, &u, 16);
+    for (int i = 0; i < V / E; ++i) {
+        const Vec u = *(const Vec*)(p + i * E);
 #pragma unroll
-            for (int e = 0; e < E; ++e) x[i * E + e] = (float)t[e];
-        }
+        for (int e = 0; e < E; ++e) x[i * E + e] = (float)u[e];
     }
 }
 template <typename T, int V>
 __device__ __forceinline__ void write(T* p, const float (&x)[V], float scale) {
-    if constexpr (V == 1) {
-        p[0] = (T)(x[0] * scale);
-    } else {
-        constexpr int E = 16 / sizeof(T);
+    constexpr int E = kAtOnce<T, V>;
+    typedef T Vec __attribute__((ext_vector_type(E)));
 #pragma unroll
-        for (int i = 0; i < V / E; ++i) {
-            T t[E];
+    for (int i = 0; i < V / E; ++i) {
+        Vec u;
 #pragma unroll
-            for (int e = 0; e < E; ++e) t[e] = (T)(x[i * E + e] * scale);
-            u32x4 u;
-            __builtin_memcpy(&u, t, 16);
-            *(u32x4*)(p + i * E) = u;
-        }
+        for (int e = 0; e < E; ++e) u[e] = (T)(x[i * E + e] * scale);
+        *(Vec*)(p + i * E) = u;
     }
 }
 
@@ -63,6 +62,21 @@ __device__ __forceinline__ void write(T* p, const float (&x)[V], float scale) {
 __device__ __forceinline__ int token_of(const EmbedArgs& a, int64_t n) {
     const int64_t t = a.wide ? ((const int64_t*)a.tokens)[n] : ((const int*)a.tokens)[n];
     return t >= 0 && t < a.V ? (int)t : -1;
+}
+
+// Tokens n, n + 64, ..., -1 from `end` on; all on their way at once.
+template <int U>
+__device__ __forceinline__ void tokens_of(const EmbedArgs& a, int (&t)[U], int64_t n, int64_t end) {
+    int64_t x[U];
+    if (a.wide) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) x[u] = n + u * 64 < end ? ((const int64_t*)a.tokens)[n + u * 64] : -1;
+    } else {
+#pragma unroll
+        for (int u = 0; u < U; ++u) x[u] = n + u * 64 < end ? ((const int*)a.tokens)[n + u * 64] : -1;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) t[u] = x[u] >= 0 && x[u] < a.V ? (int)x[u] : -1;
 }
 
 // HIP counts the threads along a grid dimension in 32 bits.
@@ -115,11 +129,16 @@ __global__ __launch_bounds__(64 * kOrderWaves) void embed_order_kernel(EmbedArgs
     const int64_t per = ((a.N + kOrderWaves - 1) / kOrderWaves + 63) / 64 * 64;
     const int64_t n0 = wave * per, n1 = n0 + per < a.N ? n0 + per : a.N;
     int below = 0;
-    for (int64_t n = n0 + lane; n < n1; n += 64) {
-        const int t = token_of(a, n);
-        below += t >= 0 && t < v0;
-        const int r = t - v0;
-        if (t >= 0 && r >= 0 && r < R) atomicAdd(&cnt[wave][r], 1);
+    constexpr int U = 8;  // tokens on their way to a lane
+    for (int64_t i = n0; i < n1; i += 64 * U) {
+        int t[U];
+        tokens_of<U>(a, t, i + lane, n1);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            below += t[u] >= 0 && t[u] < v0;
+            const int r = t[u] - v0;
+            if (t[u] >= 0 && r >= 0 && r < R) atomicAdd(&cnt[wave][r], 1);
+        }
     }
     below = wave_inclusive(below);
     if (lane == 63) sums[wave] = below;
@@ -147,33 +166,38 @@ __global__ __launch_bounds__(64 * kOrderWaves) void embed_order_kernel(EmbedArgs
         if (v0 + (int)threadIdx.x == a.V - 1) a.start[a.V] = at;
     }
     __syncthreads();
-    for (int64_t i = n0; i < n1; i += 64) {
-        const int64_t n = i + lane;
-        const int t = n < n1 ? token_of(a, n) : -1, r = t - v0;
-        const bool in = t >= 0 && r >= 0 && r < R;
-        unsigned long long same = __ballot(in);
-        if (!same) continue;
-        for (int b = 0; b < bits; ++b) {  // lanes with the same token
-            const unsigned long long set = __ballot((r >> b) & 1);
-            same &= (r >> b) & 1 ? set : ~set;
-        }
-        if (in) {
-            const int rank = lanes_below(same), to = cnt[wave][r];
-            a.order[to + rank] = (int)n;
-            if (rank == 0) cnt[wave][r] = to + __popcll(same);
+    for (int64_t i = n0; i < n1; i += 64 * U) {
+        int t[U];
+        tokens_of<U>(a, t, i + lane, n1);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int r = t[u] - v0;
+            const bool in = t[u] >= 0 && r >= 0 && r < R;
+            unsigned long long same = __ballot(in);
+            if (!same) continue;
+            for (int b = 0; b < bits; ++b) {  // lanes with the same token
+                const unsigned long long set = __ballot((r >> b) & 1);
+                same &= (r >> b) & 1 ? set : ~set;
+            }
+            if (in) {
+                const int rank = lanes_below(same), to = cnt[wave][r];
+                a.order[to + rank] = (int)(i + u * 64 + lane);
+                if (rank == 0) cnt[wave][r] = to + __popcll(same);
+            }
         }
     }
 }
 
 // ------------------------------------------------------------- 2: the sums
-// acc += the rows of places [s, e), at most kEmbedPiece of them, columns c0 on.
+// acc += the rows of `count` places, kEmbedPiece at most, from order[s] on; columns c0 on.
 template <typename TI, int V, int NU>
-__device__ __forceinline__ void sum_places(const EmbedArgs& a, float (&acc)[NU][V], int s, int e, int64_t c0) {
-    constexpr int U = NU > 1 ? 2 : 4;  // places whose rows are on their way together
+__device__ __forceinline__ void sum_places(const EmbedArgs& a, float (&acc)[NU][V], int s, int count, int64_t c0) {
+    constexpr int E = kAtOnce<TI, V>, kFit = 32 / (NU * V) * (int)(4 / sizeof(TI)), U = kFit < 2 ? 2 : kFit;
+    typedef TI Vec __attribute__((ext_vector_type(E)));
     const int lane = threadIdx.x & 63;
-    const int mine = s + lane < e ? a.order[s + lane] : 0;
-    for (int k = 0; k < e - s; k += U) {
-        float x[U][NU][V];
+    const int mine = lane < count ? a.order[s + lane] : 0;
+    for (int k = 0; k < count; k += U) {
+        Vec x[U][NU][V / E];  // U places' rows on their way together
 #pragma unroll
         for (int j = 0; j < U; ++j) {
             const int64_t n = __builtin_amdgcn_readlane(mine, (k + j) & 63);
@@ -182,17 +206,17 @@ __device__ __forceinline__ void sum_places(const EmbedArgs& a, float (&acc)[NU][
             for (int i = 0; i < NU; ++i) {
                 const int64_t c = c0 + ((int64_t)i * 64 + lane) * V;
 #pragma unroll
-                for (int q = 0; q < V; ++q) x[j][i][q] = 0.f;
-                if (k + j < e - s && c < a.W) read<TI, V>(x[j][i], row + c);
+                for (int p = 0; p < V / E; ++p)
+                    if (k + j < count && c < a.W) x[j][i][p] = *(const Vec*)(row + c + p * E);
             }
         }
 #pragma unroll
         for (int j = 0; j < U; ++j)
-            if (k + j < e - s) {
+            if (k + j < count) {
 #pragma unroll
                 for (int i = 0; i < NU; ++i)
 #pragma unroll
-                    for (int q = 0; q < V; ++q) acc[i][q] += x[j][i][q];
+                    for (int q = 0; q < V; ++q) acc[i][q] += (float)x[j][i][q / E][q % E];
             }
     }
 }
@@ -210,7 +234,7 @@ __device__ __forceinline__ void write_row(const EmbedArgs& a, TO* row, const flo
 // A wave per piece, then one per row of the table; 64 V NU columns each.
 template <typename TI, typename TO, int V, int NU>
 __global__ __launch_bounds__(256) void embed_sum_kernel(EmbedArgs a, int64_t pieces) {
-    const int64_t w = group_index() * 4 + (threadIdx.x >> 6);
+    const int64_t w = group_index() * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t c0 = (int64_t)blockIdx.z * (64 * V * NU);
     if (w < pieces) {
         const int total = a.start[a.V], b0 = (int)w * kEmbedPiece;
@@ -223,7 +247,8 @@ __global__ __launch_bounds__(256) void embed_sum_kernel(EmbedArgs a, int64_t pie
             const bool starts = s >= b0;
             if (e - s > kEmbedPiece && starts == (k == 1)) {
                 float acc[NU][V] = {};
-                sum_places<TI, V, NU>(a, acc, s > b0 ? s : b0, e < b1 ? e : b1, c0);
+                const int lo = s > b0 ? s : b0, hi = e < b1 ? e : b1;
+                sum_places<TI, V, NU>(a, acc, lo, hi - lo, c0);
                 write_row<float, V, NU>(a, a.part + (2 * w + k) * a.W, acc, 1.f, c0);
             }
         }
@@ -234,7 +259,7 @@ __global__ __launch_bounds__(256) void embed_sum_kernel(EmbedArgs a, int64_t pie
     const int s = a.start[v], e = a.start[v + 1];
     if (e - s > kEmbedPiece) return;
     float acc[NU][V] = {};
-    sum_places<TI, V, NU>(a, acc, s, e, c0);
+    sum_places<TI, V, NU>(a, acc, s, e - s, c0);
     write_row<TO, V, NU>(a, (TO*)a.out + v * a.W, acc, a.scale, c0);
 }
 
@@ -296,15 +321,18 @@ hipError_t sums(const EmbedArgs& a, int64_t pieces, hipStream_t s) {
 
 template <typename TI, typename TO, int V>
 hipError_t backward(const EmbedArgs& a, hipStream_t s) {
-    int bits = 0;  // about 512 workgroups, each with as few tokens as that leaves
-    while (bits < 9 && ((int64_t)a.V >> bits) > 512) ++bits;
+    int bits = 0;  // a workgroup per compute unit, each with as few tokens as that leaves
+    while (bits < 9 && ((int64_t)a.V >> bits) > 256) ++bits;
     static_assert(1 << 9 == kRange, "a workgroup's range fits its counters");
     const int64_t groups = ((int64_t)a.V + (1 << bits) - 1) >> bits;
     embed_order_kernel<<<dim3((unsigned)groups), dim3(64 * kOrderWaves), 0, s>>>(a, bits);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     const int64_t pieces = a.N > kEmbedPiece ? (a.N + kEmbedPiece - 1) / kEmbedPiece : 0;
-    e = a.W <= 64 * V ? sums<TI, TO, V, 1>(a, pieces, s) : sums<TI, TO, V, 4>(a, pieces, s);
+    // 64 V columns to a wave while all of them fit the chip at once (256 rows of 512: 7 us,
+    // 26 with 16 times 64), else more, so that fewer look for their places
+    const int64_t narrow = (a.W + 64 * V - 1) / (64 * V);
+    e = (pieces + a.V) * narrow <= 8192 ? sums<TI, TO, V, 1>(a, pieces, s) : sums<TI, TO, V, 16 / V>(a, pieces, s);
     if (e != hipSuccess || pieces == 0) return e;
     embed_join_kernel<TO, V><<<grid_of(pieces, (unsigned)((a.W + 64 * V - 1) / (64 * V))), dim3(64 * kJoinWaves), 0, s>>>(a);
     return hipGetLastError();
@@ -321,8 +349,8 @@ hipError_t launch_embedding_forward(const EmbedArgs& a, hipStream_t s) {
 
 hipError_t launch_embedding_backward(const EmbedArgs& a, hipStream_t s) {
     if (a.in_f32 && a.out_f32) return a.vec ? backward<float, float, 4>(a, s) : backward<float, float, 1>(a, s);
-    if (a.in_f32) return a.vec ? backward<float, __bf16, 8>(a, s) : backward<float, __bf16, 1>(a, s);
-    if (a.out_f32) return a.vec ? backward<__bf16, float, 8>(a, s) : backward<__bf16, float, 1>(a, s);
+    if (a.in_f32) return a.vec ? backward<float, __bf16, 4>(a, s) : backward<float, __bf16, 1>(a, s);
+    if (a.out_f32) return a.vec ? backward<__bf16, float, 4>(a, s) : backward<__bf16, float, 1>(a, s);
     return a.vec ? backward<__bf16, __bf16, 8>(a, s) : backward<__bf16, __bf16, 1>(a, s);
 }
 

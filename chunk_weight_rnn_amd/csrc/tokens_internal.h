@@ -24,7 +24,7 @@ struct EmbedArgs {
     float* part;     // [2 ceil(N / kEmbedPiece)][W] sums over pieces of rows with many places
 };
 // Places that a wave sums for one row; rows with more are cut into pieces.
-constexpr int kEmbedPiece = 32;
+constexpr int kEmbedPiece = 16;
 hipError_t launch_embedding_forward(const EmbedArgs& a, hipStream_t s);
 hipError_t launch_embedding_backward(const EmbedArgs& a, hipStream_t s);
 
