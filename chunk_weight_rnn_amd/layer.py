@@ -59,6 +59,22 @@ def _call(fn: str, dev: int, *args):
         raise E2TTTError(fn, st)
 
 
+def _one_stream(out, dev: int):
+    """Refuses a capture with gradients for leaves that an eager graph, still alive, used on
+    another stream: the backward pass ends by making that stream wait, which a capture does
+    not survive (the process ends in it)."""
+    node = out.grad_fn
+    if node is None:
+        return
+    stream, capturing = torch._C._cuda_getCurrentRawStream(dev), torch.cuda.is_current_stream_capturing()
+    for leaf, _ in node.next_functions:
+        # one such node per leaf, as long as a graph holds it
+        if leaf is not None and leaf.name() == "torch::autograd::AccumulateGrad":
+            if leaf.metadata.setdefault("e2ttt_stream", stream) != stream and capturing:
+                raise RuntimeError("a leaf of this capture is in an autograd graph of another stream: "
+                                   "drop that graph's outputs first")
+
+
 def _p(t):
     return None if t is None else t.data_ptr()
 
@@ -421,8 +437,11 @@ class _GatedScan(torch.autograd.Function):
 
 def gated_scan(x, a, cu_seqlens, h0=None):
     """``gated_scan_forward`` as a differentiable op: returns (out, state), with
-    gradients for x, a and h0 from ``gated_scan_backward``."""
-    return _GatedScan.apply(x, a, h0, cu_seqlens)
+    gradients for x, a and h0 from ``gated_scan_backward``.  Captured into a graph with its
+    backward pass, no eager graph of the same leaves may be alive (RuntimeError)."""
+    out, state = _GatedScan.apply(x, a, h0, cu_seqlens)
+    _one_stream(out, x.get_device())
+    return out, state
 
 
 def norm_forward(x, weight, *, residual=None, eps: float = 1e-6, bits8: bool = False, h=None, stream=None):

@@ -116,3 +116,23 @@ def test_paged8_arguments(z):
     refused(TypeError, "k_scale must be", lambda: f(ks=z(5, 2, 16)))
     refused(ValueError, "v_scale must have shape", lambda: f(vs=z(5, 16, 2, d=E8)))
     refused(ValueError, "k_scale must be contiguous", lambda: f(ks=z(5, 16, 2, d=E8).transpose(1, 2)))
+
+
+def test_leaves_of_a_live_graph_are_refused_in_a_capture(monkeypatch):
+    """The check behind embedding and gated_scan, on the CPU with the stream and the capture given."""
+    from chunk_weight_rnn_amd import layer
+    stream, capturing = [1], [False]
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: stream[0], raising=False)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: capturing[0])
+    w = torch.ones(3, requires_grad=True)
+    alive = w * 2
+    layer._one_stream(alive, 0)
+    stream[0] = 2
+    layer._one_stream(w * 3, 0)  # not captured: torch orders the streams
+    capturing[0] = True
+    with pytest.raises(RuntimeError, match="another stream"):
+        layer._one_stream(w * 3, 0)
+    layer._one_stream(torch.ones(3), 0)  # no gradients
+    layer._one_stream((w * 2) * 3, 0)  # not a leaf
+    del alive
+    layer._one_stream(w * 3, 0)
