@@ -3,8 +3,12 @@
 //
 // The work is shared out as in attn_decode.hip: units of 128 keys of all items in
 // one line, an equal stretch of it per workgroup, four waves that each stream their
-// own 32 keys through LDS stages of their own.  A stage is half as large, so there
-// are twice as many and as many bytes are on their way.  A wave needs the page of
+// own 32 keys through LDS stages of their own.  A stage is half as large, so that where
+// the keys are shared out two workgroups fit a compute unit: bound by HBM and by what a
+// wave does with a unit, one after the other, which a second wave on the same SIMD fills
+// (64 sequences at up to 16383 keys, 16 heads of 128 over 4, 520 MB: 149 us with one
+// workgroup of four stages, 107 with two of two, and 5 each to write the new tokens and
+// to join).  Without sharing a workgroup has four stages.  A wave needs the page of
 // each of its keys for the copies, and the scale of each key and value, which come
 // with them, a byte per lane (keys' in lanes 0..31, values' in lanes 32..63).
 //
@@ -18,8 +22,6 @@
 namespace e2ttt {
 namespace attn {
 namespace {
-
-constexpr int NS = 4;  // LDS stages of a wave
 
 // A tile holds 32 rows of DP bytes, 16-byte chunk c of row t at chunk c ^ swz8(t).
 // Two reads have to be free of bank conflicts (64 four-byte banks):
@@ -44,17 +46,18 @@ __device__ __forceinline__ void copy1_at(const void* p, unsigned lds) {
 }
 
 template <int DP, bool SPLIT>
-__global__ __launch_bounds__(256, 1) void attn_decode8_kernel(AttnArgs a, int groups) {
+__global__ __launch_bounds__(256, SPLIT ? 2 : 1) void attn_decode8_kernel(AttnArgs a, int groups) {
+    constexpr int NS = SPLIT ? 2 : 4;         // LDS stages of a wave
     constexpr int TILE = BW * DP;             // a wave's keys (or values) of a unit
     constexpr int CH = DP / 16, RPI = 64 / CH;  // chunks of a row, rows per copy instruction
     constexpr int NI = BW / RPI;
     constexpr int KP = DP / 32, DT = DP / 32;  // pairs of 16-wide steps over the head dimension
     constexpr int COPIES = 2 * NI + 2;         // of a unit: keys, values, scales, and pages later
-    __shared__ __attribute__((aligned(1024))) unsigned char lds[4][NS][2][TILE];  // [wave][stage][K, V]
+    constexpr int STAGES = 8 * NS * TILE, AREA = kMergeFloats<DP> * 4 > STAGES ? kMergeFloats<DP> * 4 : STAGES;
+    __shared__ __attribute__((aligned(1024))) unsigned char lds[AREA];  // [wave][stage][K, V][TILE], then the merge area
     __shared__ float stat[4][2][BM];
-    __shared__ __attribute__((aligned(256))) int pages[4][2 * NS][64];            // [wave][unit % 8][key, twice]
+    __shared__ __attribute__((aligned(256))) int pages[4][2 * NS][64];            // [wave][unit % 2 NS][key, twice]
     __shared__ __attribute__((aligned(256))) unsigned scales[4][NS][64];          // [wave][stage][keys', values']
-    static_assert(kMergeFloats<DP> * 4 <= (int)sizeof(lds), "the merge area fits in the stages");
 
     if ((int)blockIdx.x >= groups) {
         clear_block<__bf16>(a, blockIdx.x - groups);
@@ -77,7 +80,7 @@ __global__ __launch_bounds__(256, 1) void attn_decode8_kernel(AttnArgs a, int gr
     const int tp = lane & 15, tr = tp >> 1, trow = (tr < 4 ? tr : tr + 4) + 4 * g;
     const unsigned tb = (unsigned)(trow * DP + 16 * (((lane >> 4) & 1) ^ swz8<DP>(trow)) + 8 * (tp & 1));
     const int crow = lane / CH;
-    const unsigned base = lds_addr(&lds[wave][0][0][0]);
+    const unsigned base = lds_addr(lds + wave * (2 * NS * TILE));
     const int mask = (1 << a.pg.shift) - 1;
 
     bool first_seg = true;
@@ -158,15 +161,15 @@ __global__ __launch_bounds__(256, 1) void attn_decode8_kernel(AttnArgs a, int gr
         for (int b = b0; b < b1; ++b) {
             // unit b has come, and the pages of unit b + NS: what may be outstanding are
             // the units after it, with a copy of pages each
-            static_assert(NS == 4, "a wait for each number of units on their way");
+            static_assert(NS == 2 || NS == 4, "a wait for each number of units on their way");
             const int after = b1 - 1 - b;
-            if (after >= 3) wait_vm<3 * COPIES>();
-            else if (after == 2) wait_vm<2 * COPIES>();
-            else if (after == 1) wait_vm<COPIES>();
+            if (NS == 4 && after >= 3) wait_vm<3 * COPIES>();
+            else if (NS == 4 && after == 2) wait_vm<2 * COPIES>();
+            else if (after >= 1) wait_vm<COPIES>();
             else wait_vm<0>();
             const int stage = b & (NS - 1), p0 = w.lo + b * UNIT + BW * wave;
             if (p0 <= last) {
-                const unsigned char *kt = lds[wave][stage][0], *vt = lds[wave][stage][1];
+                const unsigned char *kt = lds + (wave * NS + stage) * (2 * TILE), *vt = kt + TILE;
                 const unsigned* sl = scales[wave][stage];
                 const float kscale = scale_bits(sl[col]);
                 f32x16 sc = {};
@@ -244,7 +247,7 @@ __global__ __launch_bounds__(256, 1) void attn_decode8_kernel(AttnArgs a, int gr
             }
         }
         wait_lds();
-        finish_item<DP, SPLIT>(a, w, acc, m, l, live, whole, 2 * blockIdx.x + (first_seg ? 0 : 1), (float*)&lds[0][0][0][0], stat);
+        finish_item<DP, SPLIT>(a, w, acc, m, l, live, whole, 2 * blockIdx.x + (first_seg ? 0 : 1), (float*)lds, stat);
         __syncthreads();  // the area is the next item's stages
         u += b1 - b0;
         first_seg = false;
@@ -255,7 +258,7 @@ __global__ __launch_bounds__(256, 1) void attn_decode8_kernel(AttnArgs a, int gr
 template <int DP>
 hipError_t launch(const AttnArgs& a, hipStream_t s) {
     const int64_t items = (int64_t)a.ntiles * a.K;
-    const int64_t groups = a.nsplit > 1 ? kDecodeGroups : items;
+    const int64_t groups = a.nsplit > 1 ? a.shares : items;
     const int64_t grid = groups + a.clear;
     if (grid > kMaxGroups || items > kMaxGroups) return hipErrorInvalidConfiguration;
     if (a.nsplit > 1)

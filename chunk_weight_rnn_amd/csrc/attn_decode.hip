@@ -238,14 +238,14 @@ __global__ __launch_bounds__(256) void attn_decode_join_kernel(AttnArgs a, int g
 
 template <int DP>
 hipError_t join(const AttnArgs& a, int64_t items, hipStream_t s) {
-    attn_decode_join_kernel<DP><<<dim3((unsigned)items), dim3(256), 0, s>>>(a, kDecodeGroups);
+    attn_decode_join_kernel<DP><<<dim3((unsigned)items), dim3(256), 0, s>>>(a, a.shares);
     return hipGetLastError();
 }
 
 template <int DP>
 hipError_t launch(const AttnArgs& a, hipStream_t s) {
     const int64_t items = (int64_t)a.ntiles * a.K;
-    const int64_t groups = a.nsplit > 1 ? kDecodeGroups : items;
+    const int64_t groups = a.nsplit > 1 ? a.shares : items;
     const int64_t grid = groups + a.clear + append_blocks(a, 8);
     if (grid > kMaxGroups || items > kMaxGroups) return hipErrorInvalidConfiguration;
     if (a.nsplit > 1)

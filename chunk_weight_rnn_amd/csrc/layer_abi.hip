@@ -131,20 +131,27 @@ void plan(AttnArgs& a, bool f32, int64_t longest) {
 // and 12.9, at 1000 19.6 and 12.3; 16 sequences at 640 14.7 and 18.5, at 700 16.5
 // and 15.1, at 1000 19.7 and 16.4; 64 at 640 19.0 and 23.0, at 1000 25.2 and 29.1.
 constexpr int64_t kOneLaunch = 640;
-void plan_paged(AttnArgs& a, bool f32, int64_t longest) {
+// Over a cache in 8 bits (with the launch that writes the new token), one sequence and
+// 16: at 250 keys 11.8 and 13.5, 12.5 and 14.3, at 380 13.9 and 13.4, 14.9 and 14.4, at 500
+// 16.1 and 13.4, 16.9 and 14.5; 64, whose items are a workgroup for every compute unit: at
+// 500 18.4 and 20.3, at 760 24.1 and 25.3, at 1000 28.6 and 27.7.
+constexpr int64_t kOneLaunch8 = 384, kOneLaunch8Full = 768;
+void plan_paged(AttnArgs& a, bool f32, bool bits8, int64_t longest) {
     const int64_t units = (longest + a.N + 127) / 128, tiles = a.N * a.G / 32 + a.S;
     if (!f32 && a.N * a.G <= 32 * (int64_t)a.S && tiles * a.K <= 0x7fffffff / (units + 1)) {
         a.decode = 1;
         a.ntiles = (int)tiles;
         if (a.window > 0 && longest > (int64_t)a.window + 64) longest = (int64_t)a.window + 64;
-        a.nsplit = longest <= kOneLaunch ? 1 : 2;
+        const int64_t one = !bits8 ? kOneLaunch : tiles * a.K < kDecodeGroups ? kOneLaunch8 : kOneLaunch8Full;
+        a.nsplit = longest <= one ? 1 : 2;
+        a.shares = bits8 ? kDecode8Groups : kDecodeGroups;
         return;
     }
     plan(a, f32, longest);
 }
 
 size_t partial_rows(const AttnArgs& a) {
-    return a.decode ? (size_t)2 * kDecodeGroups * 32 : (size_t)a.nsplit * a.N * a.H;
+    return a.decode ? (size_t)2 * a.shares * 32 : (size_t)a.nsplit * a.N * a.H;
 }
 
 size_t split_bytes(const AttnArgs& a) {
@@ -176,7 +183,7 @@ int run_forward(AttnArgs& a, bool f32, hipStream_t s) {
 // call that is refused.
 bool grids8_ok(const AttnArgs& a) {
     const int64_t items = (int64_t)a.ntiles * a.K, append = (2 * a.N * a.K + kAppend8Rows - 1) / kAppend8Rows;
-    const int64_t attend = (a.decode ? (a.nsplit > 1 ? kDecodeGroups : items) : items * a.nsplit) + a.clear;
+    const int64_t attend = (a.decode ? (a.nsplit > 1 ? a.shares : items) : items * a.nsplit) + a.clear;
     return items <= kMaxGroups && attend <= kMaxGroups && append <= kMaxGroups && (a.N * a.H + 7) / 8 <= kMaxGroups;
 }
 
@@ -360,14 +367,14 @@ int e2ttt_attention_backward(const e2ttt_attention_desc* d, const void* q, const
     return launch_status(e);
 }
 
-static size_t paged_bytes(const e2ttt_paged_desc* d) {
+static size_t paged_bytes(const e2ttt_paged_desc* d, bool bits8) {
     AttnArgs a = make_args(d->a);
-    plan_paged(a, d->a.io_dtype == E2TTT_F32, d->table_width * d->page_size);
+    plan_paged(a, d->a.io_dtype == E2TTT_F32, bits8, d->table_width * d->page_size);
     return split_bytes(a);
 }
 
 size_t e2ttt_paged_workspace_size(const e2ttt_paged_desc* d) {
-    return paged_desc_status(d, false) == E2TTT_OK ? paged_bytes(d) : kBad;
+    return paged_desc_status(d, false) == E2TTT_OK ? paged_bytes(d, false) : kBad;
 }
 
 // bits8: a cache of one-byte elements, with a scale per slot and head.
@@ -385,7 +392,7 @@ static int paged_attention(const e2ttt_paged_desc* d, bool bits8, const void* q,
     if (d->table_width > 0 && !aligned(table, 4)) return E2TTT_ERR_INVALID_ARG;
     const bool f32 = d->a.io_dtype == E2TTT_F32;
     AttnArgs a = make_args(d->a);
-    plan_paged(a, f32, d->table_width * d->page_size);
+    plan_paged(a, f32, bits8, d->table_width * d->page_size);
     if (bits8 && d->pages > 0 && (!k_scale || !v_scale)) return E2TTT_ERR_INVALID_ARG;
     const size_t need = split_bytes(a);
     const int wst = workspace_status(ws, ws_bytes, need);
@@ -446,7 +453,7 @@ int e2ttt_paged_attention(const e2ttt_paged_desc* d, const void* q, const void* 
 }
 
 size_t e2ttt_paged8_workspace_size(const e2ttt_paged_desc* d) {
-    return paged8_desc_status(d, false) == E2TTT_OK ? paged_bytes(d) : kBad;
+    return paged8_desc_status(d, false) == E2TTT_OK ? paged_bytes(d, true) : kBad;
 }
 
 int e2ttt_paged8_attention(const e2ttt_paged_desc* d, const void* q, const void* k, const void* v, void* k_cache,

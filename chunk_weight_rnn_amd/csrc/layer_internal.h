@@ -42,6 +42,7 @@ struct AttnArgs {
     int ntiles;   // row tiles at most, over all sequences
     int nsplit;   // key ranges per row tile; > 1: partial results, joined after
     int decode;   // paged: the kernel for few rows per sequence
+    int shares;   // decode, nsplit > 1: workgroups that the keys are shared out over
     int clear;    // workgroups that write the rows of tokens outside every sequence
     float* po;    // [nsplit][N][H][D] partial outputs
     float* pl;    // [nsplit][N][H] their base-2 log sums
@@ -53,15 +54,17 @@ constexpr int kF32Rows = 16;   // and fp32
 hipError_t launch_attn_fwd_bf16(const AttnArgs& a, hipStream_t s);
 hipError_t launch_attn_fwd_f32(const AttnArgs& a, hipStream_t s);
 // Few new tokens per sequence over a paged cache; nsplit > 1: the keys of all
-// items shared out evenly over kDecodeGroups workgroups, po / pl
-// [2 kDecodeGroups][32][D] / [2 kDecodeGroups][32].  One workgroup per compute
+// items shared out evenly over `shares` workgroups, po / pl [2 shares][32][D] /
+// [2 shares][32].  One workgroup per compute
 // unit: its LDS stages fill one (16 sequences at 2000 keys: 22.0 us, with twice as
 // many half as long 27.5; 64 at 12000 the same).
 constexpr int kDecodeGroups = 256;
 hipError_t launch_attn_decode_bf16(const AttnArgs& a, hipStream_t s);
-hipError_t launch_attn_decode_join(const AttnArgs& a, hipStream_t s);  // of D up to 128 and kDecodeGroups
+hipError_t launch_attn_decode_join(const AttnArgs& a, hipStream_t s);  // of D up to 128
 hipError_t launch_attn_join(const AttnArgs& a, bool f32, hipStream_t s);
-// The same over a cache in 8 bits; the new tokens go into it in a launch before.
+// The same over a cache in 8 bits; the new tokens go into it in a launch before.  Two
+// workgroups per compute unit, whose stages are half as large.
+constexpr int kDecode8Groups = 512;
 constexpr int kAppend8Rows = 16;  // rows of keys and values per workgroup
 hipError_t launch_append8(const AttnArgs& a, hipStream_t s);
 hipError_t launch_attn_decode8(const AttnArgs& a, hipStream_t s);

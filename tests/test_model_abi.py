@@ -239,7 +239,7 @@ def test_paged8_refusals(lib):  # noqa: F811
             assert page8(lib, paged(), p) == ALIAS, (o, i)
     d = paged(W=4096)
     need = lib.e2ttt_paged8_workspace_size(ctypes.byref(d))
-    assert need == lib.e2ttt_paged_workspace_size(ctypes.byref(d)) > 0
+    assert need == 2 * lib.e2ttt_paged_workspace_size(ctypes.byref(d)) > 0  # twice the workgroups share the keys
     assert page8(lib, d, ws=None) == WORKSPACE and page8(lib, d, n=need - 1) == WORKSPACE
     d = paged()
     d.a.tokens = 0
