@@ -237,3 +237,28 @@ def test_second_derivatives_are_refused():
         (g,) = torch.autograd.grad((y * y).sum(), leaf, create_graph=True)
         with pytest.raises(RuntimeError):
             torch.autograd.grad(g.sum(), leaf)
+
+
+def test_recurrences_on_several_streams_at_once():
+    """Tiles wait for tiles of their own call alone, however the calls share the chip."""
+    note("recurrences on four streams")
+    import chunk_weight_rnn_amd as e2
+    g = torch.Generator(device="cuda").manual_seed(7)
+    calls = []
+    for n in (9000, 6000, 4097, 8191):
+        x, d = (torch.randn(n, 1000, generator=g, device="cuda").bfloat16() for _ in range(2))
+        a, cu = torch.rand(n, 1000, generator=g, device="cuda"), _cu([n // 3, n - n // 3])
+        out, state, starts = e2.gated_scan_forward(x, a, cu, save=True)
+        grads = e2.gated_scan_backward(d, x, a, starts, cu)
+        calls.append((x, a, cu, d, (out, state, starts), tuple(grads.values())))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in calls]
+    got = []
+    for _ in range(3):
+        for s, (x, a, cu, d, *_rest) in zip(streams, calls):
+            f = e2.gated_scan_forward(x, a, cu, save=True, stream=s)
+            got.append((f, tuple(e2.gated_scan_backward(d, x, a, f[2], cu, stream=s).values())))
+    torch.cuda.synchronize()
+    for i, (f, b) in enumerate(got):
+        want = calls[i % len(calls)]
+        assert _same(f[:2], want[4][:2]) and _same(b, want[5]), i
