@@ -154,10 +154,10 @@ E2TTT_API int e2ttt_paged8_attention(const e2ttt_paged_desc* desc, const void* q
  *               fp32: the state before token E2TTT_SCAN_TILE j of sequence s, in
  *               row cu_seqlens[s] / E2TTT_SCAN_TILE + s + j; other rows are left alone
  *   workspace   >= e2ttt_scan_workspace_size(desc) bytes, 256-byte aligned;
- *               clobbered (NULL when that is 0)
- * Tensors are aligned to their elements; where width and strides are even and
- * pairs of channels aligned to their size, they are read in pairs.  Outputs must
- * not overlap any other buffer.
+ *               clobbered (NULL when that is 0); calls that overlap in time need
+ *               one each
+ * Tensors are aligned to their elements.  Outputs must not overlap any other
+ * buffer.
  */
 #define E2TTT_SCAN_TILE 128
 typedef struct {
