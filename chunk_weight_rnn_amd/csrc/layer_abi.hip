@@ -241,9 +241,10 @@ ScanArgs scan_plan(const e2ttt_scan_desc& d, bool backward) {
     a.slabs = (int)slabs;
     // A wave per sequence while they have 16 tokens at most on average, or 4 where no
     // sequence can have two tiles, so that there are no words to clear (2048 channels, us so and with a
-    // workgroup per tile: 64 sequences of one token 2.9 and 12.9, of 16 6.6 and 20, 256 of 16
-    // 16 and 64; 8 of 4 3.0 and 4.2, of 16 4.9 and 4.2).  Longer ones gain as well where
-    // all are alike (64 of 48: 14 and 22), but a single long one would be a single wave's.
+    // workgroup per tile: 64 sequences of one token 2.5 and 12.9, of 16 5.9 and 20, 256 of 16
+    // 13 and 64; 8 of 4 2.6 and 4.2, of 16 4.9 and 4.2).  Longer ones gain as well where
+    // all are alike (64 of 48: 14 and 22).  Single long ones among them are taken by whole
+    // workgroups of the same launch.
     a.shorts = !backward && d.tokens <= (d.tokens > E2TTT_SCAN_TILE ? 16 : 4) * d.seqs;
     const int64_t groups = (a.shorts ? d.seqs : d.tokens / E2TTT_SCAN_TILE + d.seqs) * slabs;
     a.groups = (int)(groups < kMaxScanGroups ? groups : kMaxScanGroups + 1);

@@ -134,6 +134,7 @@ struct ScanArgs {
     int slabs;    // of 64 lanes, over the channels
     int groups;   // (tile or sequence, slab) pairs
     int shorts;   // forward: sequences of a few tokens
+    int helpers;  // shorts: workgroups per slab for those that are long all the same
     int clear;    // workgroups that write the rows of tokens outside every sequence
     unsigned long long* words;  // what tiles tell each other, scan_words of them; null where no sequence has two
 };

@@ -268,36 +268,111 @@ __global__ __launch_bounds__(64 * NW, 2 * kStay) void scan_fwd_kernel(ScanArgs a
 
 // Sequences of a few tokens: a wave each and slab, no exchange; sixteen tokens' loads
 // together, and fewer where fewer are left (one token each of 64 sequences, 2048 channels:
-// always sixteen 6.3 us, so 3).
+// always sixteen 6.3 us, so 2.5).  The host knows the lengths' sum alone, so that any of
+// them may be long: above kAlone tokens, where a wave's ways to memory one after the other
+// add up, a sequence is left to workgroups of their own, a.helpers per slab, that each look
+// through their share of the sequences and walk through a long one tile by tile, the state
+// in registers (256 sequences of one token and one of 3800: 70 us; as a wave's 580, alone in
+// tiles side by side 21; without a long one the helpers cost 0.2 us at most).
+constexpr int kAlone = 4 * R;
 template <typename TX, typename TA>
-__global__ __launch_bounds__(256) void scan_short_kernel(ScanArgs a) {
+__device__ __forceinline__ void walk(const ScanArgs& a, float2 (*all)[NW][64], int& turn, int seq, int tok0, int n, int c, bool in) {
+    constexpr int K = R * 2 / sizeof(TX);  // tokens of a wave at a time: few enough registers for eight waves side by side
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int past = (int)blockIdx.x - (a.groups + 3) / 4;
+    float h = a.h0 && in ? a.h0[(int64_t)seq * a.C + c] : 0.f;
+    float* st = a.starts ? a.starts + (int64_t)(tok0 / TILE + seq) * a.C + c : nullptr;
+#pragma unroll 1
+    for (int lo = 0; lo < n; lo += K * NW) {
+        const int t = lo + wave * K;
+        const int64_t tok = (int64_t)tok0 + t;
+        TX x[K];
+        TA g[K];
+        int64_t xs = a.x_tok, as = a.a_tok, os = a.C;  // as below
+        asm volatile("" : "+s"(xs), "+s"(as), "+s"(os));
+        load(x, (const TX*)a.x + tok * a.x_tok, xs, n - t, c, in, 0.f);
+        load(g, (const TA*)a.a + tok * a.a_tok, as, n - t, c, in, 1.f);
+        float P = 1.f, H = 0.f;
+#pragma unroll
+        for (int r = 0; r < K; ++r) {
+            H = __builtin_fmaf((float)g[r], H, (float)x[r]);
+            P *= (float)g[r];
+        }
+        float2 (*const sh)[64] = all[turn];  // the other half is still being read
+        turn ^= 1;
+        sh[wave][lane] = make_float2(P, H);
+        asm volatile("" : "+v"(h));  // is here before the barrier: state may be h0
+        __syncthreads();
+        if (st && wave == 0 && in && lo % TILE == 0) st[(int64_t)(lo / TILE) * a.C] = h;
+        float end = h;
+#pragma unroll 2
+        for (int w = 0; w < NW; ++w) {
+            const float2 f = sh[w][lane];
+            if (w == wave) h = end;
+            end = __builtin_fmaf(f.x, end, f.y);
+        }
+        TX* op = (TX*)a.out + tok * a.C;
+#pragma unroll
+        for (int r = 0; r < K; ++r) {
+            h = __builtin_fmaf((float)g[r], h, (float)x[r]);
+            if (in && r < n - t) op[c] = (TX)h;
+            op += os;
+        }
+        h = end;
+    }
+    if (a.state && wave == NW - 1 && in) a.state[(int64_t)seq * a.C + c] = h;
+}
+
+template <typename TX, typename TA>
+__global__ __launch_bounds__(64 * NW, 8) void scan_short_kernel(ScanArgs a) {
+    __shared__ float2 all[2][NW][64];  // (P, H) of the waves
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    int b = (int)blockIdx.x;
+    if (b < a.helpers * a.slabs) {
+        const int c = b % a.slabs * 64 + lane, mine = b / a.slabs;
+        int turn = 0;
+        for (int64_t s0 = mine; s0 < a.S; s0 += 64 * a.helpers) {  // the same for all waves
+            const int64_t seq = s0 + lane * a.helpers;
+            const int tok0 = seq < a.S ? clamped(a.cu[seq], (int)a.N) : 0;
+            const int n = seq < a.S ? clamped(a.cu[seq + 1], (int)a.N) - tok0 : 0;
+            for (u64 longs = __ballot(n > kAlone); longs; longs &= longs - 1) {
+                const int i = __builtin_ctzll(longs);
+                walk<TX, TA>(a, all, turn, (int)s0 + i * a.helpers, __builtin_amdgcn_readlane(tok0, i), __builtin_amdgcn_readlane(n, i), c, c < a.C);
+            }
+        }
+        return;
+    }
+    b -= a.helpers * a.slabs;
+    const int past = b - (a.groups + NW - 1) / NW;
     if (past >= 0) {
         clear_rows(a, (TX*)a.out, past);
         return;
     }
-    const int unit = (int)blockIdx.x * 4 + wave;
+    const int unit = b * NW + wave;
     if (unit >= a.groups) return;
     const int c = unit % a.slabs * 64 + lane;
     const bool in = c < a.C;
     const int seq = unit / a.slabs, tok0 = clamped(a.cu[seq], (int)a.N), n = clamped(a.cu[seq + 1], (int)a.N) - tok0;
+    if (n > kAlone) return;
     float h = a.h0 && in ? a.h0[(int64_t)seq * a.C + c] : 0.f;
     const TX* xp = (const TX*)a.x + tok0 * a.x_tok;
     const TA* ap = (const TA*)a.a + tok0 * a.a_tok;
     TX* op = (TX*)a.out + (int64_t)tok0 * a.C;
-    float* st = a.starts ? a.starts + (tok0 / TILE + seq) * a.C + c : nullptr;
+    if (a.starts && n > 0 && in) a.starts[(int64_t)(tok0 / TILE + seq) * a.C + c] = h;
     auto step = [&](int t, auto count) {
         constexpr int K = decltype(count)::value;
         TX x[K];
         TA g[K];
-        load(x, xp + t * a.x_tok, a.x_tok, n - t, c, in, 0.f);
-        load(g, ap + t * a.a_tok, a.a_tok, n - t, c, in, 1.f);
-        if (st && t % TILE == 0 && in) st[(int64_t)(t / TILE) * a.C] = h;
+        // else the compiler keeps a multiple of the strides for every row over the loop, in more
+        // scalars than there are (256 sequences of 16 tokens: 15.9 us, so 13.0)
+        int64_t xs = a.x_tok, as = a.a_tok, os = a.C;
+        asm volatile("" : "+s"(xs), "+s"(as), "+s"(os));
+        load(x, xp + t * a.x_tok, xs, n - t, c, in, 0.f);
+        load(g, ap + t * a.a_tok, as, n - t, c, in, 1.f);
+        TX* o = op + t * a.C;
 #pragma unroll
-        for (int r = 0; r < K; ++r) {
+        for (int r = 0; r < K; ++r, o += os) {
             h = __builtin_fmaf((float)g[r], h, (float)x[r]);
-            if (in && r < n - t) op[(int64_t)(t + r) * a.C + c] = (TX)h;
+            if (in && r < n - t) o[c] = (TX)h;
         }
     };
     int t = 0;
@@ -393,7 +468,10 @@ template <typename TX, typename TA>
 hipError_t forward(ScanArgs a, hipStream_t s) {
     const dim3 bl(64 * NW);
     if (a.shorts) {
-        scan_short_kernel<TX, TA><<<dim3((unsigned)((a.groups + 3) / 4 + a.clear)), dim3(256), 0, s>>>(a);
+        // as many as there may be long sequences, and up to 512 workgroups
+        const int64_t most = a.N / (kAlone + 1), fit = a.slabs < 512 ? 512 / a.slabs : 1;
+        a.helpers = (int)(most < fit ? most : fit);
+        scan_short_kernel<TX, TA><<<dim3((unsigned)(a.helpers * a.slabs + (a.groups + NW - 1) / NW + a.clear)), bl, 0, s>>>(a);
     } else if (a.words) {
         int cus = 0;
         hipError_t e = device_cu_count(&cus);
