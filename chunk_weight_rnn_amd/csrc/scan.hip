@@ -24,9 +24,9 @@
 // Workgroups take their tiles by a ticket, in the order of the sequences, so a tile
 // waits only for tiles that were taken before it, by workgroups that run already and
 // finish theirs in the order they took them, and words only grow, whatever the offsets
-// hold: every wait ends.  (One that does not,
-// because another call was given the same workspace meanwhile, is given up after
-// kSpinTicks, and its results are NaN.)  What is published is a word of 64 bits, stored
+// hold: every wait ends.  (One that does not, because another call was given the same
+// workspace meanwhile, is given up after seconds of looking, scan_wait.h, and its results
+// are NaN.)  What is published is a word of 64 bits, stored
 // and loaded as a whole past the caches of the compute dies, so nothing has to be flushed.
 //
 // The gradient goes the same way from the last tile to the first.  It needs
@@ -36,6 +36,7 @@
 #include <type_traits>
 
 #include "attn_common.h"
+#include "scan_wait.h"
 
 namespace e2ttt {
 namespace {
@@ -128,8 +129,6 @@ __device__ __forceinline__ int take_ticket(const ScanArgs& a, int slab) {
     return (int)__hip_atomic_fetch_add((unsigned*)(a.words + 8 * (slab + 1)), 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
-constexpr u64 kSpinTicks = 200000000;  // 2 s of the 100 MHz wall clock
-
 // The state h that enters the tile from the `before` tiles in direction -dir, the
 // words of the nearest at `row`: each wave waits for its share of the kLook nearest,
 // the farthest of which has to be a state, and all are folded in order.  Words that are
@@ -158,7 +157,7 @@ __device__ __forceinline__ void enter(const ScanArgs& a, float& h, u64 (*sh)[64]
             if (tries % 64 == 0) {
                 const u64 now = wall_clock64();
                 if (since == 0) since = now;
-                if (now - since > kSpinTicks || published(a.words) != 0) {
+                if (gives_up(tries, now - since) || published(a.words) != 0) {
                     publish(a.words, 1);
                     w[j] = word_of(__builtin_nanf(""), kState);
                     break;

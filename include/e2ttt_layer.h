@@ -155,7 +155,9 @@ E2TTT_API int e2ttt_paged8_attention(const e2ttt_paged_desc* desc, const void* q
  *               row cu_seqlens[s] / E2TTT_SCAN_TILE + s + j; other rows are left alone
  *   workspace   >= e2ttt_scan_workspace_size(desc) bytes, 256-byte aligned;
  *               clobbered (NULL when that is 0); calls that overlap in time need
- *               one each
+ *               one each: with a workspace that another call overwrites meanwhile the
+ *               results are not defined, and are NaN, without an error, where a part of
+ *               the call has waited in vain for what the workspace should have told it
  * Tensors are aligned to their elements.  Outputs must not overlap any other
  * buffer.
  */
