@@ -37,7 +37,7 @@ from . import _lib
 from ._lib import (E2TTTError, FLAG_CHUNK_AVG, FLAG_FORCE_GENERIC, FLAG_NO_MOMENTUM, FLAG_PRECISE, FLAG_SAVE_STATES,
                    make_desc)
 
-from .layer import (attention, attention_backward, attention_forward, gated_scan, gated_scan_backward,
+from .layer import (_mark_leaves, attention, attention_backward, attention_forward, gated_scan, gated_scan_backward,
                     gated_scan_forward, norm_backward, norm_forward, paged_attention, rms_norm)
 from .tokens import embedding, embedding_backward, embedding_forward, sample
 
@@ -327,5 +327,8 @@ def chunk_update(q, k, v, eta, alpha, beta, W0, M0, *, chunk: int, kind: str = "
         dummy = torch.zeros((), device=q.device)  # keeps the argument list tensor-typed
         out, W, _ = _ChunkUpdate.apply(q, k, v, eta, alpha, dummy, W0, dummy, chunk, kind, loss, Hd, False,
                                        chunk_avg)
+        _mark_leaves(out, q.get_device())
         return out, W, None
-    return _ChunkUpdate.apply(q, k, v, eta, alpha, beta, W0, M0, chunk, kind, loss, Hd, True, chunk_avg)
+    r = _ChunkUpdate.apply(q, k, v, eta, alpha, beta, W0, M0, chunk, kind, loss, Hd, True, chunk_avg)
+    _mark_leaves(r[0], q.get_device())
+    return r

@@ -59,20 +59,52 @@ def _call(fn: str, dev: int, *args):
         raise E2TTTError(fn, st)
 
 
+def _leaves(nodes):
+    """Those that stand for leaves: one node per leaf, as long as a graph holds it."""
+    return [node for node in nodes if node is not None and node.name() == "torch::autograd::AccumulateGrad"]
+
+
+def _before(node):
+    return [n for n, _ in node.next_functions]
+
+
+def _mark_leaves(out, dev: int):
+    """Notes at each leaf that the call behind ``out`` was given the stream of the first such
+    call in a graph that is still alive."""
+    if out.grad_fn is not None:
+        stream = torch._C._cuda_getCurrentRawStream(dev)
+        for leaf in _leaves(_before(out.grad_fn)):
+            leaf.metadata.setdefault("e2ttt_stream", stream)
+
+
+def _refuse_other_streams(leaves, dev: int):
+    stream = torch._C._cuda_getCurrentRawStream(dev)
+    if any(leaf.metadata.get("e2ttt_stream", stream) != stream for leaf in leaves):
+        raise RuntimeError("a leaf of this capture is in an autograd graph of another stream: "
+                           "drop that graph's outputs first")
+
+
 def _one_stream(out, dev: int):
     """Refuses a capture with gradients for leaves that an eager graph, still alive, used on
     another stream: the backward pass ends by making that stream wait, which a capture does
-    not survive (the process ends in it)."""
-    node = out.grad_fn
-    if node is None:
+    not survive (the process ends in it).  The leaves that the call behind ``out`` was given."""
+    _mark_leaves(out, dev)
+    if out.grad_fn is not None and torch.cuda.is_current_stream_capturing():
+        _refuse_other_streams(_leaves(_before(out.grad_fn)), dev)
+
+
+def _one_stream_behind(out, dev: int):
+    """``_one_stream`` for all leaves behind ``out``; the streams are known of those that a call
+    of this package was given directly."""
+    _one_stream(out, dev)
+    if out.grad_fn is None or not torch.cuda.is_current_stream_capturing():
         return
-    stream, capturing = torch._C._cuda_getCurrentRawStream(dev), torch.cuda.is_current_stream_capturing()
-    for leaf, _ in node.next_functions:
-        # one such node per leaf, as long as a graph holds it
-        if leaf is not None and leaf.name() == "torch::autograd::AccumulateGrad":
-            if leaf.metadata.setdefault("e2ttt_stream", stream) != stream and capturing:
-                raise RuntimeError("a leaf of this capture is in an autograd graph of another stream: "
-                                   "drop that graph's outputs first")
+    todo, seen = [out.grad_fn], {out.grad_fn}
+    while todo:
+        new = {node for node in _before(todo.pop()) if node is not None} - seen
+        seen |= new
+        todo += new
+    _refuse_other_streams(_leaves(seen), dev)
 
 
 def _p(t):
@@ -296,7 +328,9 @@ class _Attention(torch.autograd.Function):
 def attention(q, k, v, cu_seqlens, *, window: int = 0, scale: float | None = None):
     """``attention_forward`` as a differentiable op: returns out, with gradients
     for q, k and v from ``attention_backward``."""
-    return _Attention.apply(q, k, v, cu_seqlens, window, scale)
+    out = _Attention.apply(q, k, v, cu_seqlens, window, scale)
+    _mark_leaves(out, q.get_device())
+    return out
 
 
 def paged_attention(q, k, v, k_cache, v_cache, table, cu_seqlens, cached, *, window: int = 0,
@@ -438,9 +472,10 @@ class _GatedScan(torch.autograd.Function):
 def gated_scan(x, a, cu_seqlens, h0=None):
     """``gated_scan_forward`` as a differentiable op: returns (out, state), with
     gradients for x, a and h0 from ``gated_scan_backward``.  Captured into a graph with its
-    backward pass, no eager graph of the same leaves may be alive (RuntimeError)."""
+    backward pass, no eager graph of the same leaves may be alive (RuntimeError, where one of
+    the leaves was given to a call of this package directly)."""
     out, state = _GatedScan.apply(x, a, h0, cu_seqlens)
-    _one_stream(out, x.get_device())
+    _one_stream_behind(out, x.get_device())
     return out, state
 
 
@@ -527,6 +562,6 @@ class _Norm(torch.autograd.Function):
 def rms_norm(x, weight, residual=None, *, eps: float = 1e-6):
     """``norm_forward`` as a differentiable op: returns (y, h), h = x + residual
     (x itself without ``residual``), with gradients for x, weight and residual."""
-    if residual is None:
-        return _Norm.apply(x, None, weight, eps)[0], x
-    return _Norm.apply(x, residual, weight, eps)
+    y, h = (_Norm.apply(x, None, weight, eps)[0], x) if residual is None else _Norm.apply(x, residual, weight, eps)
+    _mark_leaves(y, x.get_device())
+    return y, h

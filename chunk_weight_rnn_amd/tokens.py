@@ -12,7 +12,7 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from ._lib import EmbeddingDesc, SampleDesc
-from .layer import _IO, _call, _device, _full, _layout, _on, _one_stream, _p, _size, _workspace
+from .layer import _IO, _call, _device, _full, _layout, _on, _one_stream_behind, _p, _size, _workspace
 
 _TOKEN_BYTES = {torch.int32: 4, torch.int64: 8}
 
@@ -96,9 +96,10 @@ class _Embedding(torch.autograd.Function):
 def embedding(tokens, weight, *, scale: float = 1.0, dtype=None):
     """``embedding_forward`` as a differentiable op, with the weight's gradient
     (dense, in the weight's type) from ``embedding_backward``.  Captured into a graph
-    with its backward pass, no eager graph of the same weight may be alive (RuntimeError)."""
+    with its backward pass, no eager graph of the same leaves may be alive (RuntimeError, where
+    one of the leaves was given to a call of this package directly)."""
     out = _Embedding.apply(tokens, weight, scale, dtype)
-    _one_stream(out, tokens.get_device())
+    _one_stream_behind(out, tokens.get_device())
     return out
 
 
