@@ -112,6 +112,7 @@ def _sample_plan(logits, temperature, top_k, top_p, min_p):
         raise TypeError(f"expected float32 or bfloat16, got {dtype}")
     if shape[1] > 1 and stride[1] != 1:
         raise ValueError("logits' last dimension must be contiguous")
+    top_k = max(0, min(top_k, 0x7fffffff))  # ctypes would take a larger number's low 32 bits
     d = SampleDesc(_IO[dtype], top_k, temperature, top_p, min_p, 0, shape[0], shape[1], stride[0])
     return shape[0], ctypes.byref(d), _size("e2ttt_sample_workspace_size", d), d
 
