@@ -169,6 +169,8 @@ def _attention_desc(q, k, v, cu, window, scale, kv_heads):
         raise ValueError("cu_seqlens must be a contiguous int32 tensor of shape (sequences + 1,)")
     if scale is None:
         scale = D ** -0.5 if D else 1.0
+    # ctypes would take a larger number's low 32 bits; one as long as any sequence leaves none out
+    window = max(-1, min(window, 0x7fffffff))
     return AttentionDesc(_IO[dtype], window, N, cu[0][0] - 1, H, kv_heads, D, scale, 0, stride[0], stride[1],
                          ks[0], ks[1], vs[0], vs[1])
 
