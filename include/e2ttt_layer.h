@@ -127,6 +127,9 @@ E2TTT_API int e2ttt_paged_attention(const e2ttt_paged_desc* desc, const void* q,
  * such scale with max|x| <= 448 scale (1 for zeros), and x / scale rounded to
  * nearest even; one that holds a NaN or an Inf becomes NaN as a whole.  Queries
  * see keys and values as the cache holds them, the new ones among them.
+ * Probabilities are rounded to bf16 as operands, as over a cache of bf16; a
+ * value's scale goes into its probability, which loses bits, as the smallest
+ * numbers of bf16 do, where the values are all below some 2^-110.
  * io_dtype is bf16, in which an 8-bit value times its scale is exact, and D a
  * multiple of 16 (else E2TTT_ERR_UNSUPPORTED).  The cache's strides count
  * elements of one byte, in multiples of 16.  Everything else as above.
@@ -159,7 +162,9 @@ E2TTT_API int e2ttt_paged8_attention(const e2ttt_paged_desc* desc, const void* q
  *               results are not defined, and are NaN, without an error, where a part of
  *               the call has waited in vain for what the workspace should have told it
  * Tensors are aligned to their elements.  Outputs must not overlap any other
- * buffer.
+ * buffer.  tokens up to 2^31 - 4097, seqs below 2^28, width up to 2^24, and
+ * (tokens / E2TTT_SCAN_TILE + seqs) ceil(width / 64) up to 2^22 (else
+ * E2TTT_ERR_UNSUPPORTED; the forward takes more tokens of short sequences).
  */
 #define E2TTT_SCAN_TILE 128
 typedef struct {

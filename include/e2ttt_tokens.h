@@ -20,10 +20,12 @@ extern "C" {
 #endif
 
 /*
- * Token lookup: out[n] = scale table[tokens[n]], rounded once; and its
- * gradient, a dense tensor: dtable[v] = scale times the sum, in 32 bits and in
- * the order of n, of dout[n] over the n with tokens[n] = v, 0 for a v that no
- * token names.
+ * Token lookup: out[n] = scale table[tokens[n]], a product in 32 bits rounded to
+ * io_dtype; and its gradient, a dense tensor: dtable[v] = scale times the sum, in
+ * 32 bits, of dout[n] over the n with tokens[n] = v, 0 for a v that no token
+ * names.  Up to 16 of them are added up in the order of n; more are cut into
+ * pieces, at the multiples of 16 of all places in the order of their tokens,
+ * whose sums are then added up, in an order that the tokens alone determine.
  *   tokens  [tokens] int32 or int64; one outside [0, vocab) reads a row of
  *           zeros and has no part in the gradient
  *   table, dtable  [vocab][width] table_dtype contiguous
@@ -54,7 +56,12 @@ E2TTT_API int e2ttt_embedding_backward(const e2ttt_embedding_desc* desc, const v
  * With temperature T > 0 and x the row's largest logit, token i has the weight
  *   w_i = 2^-44 round(2^44 exp((logit_i - x) / T)),
  * a whole number of 2^-44, so that sums of weights are exact (a token of less
- * than 2^-45 of the largest one's probability is never chosen).  The tokens are
+ * than 2^-45 of the largest one's probability is never chosen).  There are two
+ * exceptions: without any filter, and with top_p but no top_k on rows of more than
+ * 8192, the row's sum is one of weights before they are rounded, in 64-bit floats.
+ * It is off by 2^-45 of the largest weight per logit at most, so that the token may
+ * be a neighbour, or top_p keep one more or less, where u or top_p is within 2^-27
+ * of a border.  (Rows of equal logits are exact all the same.)  The tokens are
  * put in order of falling logit, equal ones by index, and kept are
  *   1. the first top_k of them (0 or less: all);
  *   2. of those, as many as it takes for their weight to reach top_p of that of
