@@ -12,7 +12,9 @@
 //    order.  A workgroup owns a range of tokens and reads all of them twice: once
 //    to count those below its range and, wave by wave, each of its own; then to
 //    put every place where it belongs.  No workgroup waits for another, and the
-//    reads (the tokens alone, from the L2 cache) are little beside the rows.
+//    reads (the tokens alone, from the L2 cache) are little beside the rows, though they
+//    grow with tokens times workgroups (rows of 64, in all: 30 us from 16384 tokens, 138 from
+//    131072; of 2048, 97 and 391).
 // 2. A wave per row of the table and 1024 columns sums its places' rows from registers
 //    and writes the row.  Rows with more than kEmbedPiece places (a text's commonest
 //    words) are left to waves that own a piece of the sorted places each: a wave's

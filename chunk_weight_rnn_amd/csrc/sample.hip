@@ -35,7 +35,8 @@
 // every logit where its weight is needed, and the histogram (64 additions in the LDS
 // take some 25 cycles, and 6 each where they are to one address: so threads that agree
 // add once); of a few rows the chain of barriers.  One row of 32000 in bf16 with all
-// filters 17 us, 64 of them with top_p 45, 256 rows of 128257 in fp32 100 (1.3 TB/s).
+// filters 17 us, 64 of them with top_p 50, 256 rows of 128257 in fp32 101 (1.3 TB/s); of
+// equal logits, the slow way, 86 and 280.
 #include "tokens_internal.h"
 
 namespace e2ttt {

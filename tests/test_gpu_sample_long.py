@@ -128,3 +128,14 @@ def test_settings_of_each_long_row(dtype):
     col = lambda k, off, d=torch.float32: torch.tensor([FILTERS[n].get(k, off) for n in names], device="cuda", dtype=d)
     compare(x, u, dict(temperature=col("temperature", 1.0), top_k=col("top_k", 0, torch.int32), top_p=col("top_p", 1.0),
                        min_p=col("min_p", 0.0)), f"settings of each row {dtype}")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("V", [300, 9001])
+def test_temperatures_of_each_row_at_the_ends(V, dtype):
+    """Infinite (every finite logit alike), and so small that 1 / T overflows."""
+    x, u = logits_of("plain", 8, V, dtype, seed=V)
+    x[:, ::5] = -float("inf")
+    t = torch.tensor([float("inf"), 1e-45, 3e38, 1e-30] * 2, device="cuda")
+    for name in ("none", "k20", "k1001", "p", "m", "k5000_p"):
+        compare(x, u, dict(FILTERS[name], temperature=t), f"temperatures at the ends {name} {dtype} V={V}")
