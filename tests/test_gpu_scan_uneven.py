@@ -45,6 +45,13 @@ def test_widths(C):
     check([1] * 30 + [150, 3, 200] + [1] * 30, C, "bf16", "f32")
 
 
+@pytest.mark.parametrize("C,lens", [(16400, [1] * 66 + [100] + [2] * 5 + [80] + [1] * 70), (2000, [1] * 1200 + [300, 0, 70] + [1] * 200 + [150])])
+def test_more_sequences_than_one_look(C, lens):
+    """The workgroups for long ones look at 64 sequences each at a time: one of them per 64
+    channels of many, sixteen of 2000."""
+    check(lens, C, "bf16", "bf16", low=0.5)
+
+
 @pytest.mark.parametrize("before,after", [(0, 40), (17, 0), (130, 300)])
 def test_tokens_outside_every_sequence(before, after, monkeypatch):
     real = torch.empty
